@@ -31,6 +31,9 @@ EXPORTS = (
     "omni_routed_backward", "omni_shared_mlp_workspace", "omni_shared_mlp",
     "omni_atomic_forward_glu", "omni_flat_router_workspace", "omni_flat_router_topk",
     "omni_product_topk_static",
+    "omni_expert_matmul", "omni_expert_weight_grad", "omni_expert_combine",
+    "omni_expert_combine_backward", "omni_quantize_rows", "omni_quantized_matmul",
+    "omni_quantized_expert_matmul",
 )
 
 
@@ -73,6 +76,13 @@ _SIGS = {
     "omni_flat_router_topk": (_i, [_i, _i, _i, _i, _i] + [_vp] * 8 + [_sz, _vp]),
     "omni_atomic_forward_glu": (_i, [_i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp,
                                      ctypes.POINTER(ScheduleStruct), _vp, _i, _vp, _sz, _vp]),
+    "omni_expert_matmul": (_i, [_i] * 7 + [_vp] * 4 + [_i, _i] + [_vp] * 3),
+    "omni_expert_weight_grad": (_i, [_i] * 7 + [_vp] * 7),
+    "omni_expert_combine": (_i, [_i] * 4 + [_vp] * 3 + [_i, _vp]),
+    "omni_expert_combine_backward": (_i, [_i] * 4 + [_vp] * 6),
+    "omni_quantize_rows": (_i, [_i] * 3 + [_vp] * 4),
+    "omni_quantized_matmul": (_i, [_i] * 4 + [_vp] * 4 + [_i, _vp, _vp]),
+    "omni_quantized_expert_matmul": (_i, [_i] * 7 + [_vp] * 6 + [_i] + [_vp] * 3),
     "omni_shared_mlp": (_i, [_i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
 }
 
@@ -479,3 +489,188 @@ def routed_backward(x, wr_t, wc_t, w, v, expert_idx, gate, dy, out=None, workspa
         _ptr(r["dv"]), _ptr(r["dgate"]), _ptr(ws), nws, _stream(stream)))
     r["workspace"] = ws
     return r
+
+
+def _same_device(*tensors):
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+
+
+def _tasks(rows, offsets, x_row, other_row, other_name):
+    """The number of tasks: the row lists' length, else the rows there are."""
+    _req(offsets, "offsets", torch.int32)
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be [E + 1]")
+    M = rows
+    for t in (x_row, other_row):
+        if t is not None:
+            M = t.numel()
+    for name, t in (("x_row", x_row), (other_name, other_row)):
+        if t is not None:
+            _req(t, name, torch.int32, (M,))
+    if x_row is None and rows < M:
+        raise ValueError(f"{other_name} lists {M} tasks, x has {rows} rows")
+    return M
+
+
+def expert_matmul(x, w, offsets, x_row=None, out=None, out_row=None, transpose=False,
+                  swiglu=False, stream=None):
+    """omni_expert_matmul: out [., n] = x[x_row] W[e]^T over tasks sorted by expert
+    (w [E, n, k], offsets [E + 1] int32), or, with transpose, x[x_row] W[e]
+    (the input gradient; x [., n], out [., k]).  swiglu: w [E, 2n, k], out [., n]
+    = silu(gate half) * up half.  x_row / out_row: int32 row lists or None.
+    A fresh out has a row per task (unwritten where no expert has the task)."""
+    E = w.shape[0]
+    if w.dim() != 3 or (swiglu and w.shape[1] % 2):
+        raise ValueError("w must be [E, n, k] ([E, 2n, k] with swiglu)")
+    n, k = w.shape[1] // (2 if swiglu else 1), w.shape[2]
+    inner, width = (n, k) if transpose else (k, n)
+    _req(x, "x", shape=(x.shape[0], inner))
+    _req(w, "w", x.dtype)
+    M = _tasks(x.shape[0], offsets, x_row, out_row, "out_row")
+    _req(offsets, "offsets", torch.int32, (E + 1,))
+    if out is None:
+        out = torch.empty((M, width), dtype=x.dtype, device=x.device)
+    _req(out, "out", x.dtype, (out.shape[0], width))
+    _same_device(x, w, offsets, x_row, out, out_row)
+    with torch.cuda.device(x.device):
+        _check("omni_expert_matmul", lib().omni_expert_matmul(
+            _dtype_code(x), M, E, n, k, x.shape[0], out.shape[0], _ptr(x), _ptr(x_row), _ptr(w),
+            _ptr(offsets), int(bool(transpose)), int(bool(swiglu)), _ptr(out), _ptr(out_row),
+            _stream(stream)))
+    return out
+
+
+def expert_weight_grad(x, dy, offsets, x_row=None, dy_row=None, dw=None, stream=None):
+    """omni_expert_weight_grad: dw [E, n, k] float32, dw[e] = sum over expert e's tasks
+    of dy[dy_row]^T x[x_row] (x [., k], dy [., n]; zero for experts without tasks)."""
+    E, k, n = offsets.numel() - 1, x.shape[1], dy.shape[1]
+    _req(x, "x")
+    _req(dy, "dy", x.dtype)
+    M = _tasks(x.shape[0], offsets, x_row, dy_row, "dy_row")
+    if dy_row is None and dy.shape[0] < M:
+        raise ValueError(f"{M} tasks, dy has {dy.shape[0]} rows")
+    if dw is None:
+        dw = torch.empty((E, n, k), dtype=torch.float32, device=x.device)
+    _req(dw, "dw", torch.float32, (E, n, k))
+    _same_device(x, dy, offsets, x_row, dy_row, dw)
+    with torch.cuda.device(x.device):
+        _check("omni_expert_weight_grad", lib().omni_expert_weight_grad(
+            _dtype_code(x), M, E, n, k, x.shape[0], dy.shape[0], _ptr(x), _ptr(x_row), _ptr(dy),
+            _ptr(dy_row), _ptr(offsets), _ptr(dw), _stream(stream)))
+    return dw
+
+
+def expert_combine(o, K, gate=None, y=None, accumulate=False, stream=None):
+    """omni_expert_combine: y [L, n] float32 = (or +=) sum_k gate[t, k] o[t K + k]
+    for o [L*K, n] in flatten order; gate [L, K] float32, None for ones."""
+    if K < 1 or o.shape[0] % K:
+        raise ValueError(f"o has {o.shape[0]} rows, not a multiple of K={K}")
+    L, n = o.shape[0] // K, o.shape[1]
+    _req(o, "o")
+    if gate is not None:
+        _req(gate, "gate", torch.float32, (L, K))
+    if y is None:
+        if accumulate:
+            raise ValueError("accumulate needs y")
+        y = torch.empty((L, n), dtype=torch.float32, device=o.device)
+    _req(y, "y", torch.float32, (L, n))
+    _same_device(o, gate, y)
+    with torch.cuda.device(o.device):
+        _check("omni_expert_combine", lib().omni_expert_combine(
+            _dtype_code(o), L, K, n, _ptr(o), _ptr(gate), _ptr(y), int(bool(accumulate)),
+            _stream(stream)))
+    return y
+
+
+def expert_combine_backward(o, gate, dy, do=None, dgate=None, stream=None):
+    """omni_expert_combine_backward: returns (do [L*K, n] of o's type, dgate [L, K]
+    float32) for dy [L, n] float32."""
+    L, K = gate.shape
+    n = dy.shape[1]
+    _req(o, "o", shape=(L * K, n))
+    _req(gate, "gate", torch.float32)
+    _req(dy, "dy", torch.float32, (L, n))
+    if do is None:
+        do = torch.empty_like(o)
+    if dgate is None:
+        dgate = torch.empty_like(gate)
+    _req(do, "do", o.dtype, (L * K, n))
+    _req(dgate, "dgate", torch.float32, (L, K))
+    _same_device(o, gate, dy, do, dgate)
+    with torch.cuda.device(o.device):
+        _check("omni_expert_combine_backward", lib().omni_expert_combine_backward(
+            _dtype_code(o), L, K, n, _ptr(o), _ptr(gate), _ptr(dy), _ptr(do), _ptr(dgate),
+            _stream(stream)))
+    return do, dgate
+
+
+def quantize_rows(x, q=None, scale=None, stream=None):
+    """omni_quantize_rows: (q [R, k] int8, scale [R] float32), scale = max|row| / 127,
+    q = row / scale to the nearest integer.  Tokens' activations, or weights by
+    output channel (view [E, n, k] experts as [E*n, k])."""
+    R, k = x.shape
+    _req(x, "x")
+    if q is None:
+        q = torch.empty((R, k), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty(R, dtype=torch.float32, device=x.device)
+    _req(q, "q", torch.int8, (R, k))
+    _req(scale, "scale", torch.float32, (R,))
+    _same_device(x, q, scale)
+    with torch.cuda.device(x.device):
+        _check("omni_quantize_rows", lib().omni_quantize_rows(
+            _dtype_code(x), R, k, _ptr(x), _ptr(q), _ptr(scale), _stream(stream)))
+    return q, scale
+
+
+def quantized_matmul(xq, x_scale, wq, w_scale, out=None, out_dtype=torch.bfloat16, swiglu=False,
+                     stream=None):
+    """omni_quantized_matmul: out [M, n] = (xq wq^T) * x_scale[m] * w_scale[j] for int8
+    xq [M, k], wq [n, k] (swiglu: [2n, k], out = silu(gate half) * up half)."""
+    M, k = xq.shape
+    rows = wq.shape[0]
+    if swiglu and rows % 2:
+        raise ValueError("swiglu needs an even number of weight rows")
+    n = rows // (2 if swiglu else 1)
+    _req(xq, "xq", torch.int8)
+    _req(wq, "wq", torch.int8, (rows, k))
+    _req(x_scale, "x_scale", torch.float32, (M,))
+    _req(w_scale, "w_scale", torch.float32, (rows,))
+    if out is None:
+        out = torch.empty((M, n), dtype=out_dtype, device=xq.device)
+    _req(out, "out", shape=(M, n))
+    _same_device(xq, x_scale, wq, w_scale, out)
+    with torch.cuda.device(xq.device):
+        _check("omni_quantized_matmul", lib().omni_quantized_matmul(
+            _dtype_code(out), M, n, k, _ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale),
+            int(bool(swiglu)), _ptr(out), _stream(stream)))
+    return out
+
+
+def quantized_expert_matmul(xq, x_scale, wq, w_scale, offsets, x_row=None, out=None,
+                            out_row=None, out_dtype=torch.bfloat16, swiglu=False, stream=None):
+    """omni_quantized_expert_matmul: expert_matmul over int8 rows xq [., k] with
+    x_scale [.] and experts wq [E, n, k] with w_scale [E, n]."""
+    if wq.dim() != 3 or (swiglu and wq.shape[1] % 2):
+        raise ValueError("wq must be [E, n, k] ([E, 2n, k] with swiglu)")
+    E, rows, k = wq.shape
+    n = rows // (2 if swiglu else 1)
+    R = xq.shape[0]
+    _req(xq, "xq", torch.int8, (R, k))
+    _req(wq, "wq", torch.int8)
+    _req(x_scale, "x_scale", torch.float32, (R,))
+    _req(w_scale, "w_scale", torch.float32, (E, rows))
+    M = _tasks(R, offsets, x_row, out_row, "out_row")
+    _req(offsets, "offsets", torch.int32, (E + 1,))
+    if out is None:
+        out = torch.empty((M, n), dtype=out_dtype, device=xq.device)
+    _req(out, "out", shape=(out.shape[0], n))
+    _same_device(xq, x_scale, wq, w_scale, offsets, x_row, out, out_row)
+    with torch.cuda.device(xq.device):
+        _check("omni_quantized_expert_matmul", lib().omni_quantized_expert_matmul(
+            _dtype_code(out), M, E, n, k, R, out.shape[0], _ptr(xq), _ptr(x_scale), _ptr(x_row),
+            _ptr(wq), _ptr(w_scale), _ptr(offsets), int(bool(swiglu)), _ptr(out),
+            _ptr(out_row), _stream(stream)))
+    return out

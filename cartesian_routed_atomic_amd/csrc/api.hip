@@ -412,4 +412,140 @@ omni_status omni_shared_mlp(omni_dtype dt, int L, int d, int d_ff, const void* x
                                          stream));
 }
 
+// Work-items of a launch dimension are counted in 32 bits.
+static bool grid_fits(long long blocks, int threads) {
+  return blocks >= 0 && blocks < (1ll << 32) / threads;
+}
+
+static omni_status expert_product(omni::ExpertMatmulArgs& a, int k_unit, int n_unit,
+                                  omni_activation act, hipStream_t stream) {
+  if (a.M < 0 || a.E < 1 || a.n < 1 || a.k < 1 || a.R < 0 || a.Ro < 0) return OMNI_ERR_INVALID_ARG;
+  if (act != OMNI_ACT_NONE && act != OMNI_ACT_SWIGLU) return OMNI_ERR_INVALID_ARG;
+  if (act == OMNI_ACT_SWIGLU && a.transpose) return OMNI_ERR_INVALID_ARG;
+  a.swiglu = act == OMNI_ACT_SWIGLU;
+  if (!a.w || (a.type == omni::kRowsI8 && !a.w_scale)) return OMNI_ERR_INVALID_ARG;
+  if (a.M > 0 && (!a.x || !a.out || (a.type == omni::kRowsI8 && !a.x_scale)))
+    return OMNI_ERR_INVALID_ARG;
+  // without a row list task m is row m
+  if ((!a.x_row && a.R < a.M) || (!a.out_row && a.Ro < a.M)) return OMNI_ERR_INVALID_ARG;
+  if (!aligned16(a.w) || (a.M > 0 && (!aligned16(a.x) || !aligned16(a.out))))
+    return OMNI_ERR_INVALID_ARG;
+  if (a.k % k_unit != 0 || (a.transpose && a.n % n_unit != 0)) return OMNI_ERR_UNSUPPORTED;
+  if (a.type == omni::kRowsI8 && a.k > 131071) return OMNI_ERR_UNSUPPORTED;
+  if (!omni::expert_matmul_grid_fits(a)) return OMNI_ERR_UNSUPPORTED;
+  if (a.M == 0) return OMNI_OK;
+  return hip_status(omni::launch_expert_matmul(a, stream));
+}
+
+omni_status omni_expert_matmul(omni_dtype dt, int M, int E, int n, int k, int R, int Ro,
+                               const void* x, const int32_t* x_row, const void* w,
+                               const int32_t* offsets, int transpose, omni_activation act,
+                               void* out, const int32_t* out_row, hipStream_t stream) {
+  if (dt != OMNI_F32 && dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
+  if (!offsets) return OMNI_ERR_INVALID_ARG;
+  omni::ExpertMatmulArgs a = {};
+  a.type = dt == OMNI_BF16 ? omni::kRowsBf16 : omni::kRowsF32;
+  a.out_bf16 = dt == OMNI_BF16;
+  a.M = M; a.E = E; a.n = n; a.k = k; a.R = R; a.Ro = Ro;
+  a.transpose = transpose != 0;
+  a.x = x; a.x_row = x_row; a.w = w; a.offsets = offsets; a.out = out; a.out_row = out_row;
+  const int unit = dt == OMNI_BF16 ? 8 : 4;
+  return expert_product(a, unit, unit, act, stream);
+}
+
+omni_status omni_expert_weight_grad(omni_dtype dt, int M, int E, int n, int k, int R, int Ry,
+                                    const void* x, const int32_t* x_row, const void* dy,
+                                    const int32_t* dy_row, const int32_t* offsets, float* dw,
+                                    hipStream_t stream) {
+  if (dt != OMNI_F32 && dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
+  if (M < 0 || E < 1 || n < 1 || k < 1 || R < 0 || Ry < 0) return OMNI_ERR_INVALID_ARG;
+  if (!offsets || !dw || !aligned16(dw)) return OMNI_ERR_INVALID_ARG;
+  if (M > 0 && (!x || !dy || !aligned16(x) || !aligned16(dy))) return OMNI_ERR_INVALID_ARG;
+  if ((!x_row && R < M) || (!dy_row && Ry < M)) return OMNI_ERR_INVALID_ARG;
+  const int unit = dt == OMNI_BF16 ? 8 : 4;
+  if (n % unit != 0 || k % unit != 0) return OMNI_ERR_UNSUPPORTED;
+  const omni::ExpertWgradArgs a = {dt == OMNI_BF16, M, E, n, k, R, Ry, x, x_row, dy, dy_row,
+                                   offsets, dw};
+  if (!omni::expert_wgrad_grid_fits(a)) return OMNI_ERR_UNSUPPORTED;
+  return hip_status(omni::launch_expert_wgrad(a, stream));
+}
+
+static omni_status combine_args(omni_dtype dt, int L, int K, int n) {
+  if (dt != OMNI_F32 && dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
+  if (L < 0 || K < 1 || n < 1 || !fits_i32(static_cast<long long>(L) * K))
+    return OMNI_ERR_INVALID_ARG;
+  if (n % (dt == OMNI_BF16 ? 8 : 4) != 0) return OMNI_ERR_UNSUPPORTED;
+  if (!grid_fits((static_cast<long long>(L) * (n / 4) + 255) / 256, 256) ||
+      !grid_fits((static_cast<long long>(L) * K + 3) / 4, 256))
+    return OMNI_ERR_UNSUPPORTED;
+  return OMNI_OK;
+}
+
+omni_status omni_expert_combine(omni_dtype dt, int L, int K, int n, const void* o,
+                                const float* gate, float* y, int accumulate,
+                                hipStream_t stream) {
+  const omni_status st = combine_args(dt, L, K, n);
+  if (st != OMNI_OK) return st;
+  if (L == 0) return OMNI_OK;
+  if (!o || !y || !aligned16(o) || !aligned16(y)) return OMNI_ERR_INVALID_ARG;
+  return hip_status(omni::launch_expert_combine(dt == OMNI_BF16, L, K, n, o, gate, y,
+                                                accumulate != 0, stream));
+}
+
+omni_status omni_expert_combine_backward(omni_dtype dt, int L, int K, int n, const void* o,
+                                         const float* gate, const float* dy, void* dout,
+                                         float* dgate, hipStream_t stream) {
+  const omni_status st = combine_args(dt, L, K, n);
+  if (st != OMNI_OK) return st;
+  if (L == 0) return OMNI_OK;
+  if (!dy || !dout || (dgate && !o)) return OMNI_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(dout) || (dgate && !aligned16(o))) return OMNI_ERR_INVALID_ARG;
+  return hip_status(omni::launch_expert_combine_backward(dt == OMNI_BF16, L, K, n, o, gate, dy,
+                                                         dout, dgate, stream));
+}
+
+omni_status omni_quantize_rows(omni_dtype dt, int R, int k, const void* x, int8_t* q,
+                               float* scale, hipStream_t stream) {
+  if (dt != OMNI_F32 && dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
+  if (R < 0 || k < 1) return OMNI_ERR_INVALID_ARG;
+  if (k % 16 != 0 || !grid_fits(R, 256)) return OMNI_ERR_UNSUPPORTED;
+  if (R == 0) return OMNI_OK;
+  if (!x || !q || !scale || !aligned16(x) || !aligned16(q)) return OMNI_ERR_INVALID_ARG;
+  return hip_status(omni::launch_quantize_rows(dt == OMNI_BF16, R, k, x, q, scale, stream));
+}
+
+static omni_status quantized_product(omni_dtype out_dt, int M, int E, int n, int k, int R, int Ro,
+                                     const int8_t* xq, const float* x_scale,
+                                     const int32_t* x_row, const int8_t* wq,
+                                     const float* w_scale, const int32_t* offsets,
+                                     omni_activation act, void* out, const int32_t* out_row,
+                                     hipStream_t stream) {
+  if (out_dt != OMNI_F32 && out_dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
+  omni::ExpertMatmulArgs a = {};
+  a.type = omni::kRowsI8;
+  a.out_bf16 = out_dt == OMNI_BF16;
+  a.M = M; a.E = E; a.n = n; a.k = k; a.R = R; a.Ro = Ro;
+  a.x = xq; a.x_scale = x_scale; a.x_row = x_row; a.w = wq; a.w_scale = w_scale;
+  a.offsets = offsets; a.out = out; a.out_row = out_row;
+  return expert_product(a, 16, 1, act, stream);
+}
+
+omni_status omni_quantized_matmul(omni_dtype out_dt, int M, int n, int k, const int8_t* xq,
+                                  const float* x_scale, const int8_t* wq, const float* w_scale,
+                                  omni_activation act, void* out, hipStream_t stream) {
+  return quantized_product(out_dt, M, 1, n, k, M, M, xq, x_scale, nullptr, wq, w_scale, nullptr,
+                           act, out, nullptr, stream);
+}
+
+omni_status omni_quantized_expert_matmul(omni_dtype out_dt, int M, int E, int n, int k, int R,
+                                         int Ro, const int8_t* xq, const float* x_scale,
+                                         const int32_t* x_row, const int8_t* wq,
+                                         const float* w_scale, const int32_t* offsets,
+                                         omni_activation act, void* out, const int32_t* out_row,
+                                         hipStream_t stream) {
+  if (!offsets) return OMNI_ERR_INVALID_ARG;
+  return quantized_product(out_dt, M, E, n, k, R, Ro, xq, x_scale, x_row, wq, w_scale, offsets,
+                           act, out, out_row, stream);
+}
+
 }  // extern "C"

@@ -1,0 +1,95 @@
+// Combining the experts' rows of a token, and its backward:
+//   y[t] (+)= sum_k g[t, k] o[t K + k]
+//   do[t K + k] = g[t, k] dy[t],   dg[t, k] = <dy[t], o[t K + k]>
+#include "device.hpp"
+#include "launch.hpp"
+
+namespace omni {
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const uint16_t* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(a))) |
+         static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(b))) << 16;
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(uint16_t* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void combine_kernel(const T* o, const float* gate, float* y,
+                                                      int L, int K, int n, int accumulate) {
+  const size_t id = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int n4 = n / 4;
+  if (id >= static_cast<size_t>(L) * n4) return;
+  const size_t t = id / n4;
+  const int c = static_cast<int>(id - t * n4) * 4;
+  float4 s = accumulate ? load4(y + t * n + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < K; ++k) {
+    const float g = gate ? gate[t * K + k] : 1.f;
+    const float4 v = load4(o + (t * K + k) * n + c);
+    s.x = fmaf(g, v.x, s.x);
+    s.y = fmaf(g, v.y, s.y);
+    s.z = fmaf(g, v.z, s.z);
+    s.w = fmaf(g, v.w, s.w);
+  }
+  store4(y + t * n + c, s);
+}
+
+// one wave per task
+template <typename T>
+__global__ __launch_bounds__(256) void combine_backward_kernel(const T* o, const float* gate,
+                                                               const float* dy, T* dout,
+                                                               float* dgate, size_t M, int K,
+                                                               int n) {
+  const size_t m = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (m >= M) return;
+  const size_t t = m / K;
+  const float g = gate ? gate[m] : 1.f;
+  float dot = 0.f;
+  for (int c = lane() * 4; c < n; c += kWave * 4) {
+    const float4 d = load4(dy + t * n + c);
+    store4(dout + m * n + c, make_float4(g * d.x, g * d.y, g * d.z, g * d.w));
+    if (dgate) {
+      const float4 v = load4(o + m * n + c);
+      dot = fmaf(d.x, v.x, dot);
+      dot = fmaf(d.y, v.y, dot);
+      dot = fmaf(d.z, v.z, dot);
+      dot = fmaf(d.w, v.w, dot);
+    }
+  }
+  if (dgate) {
+    dot = wave_sum(dot);
+    if (lane() == 0) dgate[m] = dot;
+  }
+}
+
+hipError_t launch_expert_combine(int bf16, int L, int K, int n, const void* o, const float* gate,
+                                 float* y, int accumulate, hipStream_t s) {
+  const unsigned nb = static_cast<unsigned>((static_cast<size_t>(L) * (n / 4) + 255) / 256);
+  if (bf16)
+    combine_kernel<<<nb, 256, 0, s>>>(static_cast<const uint16_t*>(o), gate, y, L, K, n, accumulate);
+  else
+    combine_kernel<<<nb, 256, 0, s>>>(static_cast<const float*>(o), gate, y, L, K, n, accumulate);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine_backward(int bf16, int L, int K, int n, const void* o,
+                                          const float* gate, const float* dy, void* dout,
+                                          float* dgate, hipStream_t s) {
+  const size_t M = static_cast<size_t>(L) * K;
+  const unsigned nb = static_cast<unsigned>((M + 3) / 4);
+  if (bf16)
+    combine_backward_kernel<<<nb, 256, 0, s>>>(static_cast<const uint16_t*>(o), gate, dy,
+                                               static_cast<uint16_t*>(dout), dgate, M, K, n);
+  else
+    combine_backward_kernel<<<nb, 256, 0, s>>>(static_cast<const float*>(o), gate, dy,
+                                               static_cast<float*>(dout), dgate, M, K, n);
+  return hipGetLastError();
+}
+
+}  // namespace omni

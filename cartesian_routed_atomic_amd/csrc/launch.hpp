@@ -119,4 +119,47 @@ hipError_t launch_routed_backward(int bf16, int L, int d, int Nr, int Nc, int K,
                                   int32_t* counts, int32_t* active, float* dw, float* dv,
                                   float* dgate, void* ws, hipStream_t s);
 
+// expert_matmul.hip: products with experts that are matrices, tasks sorted by
+// expert.  offsets NULL: one dense product (E = 1, every row of it).
+constexpr int kRowsF32 = 0, kRowsBf16 = 1, kRowsI8 = 2;
+struct ExpertMatmulArgs {
+  int type;      // kRowsF32, kRowsBf16 or kRowsI8: x and w
+  int out_bf16;  // out's type (of the float types: theirs)
+  int M, E, n, k, R, Ro;
+  int transpose, swiglu;
+  const void* x;
+  const int32_t* x_row;
+  const float* x_scale;
+  const void* w;
+  const float* w_scale;
+  const int32_t* offsets;
+  void* out;
+  const int32_t* out_row;
+};
+struct ExpertWgradArgs {
+  int bf16, M, E, n, k, R, Ry;
+  const void* x;
+  const int32_t* x_row;
+  const void* dy;
+  const int32_t* dy_row;
+  const int32_t* offsets;
+  float* dw;
+};
+// work-items of a launch dimension are counted in 32 bits
+bool expert_matmul_grid_fits(const ExpertMatmulArgs& a);
+bool expert_wgrad_grid_fits(const ExpertWgradArgs& a);
+hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s);
+hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t s);
+
+// expert_combine.hip
+hipError_t launch_expert_combine(int bf16, int L, int K, int n, const void* o, const float* gate,
+                                 float* y, int accumulate, hipStream_t s);
+hipError_t launch_expert_combine_backward(int bf16, int L, int K, int n, const void* o,
+                                          const float* gate, const float* dy, void* dout,
+                                          float* dgate, hipStream_t s);
+
+// quantize.hip
+hipError_t launch_quantize_rows(int bf16, int R, int k, const void* x, int8_t* q, float* scale,
+                                hipStream_t s);
+
 }  // namespace omni

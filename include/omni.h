@@ -449,6 +449,135 @@ omni_status omni_shared_mlp(omni_dtype dt, int L, int d, int d_ff, const void* x
                             const void* w_gate, const void* w_up, const void* w_down, float* y,
                             int accumulate, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/*
+ * Experts that are matrices (the coarse experts the pages set the atomic ones
+ * against, e.g. gist.science explainer §1): E experts, expert e a matrix
+ * W[e] [n, k] (row j: output feature j's weights).  The tasks are sorted by
+ * expert: tasks [offsets[e], offsets[e+1]) are expert e's, as
+ * omni_schedule_tasks orders them with OMNI_GROUP_ID_WINDOW and B = 1 (its
+ * group_offsets [E + 1] are these offsets, task_token and task_index the row
+ * lists below).  Experts without tasks are allowed.
+ *
+ * Offsets are device data: values outside [0, M] count as the nearest bound
+ * and an end before its start as an empty expert; offsets that then overlap
+ * give unspecified results (nothing outside the arrays is touched).  Tasks
+ * from offsets[E] on are not computed and their output rows keep what they
+ * held.  Row lists may be NULL (task m is row m; the array then has at least
+ * M rows); x rows outside [0, R) count as zeros, output rows outside [0, Ro)
+ * are not stored; two tasks with one output row give either's result.
+ */
+typedef enum omni_activation {
+  OMNI_ACT_NONE = 0,
+  OMNI_ACT_SWIGLU = 1         /* silu(gate half) * up half                   */
+} omni_activation;
+
+/*
+ * omni_expert_matmul — ragged product of the tasks with their experts.
+ *
+ *   transpose = 0, OMNI_ACT_NONE:   out[out_row[m], j] = sum_c x[x_row[m], c] w[e, j, c]
+ *   transpose = 0, OMNI_ACT_SWIGLU: w is [E, 2n, k] (rows 0..n-1 the gate half, n..2n-1
+ *                                   the up half) and out = silu(gate) * up, [.., n]
+ *   transpose = 1 (input gradient): out[out_row[m], c] = sum_j x[x_row[m], j] w[e, j, c]
+ *
+ * M tasks; x [R, k] of dt (transpose: [R, n]); w [E, n, k] of dt; offsets
+ * [E + 1] int32; out [Ro, n] of dt (transpose: [Ro, k]); x_row, out_row [M]
+ * int32 or NULL.  Sums are float32, rounded once to dt.
+ * Requires M, R, Ro >= 0, E, n, k >= 1; k (transpose: n and k) a multiple of
+ * 8 (bf16) or 4 (float32), else UNSUPPORTED, as is a launch of 2^32
+ * work-items or more; x, w, out 16-byte aligned.  transpose with SWIGLU is
+ * INVALID_ARG.  M == 0 enqueues nothing.  Deterministic.
+ */
+omni_status omni_expert_matmul(omni_dtype dt, int M, int E, int n, int k, int R, int Ro,
+                               const void* x, const int32_t* x_row, const void* w,
+                               const int32_t* offsets, int transpose, omni_activation act,
+                               void* out, const int32_t* out_row, hipStream_t stream);
+
+/*
+ * omni_expert_weight_grad — weight gradient of omni_expert_matmul:
+ *
+ *   dw[e, j, c] = sum over expert e's tasks m of dy[dy_row[m], j] x[x_row[m], c]
+ *
+ * x [R, k], dy [Ry, n] of dt; x_row, dy_row [M] int32 or NULL; dw [E, n, k]
+ * float32, overwritten (zero for experts without tasks; M == 0 writes zeros).
+ * A task with either row out of range adds nothing.  Requires n and k
+ * multiples of 8 (bf16) or 4 (float32), else UNSUPPORTED; x, dy, dw 16-byte
+ * aligned.  Deterministic: every sum runs in a fixed order, in float32.
+ */
+omni_status omni_expert_weight_grad(omni_dtype dt, int M, int E, int n, int k, int R, int Ry,
+                                    const void* x, const int32_t* x_row, const void* dy,
+                                    const int32_t* dy_row, const int32_t* offsets, float* dw,
+                                    hipStream_t stream);
+
+/*
+ * omni_expert_combine — the experts' rows of every token summed with its gates:
+ *
+ *   y[t, :] (+)= sum_k gate[t, k] o[t K + k, :]
+ *
+ * o [L*K, n] of dt in flatten order (omni_expert_matmul with out_row =
+ * task_index leaves them so); gate [L, K] float32, or NULL for gates of one
+ * (the sum of the tasks' input gradients); y [L, n] float32; accumulate != 0
+ * adds onto y as it stands, e.g. onto omni_shared_mlp's output.  Summed in
+ * float32 in k order, without atomics.
+ * Requires K, n >= 1, n a multiple of 8 (bf16) or 4 (float32), else
+ * UNSUPPORTED; L*K < 2^31; o, y 16-byte aligned.
+ */
+omni_status omni_expert_combine(omni_dtype dt, int L, int K, int n, const void* o,
+                                const float* gate, float* y, int accumulate,
+                                hipStream_t stream);
+
+/*
+ * omni_expert_combine_backward — its gradients for dy [L, n] float32:
+ *
+ *   dout[t K + k, :] = gate[t, k] dy[t, :]      [L*K, n] of dt
+ *   dgate[t, k] = dy[t, :] . o[t K + k, :]      [L, K] float32
+ *
+ * gate NULL: gates of one; dgate NULL: not wanted (o may then be NULL).
+ * Shapes and refusals as omni_expert_combine.  Deterministic.
+ */
+omni_status omni_expert_combine_backward(omni_dtype dt, int L, int K, int n, const void* o,
+                                         const float* gate, const float* dy, void* dout,
+                                         float* dgate, hipStream_t stream);
+
+/*
+ * omni_quantize_rows — rows made 8-bit integers with one scale each:
+ *
+ *   scale[r] = max_c |x[r, c]| / 127 (float32),  q[r, c] = x[r, c] / scale[r]
+ *   rounded to the nearest integer (ties to even, of the exact quotient),
+ *   within [-127, 127]; rows of zeros have scale 0 and q 0
+ *
+ * x [R, k] of dt, q [R, k] int8, scale [R] float32.  Activations are rows of
+ * tokens, weights rows of output channels.  Requires k a multiple of 16, else
+ * UNSUPPORTED; x and q 16-byte aligned.
+ */
+omni_status omni_quantize_rows(omni_dtype dt, int R, int k, const void* x, int8_t* q,
+                               float* scale, hipStream_t stream);
+
+/*
+ * omni_quantized_matmul — product of quantised rows with quantised weights:
+ *
+ *   out[m, j] = (sum_c xq[m, c] wq[j, c]) x_scale[m] w_scale[j]
+ *
+ * xq [M, k], wq [n, k] int8 (any value), x_scale [M], w_scale [n] float32;
+ * out [M, n] of out_dt.  OMNI_ACT_SWIGLU: wq [2n, k], w_scale [2n], gate half
+ * first, out = silu(gate) * up.  The integer sum is exact (int32), then
+ * scaled in float32 (x_scale first) and rounded once to out_dt.
+ * Requires k a multiple of 16 and at most 131071, else UNSUPPORTED; xq, wq,
+ * out 16-byte aligned.
+ *
+ * omni_quantized_expert_matmul — the same over tasks sorted by expert, wq
+ * [E, n, k] and w_scale [E, n] (SWIGLU: 2n), x_scale [R] beside xq [R, k];
+ * rows, offsets and refusals as omni_expert_matmul.
+ */
+omni_status omni_quantized_matmul(omni_dtype out_dt, int M, int n, int k, const int8_t* xq,
+                                  const float* x_scale, const int8_t* wq, const float* w_scale,
+                                  omni_activation act, void* out, hipStream_t stream);
+omni_status omni_quantized_expert_matmul(omni_dtype out_dt, int M, int E, int n, int k, int R,
+                                         int Ro, const int8_t* xq, const float* x_scale,
+                                         const int32_t* x_row, const int8_t* wq,
+                                         const float* w_scale, const int32_t* offsets,
+                                         omni_activation act, void* out, const int32_t* out_row,
+                                         hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

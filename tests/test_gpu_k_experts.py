@@ -1,0 +1,305 @@
+"""Products with experts that are matrices, their gradients, the combination
+of a token's experts and the 8-bit products, against the float64 oracle.
+
+Tolerances, entry by entry.  A float32 sum of terms with absolute sum S, in
+any order of at most c additions, is off by at most c 2^-23 S (each addition,
+rounded or cut, by 2^-23 of the partial sum, which S bounds); products of
+bf16 numbers are exact in float32, those of float32 numbers off by 2^-24 of
+the term (the c + 2 below).  Rounding the result to bf16 adds 2^-8 of it,
+to float32 2^-24.  silu(g) u in float32 adds the exponential's error, a few
+2^-22 (1 + |g|) relative: 2^-16 covers |g| <= 12.  The 8-bit sum is exact: its
+conversion and the two scalings are off by 2^-24 each."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import omni_experts as OE
+from synth import bf16_bits_to_f32, f32_to_bf16_bits
+from tests.gpu_helpers import dev, host, log
+
+B = pytest.importorskip("cartesian_routed_atomic_amd.binding")
+gpu = pytest.mark.gpu
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+def rand(rng, shape, dt, scale=1.0):
+    a = (rng.standard_normal(shape) * scale).astype(np.float32)
+    return f32_to_bf16_bits(a) if dt == "bf16" else a
+
+
+def f32(a):
+    return bf16_bits_to_f32(a) if a.dtype == np.uint16 else a
+
+
+def offsets(counts):
+    return np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+
+
+def close(got, want, tol, what):
+    got = f32(got).astype(np.float64)
+    bad = ~(np.abs(got - want) <= tol)
+    if bad.any():
+        i = tuple(int(v[0]) for v in np.nonzero(bad))
+        raise AssertionError(f"{what}: {bad.sum()} of {bad.size} off, first at {i}: "
+                             f"{got[i]} want {want[i]} tol {tol[i]}")
+
+
+def sum_tol(c, mass, want, dt):
+    return (c + 2) * 2.0 ** -23 * mass + HALF[dt] * np.abs(want) * 1.001 + 1e-38
+
+
+# name: counts of the experts, n, k
+SHAPES = {
+    "one_task": ([1], 8, 8),
+    "one_row_each": ([1, 0, 1, 1, 0], 72, 136),
+    "empty_ends": ([0, 5, 0, 0, 17, 0], 40, 64),
+    "all_empty": ([0, 0, 0], 64, 64),
+    "tile_edges": ([16, 15, 17, 63, 64, 65, 127, 128, 129, 1], 136, 200),
+    "skewed": ([700, 3, 0, 41, 1, 9, 0, 130], 264, 96),
+    "many_experts": ([i % 5 for i in range(200)], 48, 72),
+    "short_inner": ([33, 2, 90], 152, 8),
+    "long_inner": ([3, 9], 24, 2056),
+    "wide": ([300, 257], 1032, 40),
+    "dense": ([513], 256, 256),
+}
+PAD = 7  # tasks behind the last expert's
+
+
+def case(name, dt, seed, gather, scatter, transpose=False, swiglu=False, n=None):
+    counts, n0, k = SHAPES[name]
+    n = n or n0
+    rng = np.random.default_rng(seed)
+    off = offsets(counts)
+    M = int(off[-1]) + PAD
+    R = M // 3 + 2 if gather else M
+    inner, width = (n, k) if transpose else (k, n)
+    x = rand(rng, (R, inner), dt)
+    w = rand(rng, (len(counts), (2 if swiglu else 1) * n, k), dt, 1 / np.sqrt(inner))
+    x_row = rng.integers(0, R, M).astype(np.int32) if gather else None
+    out_row = rng.permutation(M).astype(np.int32) if scatter else None
+    out0 = rand(rng, (M, width), dt)
+    return rng, off, M, x, w, x_row, out_row, out0
+
+
+def check_matmul(name, dt, gather, scatter, transpose=False, swiglu=False, n=None):
+    rng, off, M, x, w, xr, orow, out0 = case(name, dt, 11, gather, scatter, transpose, swiglu, n)
+    log(f"[expert_matmul] {name} {dt} gather={gather} scatter={scatter} transpose={transpose} "
+        f"swiglu={swiglu} M={M} w={w.shape}")
+    want, mass = OE.expert_matmul_f64(x, w, off, M, f32(out0), xr, orow, transpose, swiglu)
+    out = dev(out0)
+    B.expert_matmul(dev(x), dev(w), dev(off), x_row=dev(xr), out=out, out_row=dev(orow),
+                    transpose=transpose, swiglu=swiglu)
+    got = host(out)
+    tol = sum_tol(x.shape[1], mass, want, dt)
+    if swiglu:
+        tol = tol + 2.0 ** -16 * np.abs(want)
+    tol[mass == 0] = 0
+    close(got, want, tol, name)
+    # rows of no task: untouched, bit for bit
+    rows = np.arange(M) if orow is None else orow
+    idle = rows[int(off[-1]):]
+    np.testing.assert_array_equal(got[idle], out0[idle])
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_expert_matmul(name, dt):
+    check_matmul(name, dt, gather=True, scatter=False)
+    check_matmul(name, dt, gather=False, scatter=True)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_expert_matmul_transposed(name, dt):
+    check_matmul(name, dt, gather=True, scatter=True, transpose=True)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_expert_matmul_swiglu(name, dt):
+    check_matmul(name, dt, gather=True, scatter=True, swiglu=True)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 7, 33, 255])
+def test_expert_matmul_odd_width(dt, n):
+    # rows of odd width are not 16-byte aligned
+    check_matmul("skewed", dt, gather=True, scatter=False, n=n)
+    check_matmul("empty_ends", dt, gather=False, scatter=True, swiglu=True, n=n)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("name", list(SHAPES))
+def test_expert_weight_grad(name, dt):
+    counts, n, k = SHAPES[name]
+    rng = np.random.default_rng(5)
+    off = offsets(counts)
+    M = int(off[-1]) + PAD
+    x, dy = rand(rng, (M // 2 + 1, k), dt), rand(rng, (M, n), dt)
+    xr = rng.integers(0, x.shape[0], M).astype(np.int32)
+    yr = rng.permutation(M).astype(np.int32)
+    log(f"[expert_weight_grad] {name} {dt} M={M} n={n} k={k}")
+    for a, b in ((xr, yr), (None, None), (xr, None)):
+        xa = x if a is not None else rand(rng, (M, k), dt)
+        want, mass = OE.expert_weight_grad_f64(xa, dy, off, M, a, b)
+        dw = torch.full(want.shape, float("nan"), device="cuda")
+        B.expert_weight_grad(dev(xa), dev(dy), dev(off), x_row=dev(a), dy_row=dev(b), dw=dw)
+        tol = sum_tol(max(counts), mass, want, "f32")
+        tol[mass == 0] = 0
+        close(host(dw), want, tol, name)
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_out_of_range(dt):
+    """x rows out of range count as zeros, output rows out of range are dropped,
+    and their tasks add nothing to the weight gradient."""
+    rng = np.random.default_rng(8)
+    counts, n, k = [40, 0, 77], 72, 64
+    off = offsets(counts)
+    M = int(off[-1])
+    x, w = rand(rng, (50, k), dt), rand(rng, (3, n, k), dt)
+    xr = rng.integers(0, 50, M).astype(np.int32)
+    xr[[0, 50, 116]] = [-1, 50, 2 ** 31 - 1]
+    orow = rng.permutation(M).astype(np.int32)
+    orow[[1, 60]] = [M, -5]
+    out0 = rand(rng, (M, n), dt)
+    want, mass = OE.expert_matmul_f64(x, w, off, M, f32(out0), xr, orow)
+    out = dev(out0)
+    B.expert_matmul(dev(x), dev(w), dev(off), x_row=dev(xr), out=out, out_row=dev(orow))
+    close(host(out), want, sum_tol(k, mass, want, dt) * (mass > 0), "rows")
+    dy = rand(rng, (M, n), dt)
+    want, mass = OE.expert_weight_grad_f64(x, dy, off, M, xr, orow)
+    dw = B.expert_weight_grad(dev(x), dev(dy), dev(off), x_row=dev(xr), dy_row=dev(orow))
+    close(host(dw), want, sum_tol(max(counts), mass, want, "f32"), "dw rows")
+
+
+@gpu
+def test_offsets_out_of_order():
+    """Offsets outside [0, M] and ends before starts: clamped, nothing outside
+    the arrays is touched."""
+    rng = np.random.default_rng(9)
+    M, n, k = 90, 64, 64
+    x, w = rand(rng, (M, k), "bf16"), rand(rng, (4, n, k), "bf16")
+    off = np.array([-3, 20, 20, 10, 10 ** 9], dtype=np.int32)  # expert 3: [10, 90)
+    out0 = rand(rng, (M, n), "bf16")
+    want, mass = OE.expert_matmul_f64(x, w, off, M, f32(out0))
+    out = dev(out0)
+    B.expert_matmul(dev(x), dev(w), dev(off), out=out)
+    got = host(out)
+    assert got.shape == (M, n)
+    # rows 0 .. 9 are expert 0's alone, rows 20 .. 89 expert 3's alone
+    tol = sum_tol(k, mass, want, "bf16")
+    close(got[:10], want[:10], tol[:10], "clamped")
+    close(got[20:], want[20:], tol[20:], "clamped")
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("L,K,n", [(1, 1, 8), (1, 8, 2048), (5, 3, 72), (67, 6, 1000),
+                                   (300, 2, 128), (33, 64, 264)])
+def test_combine(L, K, n, dt):
+    rng = np.random.default_rng(L * 100 + K)
+    o = rand(rng, (L * K, n), dt)
+    gate = rng.random((L, K)).astype(np.float32)
+    base = rng.standard_normal((L, n)).astype(np.float32)
+    dy = rng.standard_normal((L, n)).astype(np.float32)
+    log(f"[combine] L={L} K={K} n={n} {dt}")
+    for g in (gate, None):
+        for acc in (False, True):
+            want, mass = OE.expert_combine_f64(o, K, g, base if acc else None)
+            y = dev(base) if acc else torch.full((L, n), float("nan"), device="cuda")
+            B.expert_combine(dev(o), K, gate=dev(g), y=y, accumulate=acc)
+            close(host(y), want, sum_tol(K, mass, want, "f32"), "combine")
+    do, dg, mass = OE.expert_combine_backward_f64(o, gate, dy)
+    gdo, gdg = B.expert_combine_backward(dev(o), dev(gate), dev(dy))
+    close(host(gdo), do, HALF[dt] * np.abs(do) * 1.001 + 2.0 ** -24 * np.abs(do), "do")
+    close(host(gdg), dg, sum_tol(n, mass, dg, "f32"), "dgate")
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("R,k", [(1, 16), (3, 48), (7, 1040), (2, 8208), (65, 128)])
+def test_quantize_rows(R, k, dt):
+    rng = np.random.default_rng(R + k)
+    x = f32(rand(rng, (R, k), dt))
+    x[:, ::7] *= 20
+    if R > 2:
+        x[1] = 0.0                       # a row of zeros
+        x[2, 1:] = 0.0                   # one value alone
+    if R > 4:
+        x[3] = rng.integers(-254, 255, k) * 0.5 * 2.0 ** -10   # exact halves of the scale: ties
+        x[3, 0] = 127 * 2.0 ** -10
+        x[3, 1:] = np.clip(x[3, 1:], -126.5 * 2.0 ** -10, 126.5 * 2.0 ** -10)
+        x[4] *= np.float32(1e-38)        # near the smallest normal numbers
+        x[5] *= np.float32(1e36)        # near the largest
+    if dt == "bf16":
+        x = f32_to_bf16_bits(x)
+    q, s = OE.quantize_rows(x)
+    gq, gs = B.quantize_rows(dev(x))
+    np.testing.assert_array_equal(host(gs), s)
+    np.testing.assert_array_equal(host(gq), q)
+
+
+def q_tol(mass, want, dt, swiglu):
+    t = 4 * 2.0 ** -24 * mass + HALF[dt] * np.abs(want) * 1.001 + 1e-38
+    return t + 2.0 ** -16 * np.abs(want) if swiglu else t
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("M,n,k", [(1, 8, 16), (1, 264, 2064), (3, 5, 80), (17, 130, 64),
+                                   (130, 136, 144), (257, 520, 96), (64, 1000, 272)])
+def test_quantized_matmul(M, n, k, swiglu, dt):
+    rng = np.random.default_rng(M + n + k)
+    rows = n * (2 if swiglu else 1)
+    xq = rng.integers(-128, 128, (M, k)).astype(np.int8)
+    wq = rng.integers(-128, 128, (rows, k)).astype(np.int8)
+    xq[0], wq[0] = -128, -128                    # the largest sum
+    xs = (rng.random(M) * 2.0 ** -8).astype(np.float32)
+    ws = (rng.random(rows) / k ** 0.5 * 2.0 ** -6).astype(np.float32)
+    want, mass = OE.expert_matmul_f64(xq.astype(np.float32), wq.astype(np.float32)[None],
+                                      [0, M], M, np.zeros((M, n)), swiglu=swiglu, x_scale=xs,
+                                      w_scale=ws[None])
+    log(f"[quantized_matmul] M={M} n={n} k={k} swiglu={swiglu} {dt}")
+    out = B.quantized_matmul(dev(xq), dev(xs), dev(wq), dev(ws), swiglu=swiglu,
+                             out_dtype=torch.bfloat16 if dt == "bf16" else torch.float32)
+    close(host(out), want, q_tol(mass, want, dt, swiglu), "quantized")
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("name", ["one_task", "one_row_each", "empty_ends", "all_empty",
+                                  "tile_edges", "many_experts", "skewed", "dense"])
+def test_quantized_expert_matmul(name, swiglu, dt):
+    counts, n, k = SHAPES[name]
+    k = (k + 15) // 16 * 16
+    rng = np.random.default_rng(3)
+    off = offsets(counts)
+    M, E, rows = int(off[-1]) + PAD, len(counts), n * (2 if swiglu else 1)
+    R = M // 2 + 1
+    xq = rng.integers(-128, 128, (R, k)).astype(np.int8)
+    wq = rng.integers(-128, 128, (E, rows, k)).astype(np.int8)
+    xs = (rng.random(R) * 2.0 ** -8).astype(np.float32)
+    ws = (rng.random((E, rows)) / k ** 0.5 * 2.0 ** -6).astype(np.float32)
+    xr = rng.integers(0, R, M).astype(np.int32)
+    orow = rng.permutation(M).astype(np.int32)
+    out0 = rand(rng, (M, n), dt)
+    log(f"[quantized_expert_matmul] {name} swiglu={swiglu} {dt} M={M} n={n} k={k}")
+    want, mass = OE.expert_matmul_f64(xq.astype(np.float32), wq.astype(np.float32), off, M,
+                                      f32(out0), xr, orow, swiglu=swiglu, x_scale=xs, w_scale=ws)
+    out = dev(out0)
+    B.quantized_expert_matmul(dev(xq), dev(xs), dev(wq), dev(ws), dev(off), x_row=dev(xr),
+                              out=out, out_row=dev(orow), swiglu=swiglu)
+    got = host(out)
+    idle = orow[int(off[-1]):]
+    np.testing.assert_array_equal(got[idle], out0[idle])
+    busy = orow[:int(off[-1])]
+    close(got[busy], want[busy], q_tol(mass[busy], want[busy], dt, swiglu), name)
