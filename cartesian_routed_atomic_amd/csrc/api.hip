@@ -426,6 +426,8 @@ static omni_status expert_product(omni::ExpertMatmulArgs& a, int k_unit, int n_u
   if (!a.w || (a.type == omni::kRowsI8 && !a.w_scale)) return OMNI_ERR_INVALID_ARG;
   if (a.M > 0 && (!a.x || !a.out || (a.type == omni::kRowsI8 && !a.x_scale)))
     return OMNI_ERR_INVALID_ARG;
+  // rows out of range are read as row 0 or R - 1 and their results replaced
+  if (a.M > 0 && a.R < 1) return OMNI_ERR_INVALID_ARG;
   // without a row list task m is row m
   if ((!a.x_row && a.R < a.M) || (!a.out_row && a.Ro < a.M)) return OMNI_ERR_INVALID_ARG;
   if (!aligned16(a.w) || (a.M > 0 && (!aligned16(a.x) || !aligned16(a.out))))

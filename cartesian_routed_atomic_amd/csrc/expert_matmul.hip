@@ -5,20 +5,67 @@
 // and the same forward product over 8-bit integers with a scale for each row
 // of x and each row of W.
 //
-// First form: one 64 x 64 output tile per workgroup of 256 threads, 4 x 4
-// sums per thread, 16 contraction steps at a time through LDS.
+// All of them are tiles of one matrix-core pipeline.  An output tile has an
+// operand P that runs over its rows (tasks) and an operand Q that runs over
+// its columns (output features); a stage holds 64 bytes of the contraction
+// (32 bf16, 64 int8 or 16 float32) of both.  Q is the MFMA's first operand and
+// P its second, so a lane holds four consecutive columns of one output row and
+// stores them without a pass through LDS.
 #include "device.hpp"
 #include "launch.hpp"
 
 namespace omni {
 
-constexpr int TM = 64, TN = 64, TK = 16;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-// Row tiles of the experts, found by every wave for itself: lane l counts the
-// tiles of q consecutive experts, a prefix sum over the lanes finds the lane
-// that owns row tile `rt`, and that lane's experts are walked.  Offsets are
-// clamped to [0, M] and to ascending order, so no value of theirs can lead a
-// read or write outside the row lists.
+// ------------------------------------------------------------------ element types
+
+struct Bf16Op {
+  using Frag = bf16x8;
+  using Acc = f32x4;
+  using T = uint16_t;
+  static constexpr int kBytes = 2;
+  static __device__ __forceinline__ void mma(Acc& c, Frag q, Frag p) {
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q, p, c, 0, 0, 0);
+  }
+};
+struct I8Op {
+  using Frag = i32x4;
+  using Acc = i32x4;
+  using T = int8_t;
+  static constexpr int kBytes = 1;
+  static __device__ __forceinline__ void mma(Acc& c, Frag q, Frag p) {
+    c = __builtin_amdgcn_mfma_i32_16x16x64_i8(q, p, c, 0, 0, 0);
+  }
+};
+// A 16-byte fragment holds four consecutive contraction steps of a lane; the
+// j-th of four MFMAs takes element j of both operands, so it contracts steps
+// j, 4 + j, 8 + j and 12 + j of the stage.
+struct F32Op {
+  using Frag = f32x4;
+  using Acc = f32x4;
+  using T = float;
+  static constexpr int kBytes = 4;
+  static __device__ __forceinline__ void mma(Acc& c, Frag q, Frag p) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(q[j], p[j], c, 0, 0, 0);
+  }
+};
+
+// 16 bytes of zeros: where a lane of a direct load has nothing to fetch
+__device__ __attribute__((aligned(16))) const uint32_t kZeroChunk[4] = {0, 0, 0, 0};
+
+// ------------------------------------------------------------------ row tiles of the experts
+
+// Found by every wave for itself: lane l counts the tiles of q consecutive
+// experts, a prefix sum over the lanes gives the total and the lane that owns
+// row tile `rt`, and that lane's experts are walked.  Offsets are clamped to
+// [0, M] and to ascending order, so no value of theirs can lead a read or
+// write outside the row lists.
 struct ExpertTile {
   int e, m0, m1;  // expert, first task of the tile, end of the tile (m0 == m1: none)
 };
@@ -26,22 +73,32 @@ __device__ __forceinline__ void expert_range(const int32_t* off, int e, int M, i
   lo = min(max(off[e], 0), M);
   hi = min(max(off[e + 1], lo), M);
 }
-__device__ ExpertTile find_expert_tile(const int32_t* off, int E, int M, int bm, int rt) {
+struct ExpertScan {
+  int mine, upto, total;
+};
+__device__ __forceinline__ ExpertScan scan_experts(const int32_t* off, int E, int M, int bm) {
   const int l = lane(), q = (E + kWave - 1) / kWave;
-  int mine = 0;
+  ExpertScan s{0, 0, 0};
   for (int i = 0; i < q; ++i) {
     const int e = l * q + i;
     if (e < E) {
       int lo, hi;
       expert_range(off, e, M, lo, hi);
-      mine += (hi - lo + bm - 1) / bm;
+      s.mine += (hi - lo + bm - 1) / bm;
     }
   }
-  const int upto = wave_prefix_sum(mine);
-  const uint64_t past = __ballot(upto > rt);
+  s.upto = wave_prefix_sum(s.mine);
+  s.total = __builtin_amdgcn_readlane(s.upto, 63);
+  return s;
+}
+__device__ __forceinline__ ExpertTile find_expert_tile(const ExpertScan& s, const int32_t* off,
+                                                       int E, int M, int bm, int rt) {
+  const int q = (E + kWave - 1) / kWave;
+  const uint64_t past = __ballot(s.upto > rt);
   if (past == 0) return {0, 0, 0};
   const int owner = __ffsll(static_cast<long long>(past)) - 1;
-  int left = rt - (__builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(mine, owner));
+  int left = rt - (__builtin_amdgcn_readlane(s.upto, owner) -
+                   __builtin_amdgcn_readlane(s.mine, owner));
   for (int i = 0; i < q; ++i) {
     const int e = owner * q + i;
     if (e >= E) break;
@@ -53,173 +110,734 @@ __device__ ExpertTile find_expert_tile(const int32_t* off, int E, int M, int bm,
   }
   return {0, 0, 0};
 }
-
-__device__ __forceinline__ float to_f(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ int to_acc(int8_t v) { return v; }
-__device__ __forceinline__ float to_acc(uint16_t v) { return to_f(v); }
-__device__ __forceinline__ float to_acc(float v) { return v; }
-template <typename T> struct AccOf { using type = float; };
-template <> struct AccOf<int8_t> { using type = int; };
-
-// float32 -> bf16, nearest even (NaN stays NaN)
-__device__ __forceinline__ uint16_t to_bf16(float v) {
-  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+// The expert at position pos when every run of 64 experts is put in order of
+// its task counts, most first (ties by id).
+__device__ __forceinline__ int expert_by_size(const int32_t* off, int E, int M, int pos) {
+  const int first = pos & ~63, e = first + lane();
+  int count = -1;
+  if (e < E) {
+    int lo, hi;
+    expert_range(off, e, M, lo, hi);
+    count = hi - lo;
+  }
+  int rank = 0;
+#pragma unroll 8
+  for (int j = 0; j < 64; ++j) {
+    const int c = __builtin_amdgcn_readlane(count, j);
+    rank += c > count || (c == count && j < lane()) ? 1 : 0;
+  }
+  return first + __ffsll(static_cast<long long>(__ballot(rank == pos - first))) - 1;
 }
-__device__ __forceinline__ void put(uint16_t* p, float v) { *p = to_bf16(v); }
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+// Workgroup b runs on XCD b % 8: give every XCD a contiguous run of the tiles
+// there are, so that neighbours share rows and weights in that XCD's L2.
+__device__ __forceinline__ int xcd_tile(int b, int total) {
+  const int per = total >> 3, rem = total & 7, xcd = b & 7;
+  return xcd * per + min(xcd, rem) + (b >> 3);
+}
+__device__ __forceinline__ bool xcd_has(int b, int total) {
+  return (b >> 3) < (total >> 3) + ((b & 7) < (total & 7) ? 1 : 0);
+}
+
+// ------------------------------------------------------------------ stages in LDS
+
+// A stage of an operand whose contraction is contiguous in memory: one 64-byte
+// row (four 16-byte chunks) per output row or column, chunk c of row r stored
+// at c ^ swz.  A 16-byte-per-lane read is served eight lanes at a time from one
+// 128-byte bank window; the swizzles below put the eight rows that such a
+// group reads on eight distinct 16-byte slots.
+//   P: rows r .. r + 7 (consecutive);  Q: rows 0-3 and 8-11 of a 32-row block
+//   (tiles 2i and 2i + 1 take the columns 8 g + 0..3 and 8 g + 4..7 of their 32,
+//   so a lane ends up with eight consecutive columns).
+__device__ __forceinline__ int swz_p(int r) { return (r >> 1) & 3; }
+__device__ __forceinline__ int swz_q(int r) { return ((r >> 1) & 1) | ((r >> 2) & 2); }
+// A stage of an operand whose contraction is strided: one row of `cols`
+// elements per contraction step, 16-byte chunk c of step kk at c ^ swz_t<Op>(kk).
+// bf16: the eight steps 0-3, 8-11 that half a transposing read takes at once
+// land on eight 32-byte slots; float32: the steps 4 g + j of a read on four
+// 64-byte slots.
+template <class Op>
+__device__ __forceinline__ int swz_t(int kk) {
+  return Op::kBytes == 2 ? ((kk & 3) | ((kk >> 1) & 4)) << 1 : kk & 12;
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vm_lds() {  // vmcnt <= N, lgkmcnt = 0
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+}
+// at most `after` stages of I loads each still in flight
+template <int I, int S>
+__device__ __forceinline__ void wait_stages(int after) {
+  static_assert(S <= 5, "four stages at most");
+  if (S > 4 && after >= 3) wait_vm_lds<(S > 4 ? 3 : 0) * I>();
+  else if (S > 3 && after >= 2) wait_vm_lds<(S > 3 ? 2 : 0) * I>();
+  else if (S > 2 && after >= 1) wait_vm_lds<(S > 2 ? 1 : 0) * I>();
+  else wait_vm_lds<0>();
+}
+__device__ __forceinline__ void lds_barrier() {
+  // a bare barrier: a fenced one would also wait for the stages in flight
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+}
+// Direct global -> LDS load: 16 bytes per lane to dst + 16 lane (dst uniform).
+// It writes no register.  The builtin would make the compiler wait for every
+// load in flight before each transposing read (it takes them to overlap); here
+// the pipeline's own waits order them.  M0 needs one wait state before its use
+// (nothing else in these kernels uses it).
+__device__ __forceinline__ void load_lds16(const void* src, uint32_t dst) {
+  __asm__ volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                   :
+                   : "v"(src), "s"(dst)
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) const void*)(p)));
+}
+
+// fragment of a K-contiguous stage: row r, chunk g
+template <class Op, bool Q>
+__device__ __forceinline__ typename Op::Frag frag_rows(const uint8_t* st, int r, int g) {
+  return *reinterpret_cast<const typename Op::Frag*>(
+      st + r * 64 + ((g ^ (Q ? swz_q(r) : swz_p(r))) << 4));
+}
+// fragment of a strided stage: columns c0 .. c0 + 15, this lane's steps
+template <int COLS>
+__device__ __forceinline__ bf16x8 frag_cols_bf16(const uint8_t* st, int c0, int l) {
+  // a transposing read: lane 4 r + c of 16 names the 8 bytes of step r,
+  // columns 4 c .. 4 c + 3, lane i receives the four steps of column i
+  const int i = l & 15, g = l >> 4;
+  s16x4 h[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int kk = g * 8 + u * 4 + (i >> 2);
+    const int chunk = (c0 >> 3) + ((i & 3) >> 1);
+    const uint8_t* p = st + kk * (COLS * 2) + ((chunk ^ swz_t<Bf16Op>(kk)) << 4) + (i & 1) * 8;
+    h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)(p));
+  }
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int COLS>
+__device__ __forceinline__ f32x4 frag_cols_f32(const uint8_t* st, int c0, int l) {
+  const int c = c0 + (l & 15), g = l >> 4;
+  f32x4 v;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int kk = 4 * g + j;
+    v[j] = *reinterpret_cast<const float*>(st + kk * (COLS * 4) + (((c >> 2) ^ swz_t<F32Op>(kk)) << 4) +
+                                           (c & 3) * 4);
+  }
+  return v;
+}
+template <class Op, int COLS>
+__device__ __forceinline__ typename Op::Frag frag_strided(const uint8_t* st, int c0, int l) {
+  if constexpr (Op::kBytes == 2) return frag_cols_bf16<COLS>(st, c0, l);
+  else return frag_cols_f32<COLS>(st, c0, l);
+}
+
+// The pipeline of a tile: a ring of S stages in LDS, filled by direct
+// global -> LDS loads (I of them per wave and stage).  Iteration kt: wait until
+// stage kt + 1 has landed, barrier, then run stage kt's MFMAs (its fragments
+// are in registers) while the slot of stage kt is refilled with stage kt + S
+// and stage kt + 1's fragments are read into the other register set.  Loads and
+// reads are issued between the MFMAs, one row of tiles at a time: issued
+// together after the barrier they fill the load and LDS queues, and a wave
+// that waits for room there issues no MFMA.
+//   issue(kt, u, may_end): load u of stage kt; may_end: it may be the last
+//   read_p(kt, i), read_q(kt, j): fragments of stage kt
+// The steady loop has no branch between a read and the MFMAs that use it: a
+// join there makes the compiler wait for the reads just issued.
+template <class Op, int I, int S, int TI, int TJ, class Issue, class ReadP, class ReadQ>
+__device__ __forceinline__ void run_pipeline(int nk, Issue issue, ReadP read_p, ReadQ read_q,
+                                             typename Op::Acc (&acc)[TI][TJ]) {
+  using Frag = typename Op::Frag;
+  Frag p0[TI], q0[TJ], p1[TI], q1[TJ];
+  auto mma_row = [&](int i, const Frag (&p)[TI], const Frag (&q)[TJ]) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) Op::mma(acc[i][j], q[j], p[i]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto steady = [&](int kt, const Frag (&p)[TI], const Frag (&q)[TJ], Frag (&np)[TI],
+                    Frag (&nq)[TJ]) {
+    wait_vm_lds<(S - 2) * I>();
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+#pragma unroll
+      for (int u = i * I / TI; u < (i + 1) * I / TI; ++u) issue(kt + S, u, false);
+#pragma unroll
+      for (int j = i * TJ / TI; j < (i + 1) * TJ / TI; ++j) nq[j] = read_q(kt + 1, j);
+      np[i] = read_p(kt + 1, i);
+      mma_row(i, p, q);
+    }
+  };
+  auto tail = [&](int kt, const Frag (&p)[TI], const Frag (&q)[TJ], Frag (&np)[TI],
+                  Frag (&nq)[TJ]) {
+    if (kt + 1 < nk) {
+      wait_stages<I, S>(min(kt + S - 1, nk - 1) - (kt + 1));
+      lds_barrier();
+      if (kt + S < nk) {
+#pragma unroll
+        for (int u = 0; u < I; ++u) issue(kt + S, u, true);
+      }
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) nq[j] = read_q(kt + 1, j);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) np[i] = read_p(kt + 1, i);
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) mma_row(i, p, q);
+  };
+#pragma unroll
+  for (int v = 0; v < S; ++v)
+    if (v < nk) {
+#pragma unroll
+      for (int u = 0; u < I; ++u) issue(v, u, true);
+    }
+  wait_stages<I, S + 1>(min(S, nk) - 1);
+  lds_barrier();
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) q0[j] = read_q(0, j);
+#pragma unroll
+  for (int i = 0; i < TI; ++i) p0[i] = read_p(0, i);
+  int kt = 0;
+  for (; kt + S + 2 < nk; kt += 2) {
+    steady(kt, p0, q0, p1, q1);
+    steady(kt + 1, p1, q1, p0, q0);
+  }
+  for (; kt < nk; kt += 2) {
+    tail(kt, p0, q0, p1, q1);
+    if (kt + 1 < nk) tail(kt + 1, p1, q1, p0, q0);
+  }
+}
+
+// ------------------------------------------------------------------ outputs
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {  // nearest even
+  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(a))) |
+         static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(b))) << 16;
+}
+template <int N>
+__device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[N]) {
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]),
+                                              bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+}
+template <int N>
+__device__ __forceinline__ void store_vec(float* p, const float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4)
+    *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+__device__ __forceinline__ void store_one(uint16_t* p, float v) {
+  *p = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
+// N values of row `dst` at column c; aligned: the rows start at 16 bytes
+template <typename TO, int N>
+__device__ __forceinline__ void store_cols(TO* dst, int c, int width, bool aligned,
+                                           const float (&v)[N]) {
+  if (aligned && c + N <= width) {
+    store_vec(dst + c, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (c + i < width) store_one(dst + c + i, v[i]);
+  }
+}
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
-template <typename T, typename TO, bool TRANS, bool SWIGLU>
-__global__ __launch_bounds__(256) void expert_tile_kernel(ExpertMatmulArgs a) {
-  using Acc = typename AccOf<T>::type;
-  __shared__ Acc sa[TK][TM + 1], sb[TK][TN + 1], sc[SWIGLU ? TK : 1][TN + 1];
-  const int tid = threadIdx.x;
-  // inner length, output width, and W's strides over (output column, inner)
-  const int K = TRANS ? a.n : a.k, N = TRANS ? a.k : a.n;
-  const int n_nt = (N + TN - 1) / TN;
-  const int rt = blockIdx.x / n_nt, n0 = (blockIdx.x - rt * n_nt) * TN;
-  ExpertTile t{0, rt * TM, min(a.M, (rt + 1) * TM)};
-  if (a.offsets) t = find_expert_tile(a.offsets, a.E, a.M, TM, rt);
-  if (t.m0 >= t.m1) return;
-  const T* x = static_cast<const T*>(a.x);
-  const T* w = static_cast<const T*>(a.w) +
-               static_cast<size_t>(t.e) * (SWIGLU ? 2 : 1) * a.n * a.k;
-  Acc acc[4][4] = {}, acu[4][4] = {};
-  const int ty = tid >> 4, tx = tid & 15;
-  for (int k0 = 0; k0 < K; k0 += TK) {
-    for (int i = tid; i < TM * TK; i += 256) {
-      const int r = i / TK, c = k0 + i % TK, m = t.m0 + r;
-      Acc v = 0;
-      if (m < t.m1 && c < K) {
-        const int row = a.x_row ? a.x_row[m] : m;
-        if (row >= 0 && row < a.R) v = to_acc(x[static_cast<size_t>(row) * K + c]);
-      }
-      sa[i % TK][r] = v;
-    }
-    for (int i = tid; i < TN * TK; i += 256) {
-      const int j = TRANS ? i % TN : i / TK, c = TRANS ? i / TN : i % TK;
-      const bool in = n0 + j < N && k0 + c < K;
-      const size_t at = TRANS ? static_cast<size_t>(k0 + c) * a.k + (n0 + j)
-                              : static_cast<size_t>(n0 + j) * a.k + (k0 + c);
-      sb[c][j] = in ? to_acc(w[at]) : Acc(0);
-      if constexpr (SWIGLU)
-        sc[c][j] = in ? to_acc(w[at + static_cast<size_t>(a.n) * a.k]) : Acc(0);
-    }
-    __syncthreads();
-    for (int c = 0; c < TK; ++c)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-          acc[i][j] += sa[c][ty * 4 + i] * sb[c][tx * 4 + j];
-          if constexpr (SWIGLU) acu[i][j] += sa[c][ty * 4 + i] * sc[c][tx * 4 + j];
-        }
-    __syncthreads();
+// ------------------------------------------------------------------ the product
+
+// Tile BM tasks x BN columns, WM x WN waves, ring of S stages.
+// QT: W is read as [contraction][columns] (the input gradient).
+// SWIGLU: every 64 columns of Q are 32 gate rows, then the same 32 up rows.
+template <class Op, typename TO, bool QT, bool SWIGLU, int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertMatmulArgs a) {
+  using Acc = typename Op::Acc;
+  constexpr int NW = WM * WN, KE = 64 / Op::kBytes;
+  constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
+  constexpr int IP = BM / 16 / NW, IQ = BN / 16 / NW;  // 1-KiB loads per wave and stage
+  constexpr int STAGE = (BM + BN) * 64;
+  constexpr int BNO = SWIGLU ? BN / 2 : BN;            // output columns of a tile
+  static_assert(BM % (16 * NW) == 0 && BN % (16 * NW) == 0, "loads split evenly");
+  static_assert(TJ % (SWIGLU ? 4 : 2) == 0, "column pairs");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
+
+  const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+  const int K = QT ? a.n : a.k, N = QT ? a.k : a.n;
+  const int n_nt = (N + BNO - 1) / BNO;
+  ExpertTile t;
+  int n0;
+  if (a.offsets) {
+    const ExpertScan sc = scan_experts(a.offsets, a.E, a.M, BM);
+    const int total = sc.total * n_nt;
+    if (!xcd_has(blockIdx.x, total)) return;
+    const int id = xcd_tile(blockIdx.x, total), rt = id / n_nt;
+    n0 = (id - rt * n_nt) * BNO;
+    t = find_expert_tile(sc, a.offsets, a.E, a.M, BM, rt);
+  } else {
+    const int id = xcd_tile(blockIdx.x, gridDim.x), rt = id / n_nt;
+    n0 = (id - rt * n_nt) * BNO;
+    t = {0, rt * BM, min(a.M, (rt + 1) * BM)};
   }
-  TO* out = static_cast<TO*>(a.out);
-  for (int i = 0; i < 4; ++i) {
-    const int m = t.m0 + ty * 4 + i;
-    if (m >= t.m1) continue;
-    const int row = a.out_row ? a.out_row[m] : m;
-    if (row < 0 || row >= a.Ro) continue;
-    const int xr = a.x_row ? a.x_row[m] : m;
-    const float rs = a.x_scale && xr >= 0 && xr < a.R ? a.x_scale[xr] : 1.f;
-    for (int j = 0; j < 4; ++j) {
-      const int c = n0 + tx * 4 + j;
-      if (c >= N) continue;
-      const float* ws = a.w_scale ? a.w_scale + static_cast<size_t>(t.e) * (SWIGLU ? 2 : 1) * a.n
-                                  : nullptr;
-      float v = static_cast<float>(acc[i][j]);
-      if (ws) v = v * rs * ws[c];
+  if (t.m0 >= t.m1) return;
+  const uint8_t* x = static_cast<const uint8_t*>(a.x);
+  const uint8_t* w = static_cast<const uint8_t*>(a.w) +
+                     static_cast<size_t>(t.e) * (SWIGLU ? 2 : 1) * a.n * a.k * Op::kBytes;
+
+  // Sources of this lane's direct loads.  Rows and columns past the end (and
+  // rows out of range) re-read a valid one: their results are not stored (or
+  // stored as zeros).  Contraction steps past the end fetch zeros.
+  const int nk = (K + KE - 1) / KE;
+  const int left = (K - (nk - 1) * KE) * Op::kBytes / 16;  // chunks of the last stage
+  const uint8_t* psrc[IP];
+  const uint8_t* qsrc[IQ];
+  int pc[IP], qc[IQ];  // this lane's chunk (or step) of the stage
+#pragma unroll
+  for (int u = 0; u < IP; ++u) {
+    const int r = (wv * IP + u) * 16 + (l >> 2);
+    const int m = min(t.m0 + r, t.m1 - 1);
+    const int row = min(max(a.x_row ? a.x_row[m] : m, 0), a.R - 1);
+    pc[u] = (l & 3) ^ swz_p(r);
+    psrc[u] = x + static_cast<size_t>(row) * K * Op::kBytes + pc[u] * 16;
+  }
+#pragma unroll
+  for (int u = 0; u < IQ; ++u) {
+    if constexpr (QT) {
+      constexpr int CPR = BN * Op::kBytes / 16;  // chunks per step
+      const int at = (wv * IQ + u) * 64 + l, kk = at / CPR, c = (at % CPR) ^ swz_t<Op>(kk);
+      const int col = n0 + c * (16 / Op::kBytes);
+      qc[u] = kk;
+      qsrc[u] = w + (static_cast<size_t>(kk) * N + (col < N ? col : 0)) * Op::kBytes;
+    } else {
+      const int r = (wv * IQ + u) * 16 + (l >> 2);
+      int row;
       if constexpr (SWIGLU) {
-        float u = static_cast<float>(acu[i][j]);
-        if (ws) u = u * rs * ws[a.n + c];
-        v = silu_mul(v, u);
+        row = min(n0 + (r >> 6) * 32 + (r & 31), N - 1) + ((r >> 5) & 1) * N;
+      } else {
+        row = min(n0 + r, N - 1);
       }
-      put(out + static_cast<size_t>(row) * N + c, v);
+      qc[u] = (l & 3) ^ swz_q(r);
+      qsrc[u] = w + static_cast<size_t>(row) * K * Op::kBytes + qc[u] * 16;
+    }
+  }
+  const int q_left = QT ? K - (nk - 1) * KE : left;
+  const size_t q_step = QT ? static_cast<size_t>(KE) * N * Op::kBytes : 64;
+  const uint32_t ring = lds_address(smem);
+  auto issue = [&](int kt, int u, bool may_end) {
+    const uint32_t st = ring + (kt % S) * STAGE;
+    const bool last = may_end && kt == nk - 1;
+    if (u < IP) {
+      const void* src = psrc[u] + static_cast<size_t>(kt) * 64;
+      if (last && pc[u] >= left) src = kZeroChunk;
+      load_lds16(src, st + (wv * IP + u) * 1024);
+    } else {
+      u -= IP;
+      const void* src = qsrc[u] + kt * q_step;
+      if (last && qc[u] >= q_left) src = kZeroChunk;
+      load_lds16(src, st + BM * 64 + (wv * IQ + u) * 1024);
+    }
+  };
+
+  const int wm = wv / WN, wn = wv % WN, fr = l & 15, g = l >> 4;
+  auto read_p = [&](int kt, int i) {
+    return frag_rows<Op, false>(smem + (kt % S) * STAGE, wm * (BM / WM) + i * 16 + fr, g);
+  };
+  auto read_q = [&](int kt, int j) {
+    const uint8_t* st = smem + (kt % S) * STAGE + BM * 64;
+    const int at = wn * (BN / WN);
+    if constexpr (QT)
+      return frag_strided<Op, BN>(st, at + j * 16, l);
+    else
+      return frag_rows<Op, true>(st, at + (j >> 1) * 32 + (j & 1) * 4 + (fr >> 2) * 8 + (fr & 3),
+                                 g);
+  };
+  Acc acc[TI][TJ] = {};
+  run_pipeline<Op, IP + IQ, S>(nk, issue, read_p, read_q, acc);
+
+  // lane (fr, g) holds row i * 16 + fr; columns: QT 16 j + 4 g + 0..3, else
+  // 32 (j / 2) + 8 g + 0..7 of tiles j, j + 1
+  TO* out = static_cast<TO*>(a.out);
+  const bool aligned = (N * sizeof(TO)) % 16 == 0;
+  const float* ws = a.w_scale ? a.w_scale + static_cast<size_t>(t.e) * (SWIGLU ? 2 : 1) * a.n
+                              : nullptr;
+  // scale of the weight row behind this lane's value q of column tile j
+  float wsc[Op::kBytes == 1 ? TJ : 1][4];
+  if constexpr (Op::kBytes == 1) {
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int half = SWIGLU ? (j >> 1) & 1 : 0;
+        const int c = n0 + wn * (BNO / WN) + (SWIGLU ? j >> 2 : j >> 1) * 32 + g * 8 + (j & 1) * 4 + q;
+        wsc[j][q] = c < N ? ws[half * N + c] : 0.f;
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int m = t.m0 + wm * (BM / WM) + i * 16 + fr;
+    if (m >= t.m1) continue;
+    const int row = a.out_row ? a.out_row[m] : m, xr = a.x_row ? a.x_row[m] : m;
+    if (row < 0 || row >= a.Ro) continue;
+    const bool in = xr >= 0 && xr < a.R;
+    float rs = 0.f;
+    if constexpr (Op::kBytes == 1) rs = in ? a.x_scale[xr] : 0.f;
+    TO* dst = out + static_cast<size_t>(row) * N;
+    auto value = [&](int j, int q) {
+      const float v = static_cast<float>(acc[i][j][q]);
+      if constexpr (Op::kBytes == 1) return v * rs * wsc[j][q];
+      else return in ? v : 0.f;
+    };
+    if constexpr (QT) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        float v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = value(j, q);
+        store_cols(dst, n0 + wn * (BN / WN) + j * 16 + g * 4, N, true, v);
+      }
+    } else if constexpr (SWIGLU) {
+#pragma unroll
+      for (int b = 0; b < TJ / 4; ++b) {  // blocks of 32 gate and 32 up columns
+        const int c = n0 + wn * (BN / WN / 2) + b * 32 + g * 8;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int j = b * 4 + (q >> 2);
+          v[q] = silu_mul(value(j, q & 3), value(j + 2, q & 3));
+        }
+        store_cols(dst, c, N, aligned, v);
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < TJ / 2; ++b) {
+        const int c = n0 + wn * (BN / WN) + b * 32 + g * 8;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = value(b * 2 + (q >> 2), q & 3);
+        store_cols(dst, c, N, aligned, v);
+      }
     }
   }
 }
 
-// dW tile: 64 x 64 of one expert, its tasks in order
-template <typename T>
-__global__ __launch_bounds__(256) void expert_wgrad_kernel(ExpertWgradArgs a) {
-  __shared__ float sa[TK][TM + 1], sb[TK][TN + 1];
-  const int tid = threadIdx.x, n_kt = (a.k + TN - 1) / TN, n_nt = (a.n + TM - 1) / TM;
-  const int e = blockIdx.x / (n_kt * n_nt), r = blockIdx.x - e * n_kt * n_nt;
-  const int n0 = r / n_kt * TM, c0 = r % n_kt * TN;
+// ------------------------------------------------------------------ the weight gradient
+
+// Tile BM output features (columns of dy) x BN inputs (columns of x) of one
+// expert; the contraction runs over its tasks in order, whose rows of dy and x
+// are gathered by the same ring of direct loads.  The row numbers of a stage
+// are read one stage ahead through scalar loads (a wave's direct load covers
+// whole rows, so they are uniform), which leaves the vector-memory counter to
+// the ring.
+template <class Op, int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgradArgs a) {
+  using Acc = typename Op::Acc;
+  constexpr int NW = WM * WN, KE = 64 / Op::kBytes;
+  constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
+  constexpr int IP = BM / 16 / NW, IQ = BN / 16 / NW;
+  constexpr int STAGE = (BM + BN) * 64;
+  constexpr int PR = 1024 / (BM * Op::kBytes), QR = 1024 / (BN * Op::kBytes);  // rows per load
+  static_assert(PR >= 1 && QR >= 1, "a load covers whole rows");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
+
+  const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+  const int n_nt = (a.n + BM - 1) / BM, n_kt = (a.k + BN - 1) / BN;
+  // The n_kt tiles of one expert and one dy column block are a group: they
+  // share dy's columns and x's rows in an L2.  Groups are dealt to the XCDs in
+  // turn, the experts with the most tasks first (of every 64), so that long
+  // contractions neither pile up on one XCD nor start last.
+  const int slot = blockIdx.x >> 3, group = slot / n_kt * 8 + (blockIdx.x & 7);
+  if (group >= a.E * n_nt) return;
+  const int e = expert_by_size(a.offsets, a.E, a.M, group / n_nt);
+  const int n0 = group % n_nt * BM, c0 = slot % n_kt * BN;
   int lo, hi;
   expert_range(a.offsets, e, a.M, lo, hi);
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
-  float acc[4][4] = {};
-  const int ty = tid >> 4, tx = tid & 15;
-  for (int m0 = lo; m0 < hi; m0 += TK) {
-    for (int i = tid; i < TK * 64; i += 256) {
-      const int m = m0 + i / 64, c = i % 64;
-      float va = 0.f, vb = 0.f;
-      if (m < hi) {
-        const int ry = a.dy_row ? a.dy_row[m] : m, rx = a.x_row ? a.x_row[m] : m;
-        const bool in = ry >= 0 && ry < a.Ry && rx >= 0 && rx < a.R;
-        if (in && n0 + c < a.n) va = to_f(dy[static_cast<size_t>(ry) * a.n + n0 + c]);
-        if (in && c0 + c < a.k) vb = to_f(x[static_cast<size_t>(rx) * a.k + c0 + c]);
-      }
-      sa[i / 64][c] = va;
-      sb[i / 64][c] = vb;
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  const uint8_t* x = static_cast<const uint8_t*>(a.x);
+  const uint8_t* dy = static_cast<const uint8_t*>(a.dy);
+  const int nk = (hi - lo + KE - 1) / KE;
+
+  // Row numbers of dy and x: read for the next stage as constants at uniform
+  // addresses (scalar loads), checked when that stage is issued; -1: none.
+  typedef const int32_t __attribute__((address_space(4))) ConstInt;
+  ConstInt* xl = (ConstInt*)reinterpret_cast<uintptr_t>(a.x_row ? a.x_row : a.offsets);
+  ConstInt* yl = (ConstInt*)reinterpret_cast<uintptr_t>(a.dy_row ? a.dy_row : a.offsets);
+  constexpr int NP = IP * PR, NQ = BM == BN ? 0 : IQ * QR;  // BM == BN: the same tasks
+  int raw_y[NP + NQ], raw_x[NP + NQ], prow[NP], qrow[IQ * QR];
+  auto task = [&](int kt, int r) {
+    return lo + kt * KE + (r < NP ? wv * NP + r : wv * NQ + r - NP);
+  };
+  auto fetch_rows = [&](int kt) {
+#pragma unroll
+    for (int r = 0; r < NP + NQ; ++r) {
+      const int m = min(task(kt, r), a.M - 1);
+      raw_y[r] = yl[a.dy_row ? m : 0];
+      raw_x[r] = xl[a.x_row ? m : 0];
     }
-    __syncthreads();
-    for (int c = 0; c < TK; ++c)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[c][ty * 4 + i], sb[c][tx * 4 + j], acc[i][j]);
-    __syncthreads();
+  };
+  auto check_rows = [&](int kt) {
+#pragma unroll
+    for (int r = 0; r < NP + NQ; ++r) {
+      const int m = task(kt, r);
+      const int ry = a.dy_row ? raw_y[r] : m, rx = a.x_row ? raw_x[r] : m;
+      const bool ok = m < hi && static_cast<unsigned>(ry) < static_cast<unsigned>(a.Ry) &&
+                      static_cast<unsigned>(rx) < static_cast<unsigned>(a.R);
+      if (r < NP) prow[r] = ok ? ry : -1;
+      if (NQ == 0) qrow[r] = ok ? rx : -1;
+      else if (r >= NP) qrow[r - NP] = ok ? rx : -1;
+    }
+  };
+  constexpr int PCPR = 64 / PR, QCPR = 64 / QR;  // chunks per row
+  const uint32_t ring = lds_address(smem);
+  auto load_rows = [&](const uint8_t* m, int width, int col, int row, uint32_t dst) {
+    const void* src = m + (static_cast<size_t>(row) * width + (col < width ? col : 0)) * Op::kBytes;
+    load_lds16(row < 0 ? kZeroChunk : src, dst);
+  };
+  auto issue = [&](int kt, int u, bool) {
+    const uint32_t st = ring + (kt % S) * STAGE;
+    if (u == 0) {
+      check_rows(kt);
+      fetch_rows(kt + 1);
+    }
+    if (u < IP) {
+      const int sub = l / PCPR, kk = (wv * IP + u) * PR + sub;
+      int row = prow[u * PR];
+#pragma unroll
+      for (int r = 1; r < PR; ++r) row = sub == r ? prow[u * PR + r] : row;
+      load_rows(dy, a.n, n0 + ((l % PCPR) ^ swz_t<Op>(kk)) * (16 / Op::kBytes), row,
+                st + (wv * IP + u) * 1024);
+    } else {
+      u -= IP;
+      const int sub = l / QCPR, kk = (wv * IQ + u) * QR + sub;
+      int row = qrow[u * QR];
+#pragma unroll
+      for (int r = 1; r < QR; ++r) row = sub == r ? qrow[u * QR + r] : row;
+      load_rows(x, a.k, c0 + ((l % QCPR) ^ swz_t<Op>(kk)) * (16 / Op::kBytes), row,
+                st + BM * 64 + (wv * IQ + u) * 1024);
+    }
+  };
+  const int wm = wv / WN, wn = wv % WN, fr = l & 15, g = l >> 4;
+  auto read_p = [&](int kt, int i) {
+    return frag_strided<Op, BM>(smem + (kt % S) * STAGE, wm * (BM / WM) + i * 16, l);
+  };
+  auto read_q = [&](int kt, int j) {
+    return frag_strided<Op, BN>(smem + (kt % S) * STAGE + BM * 64, wn * (BN / WN) + j * 16, l);
+  };
+  Acc acc[TI][TJ] = {};
+  if (nk > 0) {
+    fetch_rows(0);
+    run_pipeline<Op, IP + IQ, S>(nk, issue, read_p, read_q, acc);
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int rr = n0 + ty * 4 + i, cc = c0 + tx * 4 + j;
-      if (rr < a.n && cc < a.k)
-        a.dw[(static_cast<size_t>(e) * a.n + rr) * a.k + cc] = acc[i][j];
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int r = n0 + wm * (BM / WM) + i * 16 + fr;
+    if (r >= a.n) continue;
+    float* dst = a.dw + (static_cast<size_t>(e) * a.n + r) * a.k;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int c = c0 + wn * (BN / WN) + j * 16 + g * 4;
+      if (c < a.k)
+        *reinterpret_cast<float4*>(dst + c) = make_float4(acc[i][j][0], acc[i][j][1],
+                                                          acc[i][j][2], acc[i][j][3]);
     }
+  }
 }
+
+// ------------------------------------------------------------------ few rows per expert
+
+// 16 tasks x 16 CT columns per workgroup, the contraction split over its KS
+// waves: both operands go from memory to the MFMA's registers, U stages ahead,
+// and the waves' sums are added through LDS in wave order.
+template <class Op, typename TO, bool SWIGLU, int RT, int KS, int U>
+__global__ __launch_bounds__(KS * 64) void expert_rows_kernel(ExpertMatmulArgs a) {
+  using Frag = typename Op::Frag;
+  using Acc = typename Op::Acc;
+  constexpr int BM = 16 * RT, CT = SWIGLU ? 2 : 1;  // Q tiles: gate and up
+  __shared__ __attribute__((aligned(16))) Acc part[KS][RT * CT][64];
+  const int wv = threadIdx.x >> 6, l = threadIdx.x & 63, fr = l & 15, g = l >> 4;
+  const int K = a.k, N = a.n;
+  const int n_nt = (N + 15) / 16;
+  ExpertTile t;
+  int n0;
+  if (a.offsets) {
+    const ExpertScan sc = scan_experts(a.offsets, a.E, a.M, BM);
+    const int total = sc.total * n_nt;
+    if (!xcd_has(blockIdx.x, total)) return;
+    const int id = xcd_tile(blockIdx.x, total), rt = id / n_nt;
+    n0 = (id - rt * n_nt) * 16;
+    t = find_expert_tile(sc, a.offsets, a.E, a.M, BM, rt);
+  } else {
+    const int id = xcd_tile(blockIdx.x, gridDim.x), rt = id / n_nt;
+    n0 = (id - rt * n_nt) * 16;
+    t = {0, rt * BM, min(a.M, (rt + 1) * BM)};
+  }
+  if (t.m0 >= t.m1) return;
+  const size_t row_bytes = static_cast<size_t>(K) * Op::kBytes;
+  const uint8_t* w = static_cast<const uint8_t*>(a.w) +
+                     static_cast<size_t>(t.e) * CT * N * row_bytes;
+  const uint8_t* psrc[RT];
+  const uint8_t* qsrc[CT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int m = min(t.m0 + i * 16 + fr, t.m1 - 1);
+    const int row = min(max(a.x_row ? a.x_row[m] : m, 0), a.R - 1);
+    psrc[i] = static_cast<const uint8_t*>(a.x) + row * row_bytes + g * 16;
+  }
+#pragma unroll
+  for (int h = 0; h < CT; ++h)
+    qsrc[h] = w + (min(n0 + fr, N - 1) + static_cast<size_t>(h) * N) * row_bytes + g * 16;
+
+  // chunks of 16 bytes; this wave's stages are [kb, ke)
+  const int chunks = static_cast<int>(row_bytes / 16), nk = (chunks + 3) / 4;
+  const int per = (nk + KS - 1) / KS, kb = min(nk, wv * per), ke = min(nk, kb + per);
+  Acc acc[RT][CT] = {};
+  auto fetch = [&](const uint8_t* src, int kt) {
+    const bool ok = kt < ke && kt * 4 + g < chunks;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (ok) v = *reinterpret_cast<const uint4*>(src + static_cast<size_t>(kt) * 64);
+    return __builtin_bit_cast(Frag, v);
+  };
+  for (int k0 = kb; k0 < ke; k0 += U) {
+    Frag p[U][RT], q[U][CT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int h = 0; h < CT; ++h) q[u][h] = fetch(qsrc[h], k0 + u);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) p[u][i] = fetch(psrc[i], k0 + u);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int h = 0; h < CT; ++h) Op::mma(acc[i][h], q[u][h], p[u][i]);
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int h = 0; h < CT; ++h) part[wv][i * CT + h][l] = acc[i][h];
+  __syncthreads();
+  // wave wv finishes row tiles wv, wv + KS, ...
+  TO* out = static_cast<TO*>(a.out);
+  const bool aligned = (N * sizeof(TO)) % 16 == 0;
+  for (int i = wv; i < RT; i += KS) {
+    Acc s[CT];
+#pragma unroll
+    for (int h = 0; h < CT; ++h) {
+      s[h] = part[0][i * CT + h][l];
+      for (int z = 1; z < KS; ++z) s[h] += part[z][i * CT + h][l];
+    }
+    const int m = t.m0 + i * 16 + fr;
+    if (m >= t.m1) continue;
+    const int row = a.out_row ? a.out_row[m] : m, xr = a.x_row ? a.x_row[m] : m;
+    if (row < 0 || row >= a.Ro) continue;
+    const bool in = xr >= 0 && xr < a.R;
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float z[CT];
+#pragma unroll
+      for (int h = 0; h < CT; ++h) {
+        z[h] = in ? static_cast<float>(s[h][q]) : 0.f;
+        if constexpr (Op::kBytes == 1) {
+          const int c = min(n0 + g * 4 + q, N - 1);
+          z[h] = z[h] * (in ? a.x_scale[xr] : 0.f) *
+                 a.w_scale[static_cast<size_t>(t.e) * CT * N + static_cast<size_t>(h) * N + c];
+        }
+      }
+      v[q] = SWIGLU ? silu_mul(z[0], z[CT - 1]) : z[0];
+    }
+    store_cols(out + static_cast<size_t>(row) * N, n0 + g * 4, N, aligned, v);
+  }
+}
+
+// ------------------------------------------------------------------ dispatch
 
 // sum of ceil(c_e / bm) over at most min(E, M) experts with tasks
 static long long expert_row_tiles(int M, int E, int bm) {
   const long long used = E < M ? E : M;
   return (M + used * (bm - 1)) / bm;
 }
-static long long product_blocks(const ExpertMatmulArgs& a) {
+static long long product_blocks(const ExpertMatmulArgs& a, int bm, int bno) {
   const int N = a.transpose ? a.k : a.n;
-  return expert_row_tiles(a.M, a.E, TM) * ((N + TN - 1) / TN);
+  return expert_row_tiles(a.M, a.E, bm) * ((N + bno - 1) / bno);
 }
-static long long wgrad_blocks(const ExpertWgradArgs& a) {
-  return static_cast<long long>(a.E) * ((a.n + TM - 1) / TM) * ((a.k + TN - 1) / TN);
+static long long wgrad_blocks(const ExpertWgradArgs& a, int bm, int bn) {
+  const long long groups = static_cast<long long>(a.E) * ((a.n + bm - 1) / bm);
+  return (groups + 7) / 8 * 8 * ((a.k + bn - 1) / bn);
 }
 bool expert_matmul_grid_fits(const ExpertMatmulArgs& a) {
-  return product_blocks(a) < (1ll << 32) / 256;
+  return product_blocks(a, 16, 16) < (1ll << 32) / 512;
 }
 bool expert_wgrad_grid_fits(const ExpertWgradArgs& a) {
-  return wgrad_blocks(a) < (1ll << 32) / 256;
+  return wgrad_blocks(a, 64, 64) < (1ll << 32) / 512;
 }
-
-template <typename T, typename TO>
-static hipError_t run_product(const ExpertMatmulArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(product_blocks(a)));
-  if (a.transpose) expert_tile_kernel<T, TO, true, false><<<grid, 256, 0, s>>>(a);
-  else if (a.swiglu) expert_tile_kernel<T, TO, false, true><<<grid, 256, 0, s>>>(a);
-  else expert_tile_kernel<T, TO, false, false><<<grid, 256, 0, s>>>(a);
+template <class Op, typename TO, bool QT, bool SW, int BM, int BN, int WM, int WN, int S>
+static hipError_t run_tiles(const ExpertMatmulArgs& a, hipStream_t s) {
+  const unsigned nb = static_cast<unsigned>(product_blocks(a, BM, SW ? BN / 2 : BN));
+  expert_product_kernel<Op, TO, QT, SW, BM, BN, WM, WN, S><<<nb, WM * WN * 64, 0, s>>>(a);
   return hipGetLastError();
+}
+template <class Op, typename TO, bool SW, int RT, int KS, int U>
+static hipError_t run_rows(const ExpertMatmulArgs& a, hipStream_t s) {
+  const unsigned nb = static_cast<unsigned>(product_blocks(a, RT * 16, 16));
+  expert_rows_kernel<Op, TO, SW, RT, KS, U><<<nb, KS * 64, 0, s>>>(a);
+  return hipGetLastError();
+}
+// By the mean number of rows r of an expert that has tasks, and by the number
+// of tiles.  Measured with 64 experts, 2 x 704 outputs, 2048 inputs, bf16 (us):
+//   r           1     4     8    32    64   128   256   512
+//   16 rows    44    74    83   167   279   512   980  1914
+//   64 x 128   49    75    78    85   102   139   212   367
+//   128 x 128  51    78    81    89   100   117   181   290
+//   256 x 256  55   103   105   109   119   127   173   255
+template <class Op, typename TO, bool QT, bool SW>
+static hipError_t pick(const ExpertMatmulArgs& a, hipStream_t s) {
+  const int r = a.M / (a.E < a.M ? a.E : a.M);
+  const int bno = SW ? 128 : 256;
+  if constexpr (!QT)
+    if (r <= 4 || product_blocks(a, 64, bno / 2) < 64) return run_rows<Op, TO, SW, 1, 8, 4>(a, s);
+  if (r >= 192 && product_blocks(a, 256, bno) >= 192)
+    return run_tiles<Op, TO, QT, SW, 256, 256, 2, 4, 4>(a, s);
+  if (r >= 64 && product_blocks(a, 128, bno / 2) >= 192)
+    return run_tiles<Op, TO, QT, SW, 128, 128, 2, 2, 4>(a, s);
+  return run_tiles<Op, TO, QT, SW, 64, 128, 2, 2, 4>(a, s);
+}
+template <class Op, typename TO>
+static hipError_t run_product(const ExpertMatmulArgs& a, hipStream_t s) {
+  if (a.swiglu) return pick<Op, TO, false, true>(a, s);
+  if constexpr (Op::kBytes != 1)
+    if (a.transpose) return pick<Op, TO, true, false>(a, s);
+  return pick<Op, TO, false, false>(a, s);
 }
 
 hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s) {
   if (a.type == kRowsI8)
-    return a.out_bf16 ? run_product<int8_t, uint16_t>(a, s) : run_product<int8_t, float>(a, s);
-  return a.type == kRowsBf16 ? run_product<uint16_t, uint16_t>(a, s)
-                             : run_product<float, float>(a, s);
+    return a.out_bf16 ? run_product<I8Op, uint16_t>(a, s) : run_product<I8Op, float>(a, s);
+  return a.type == kRowsBf16 ? run_product<Bf16Op, uint16_t>(a, s)
+                             : run_product<F32Op, float>(a, s);
 }
 
-hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t s) {
-  const long long nb = wgrad_blocks(a);
-  if (a.bf16) expert_wgrad_kernel<uint16_t><<<static_cast<unsigned>(nb), 256, 0, s>>>(a);
-  else expert_wgrad_kernel<float><<<static_cast<unsigned>(nb), 256, 0, s>>>(a);
+template <class Op, int BM, int BN, int WM, int WN, int S>
+static hipError_t run_wgrad(const ExpertWgradArgs& a, hipStream_t s) {
+  const unsigned nb = static_cast<unsigned>(wgrad_blocks(a, BM, BN));
+  expert_wgrad_kernel<Op, BM, BN, WM, WN, S><<<nb, WM * WN * 64, 0, s>>>(a);
   return hipGetLastError();
+}
+template <class Op>
+static hipError_t pick_wgrad(const ExpertWgradArgs& a, hipStream_t s) {
+  if (wgrad_blocks(a, 256, 256) >= 256) return run_wgrad<Op, 256, 256, 2, 4, 4>(a, s);
+  return run_wgrad<Op, 128, 128, 2, 2, 4>(a, s);
+}
+hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t s) {
+  return a.bf16 ? pick_wgrad<Bf16Op>(a, s) : pick_wgrad<F32Op>(a, s);
 }
 
 }  // namespace omni
