@@ -491,25 +491,77 @@ def routed_backward(x, wr_t, wc_t, w, v, expert_idx, gate, dy, out=None, workspa
     return r
 
 
-def _same_device(*tensors):
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+# The calls below are short enough that the host's part counts: pointers go to
+# ctypes as plain integers, tensors are checked in one pass (the reason is
+# looked for only once something is wrong) and the current stream is read
+# without building a stream object (torch.cuda.current_stream takes 2.8 us of
+# a 13 us call).
 
 
-def _tasks(rows, offsets, x_row, other_row, other_name):
+def _tensors(dev, *specs):
+    """Check (tensor, name, dtype, shape) of arguments on device index dev."""
+    for t, name, dtype, shape in specs:
+        if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+                or not t.is_contiguous()):
+            _req(t, name, dtype, shape)
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+
+
+def _device_of(t, name):
+    """Device index of the argument that the others have to be with."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return dev
+
+
+def _call(fn, dev, stream, *args):
+    """Call the library on device dev, on `stream` or that device's current one."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, the tensors of cuda:{dev}")
+    else:
+        raw = stream.cuda_stream
+    f = getattr(_lib or lib(), fn)
+    if torch.cuda.current_device() == dev:
+        code = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, raw)
+    if code:
+        _check(fn, code)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return t.shape
+
+
+def _experts(w, swiglu, name):
+    """E, n, k of the experts' weights."""
+    if w.dim() != 3 or (swiglu and w.shape[1] % 2):
+        raise ValueError(f"{name} must be [E, n, k] ([E, 2n, k] with swiglu)")
+    E, rows, k = w.shape
+    return E, rows // 2 if swiglu else rows, k
+
+
+def _tasks(dev, rows, x_row, other, other_name):
     """The number of tasks: the row lists' length, else the rows there are."""
-    _req(offsets, "offsets", torch.int32)
-    if offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError("offsets must be [E + 1]")
     M = rows
-    for t in (x_row, other_row):
-        if t is not None:
-            M = t.numel()
-    for name, t in (("x_row", x_row), (other_name, other_row)):
-        if t is not None:
-            _req(t, name, torch.int32, (M,))
-    if x_row is None and rows < M:
+    if other is not None:
+        M = other.numel()
+        _tensors(dev, (other, other_name, torch.int32, (M,)))
+    if x_row is not None:
+        if other is None:
+            M = x_row.numel()
+        _tensors(dev, (x_row, "x_row", torch.int32, (M,)))
+    elif rows < M:
         raise ValueError(f"{other_name} lists {M} tasks, x has {rows} rows")
     return M
 
@@ -521,88 +573,72 @@ def expert_matmul(x, w, offsets, x_row=None, out=None, out_row=None, transpose=F
     (the input gradient; x [., n], out [., k]).  swiglu: w [E, 2n, k], out [., n]
     = silu(gate half) * up half.  x_row / out_row: int32 row lists or None.
     A fresh out has a row per task (unwritten where no expert has the task)."""
-    E = w.shape[0]
-    if w.dim() != 3 or (swiglu and w.shape[1] % 2):
-        raise ValueError("w must be [E, n, k] ([E, 2n, k] with swiglu)")
-    n, k = w.shape[1] // (2 if swiglu else 1), w.shape[2]
-    inner, width = (n, k) if transpose else (k, n)
-    _req(x, "x", shape=(x.shape[0], inner))
-    _req(w, "w", x.dtype)
-    M = _tasks(x.shape[0], offsets, x_row, out_row, "out_row")
-    _req(offsets, "offsets", torch.int32, (E + 1,))
+    E, n, k = _experts(w, swiglu, "w")
+    R, inner = _matrix(x, "x")
+    dev, dt, width = _device_of(x, "x"), x.dtype, k if transpose else n
+    M = _tasks(dev, R, x_row, out_row, "out_row")
     if out is None:
-        out = torch.empty((M, width), dtype=x.dtype, device=x.device)
-    _req(out, "out", x.dtype, (out.shape[0], width))
-    _same_device(x, w, offsets, x_row, out, out_row)
-    with torch.cuda.device(x.device):
-        _check("omni_expert_matmul", lib().omni_expert_matmul(
-            _dtype_code(x), M, E, n, k, x.shape[0], out.shape[0], _ptr(x), _ptr(x_row), _ptr(w),
-            _ptr(offsets), int(bool(transpose)), int(bool(swiglu)), _ptr(out), _ptr(out_row),
-            _stream(stream)))
+        out = torch.empty((M, width), dtype=dt, device=x.device)
+    Ro = out.shape[0]
+    _tensors(dev, (x, "x", dt, (R, n if transpose else k)), (w, "w", dt, w.shape),
+             (offsets, "offsets", torch.int32, (E + 1,)), (out, "out", dt, (Ro, width)))
+    _call("omni_expert_matmul", dev, stream, _dtype_code(x), M, E, n, k, R, Ro, x.data_ptr(),
+          _addr(x_row), w.data_ptr(), offsets.data_ptr(), 1 if transpose else 0,
+          1 if swiglu else 0, out.data_ptr(), _addr(out_row))
     return out
 
 
 def expert_weight_grad(x, dy, offsets, x_row=None, dy_row=None, dw=None, stream=None):
     """omni_expert_weight_grad: dw [E, n, k] float32, dw[e] = sum over expert e's tasks
     of dy[dy_row]^T x[x_row] (x [., k], dy [., n]; zero for experts without tasks)."""
-    E, k, n = offsets.numel() - 1, x.shape[1], dy.shape[1]
-    _req(x, "x")
-    _req(dy, "dy", x.dtype)
-    M = _tasks(x.shape[0], offsets, x_row, dy_row, "dy_row")
-    if dy_row is None and dy.shape[0] < M:
-        raise ValueError(f"{M} tasks, dy has {dy.shape[0]} rows")
+    (R, k), (Ry, n) = _matrix(x, "x"), _matrix(dy, "dy")
+    E, dev, dt = offsets.numel() - 1, _device_of(x, "x"), x.dtype
+    M = _tasks(dev, R, x_row, dy_row, "dy_row")
+    if dy_row is None and Ry < M:
+        raise ValueError(f"{M} tasks, dy has {Ry} rows")
     if dw is None:
         dw = torch.empty((E, n, k), dtype=torch.float32, device=x.device)
-    _req(dw, "dw", torch.float32, (E, n, k))
-    _same_device(x, dy, offsets, x_row, dy_row, dw)
-    with torch.cuda.device(x.device):
-        _check("omni_expert_weight_grad", lib().omni_expert_weight_grad(
-            _dtype_code(x), M, E, n, k, x.shape[0], dy.shape[0], _ptr(x), _ptr(x_row), _ptr(dy),
-            _ptr(dy_row), _ptr(offsets), _ptr(dw), _stream(stream)))
+    _tensors(dev, (x, "x", dt, (R, k)), (dy, "dy", dt, (Ry, n)),
+             (offsets, "offsets", torch.int32, (E + 1,)), (dw, "dw", torch.float32, (E, n, k)))
+    _call("omni_expert_weight_grad", dev, stream, _dtype_code(x), M, E, n, k, R, Ry,
+          x.data_ptr(), _addr(x_row), dy.data_ptr(), _addr(dy_row), offsets.data_ptr(),
+          dw.data_ptr())
     return dw
 
 
 def expert_combine(o, K, gate=None, y=None, accumulate=False, stream=None):
     """omni_expert_combine: y [L, n] float32 = (or +=) sum_k gate[t, k] o[t K + k]
     for o [L*K, n] in flatten order; gate [L, K] float32, None for ones."""
-    if K < 1 or o.shape[0] % K:
-        raise ValueError(f"o has {o.shape[0]} rows, not a multiple of K={K}")
-    L, n = o.shape[0] // K, o.shape[1]
-    _req(o, "o")
-    if gate is not None:
-        _req(gate, "gate", torch.float32, (L, K))
+    rows, n = _matrix(o, "o")
+    if K < 1 or rows % K:
+        raise ValueError(f"o has {rows} rows, not a multiple of K={K}")
+    L, dev = rows // K, _device_of(o, "o")
     if y is None:
         if accumulate:
             raise ValueError("accumulate needs y")
         y = torch.empty((L, n), dtype=torch.float32, device=o.device)
-    _req(y, "y", torch.float32, (L, n))
-    _same_device(o, gate, y)
-    with torch.cuda.device(o.device):
-        _check("omni_expert_combine", lib().omni_expert_combine(
-            _dtype_code(o), L, K, n, _ptr(o), _ptr(gate), _ptr(y), int(bool(accumulate)),
-            _stream(stream)))
+    _tensors(dev, (o, "o", o.dtype, (rows, n)), (y, "y", torch.float32, (L, n)))
+    if gate is not None:
+        _tensors(dev, (gate, "gate", torch.float32, (L, K)))
+    _call("omni_expert_combine", dev, stream, _dtype_code(o), L, K, n, o.data_ptr(), _addr(gate),
+          y.data_ptr(), 1 if accumulate else 0)
     return y
 
 
 def expert_combine_backward(o, gate, dy, do=None, dgate=None, stream=None):
     """omni_expert_combine_backward: returns (do [L*K, n] of o's type, dgate [L, K]
     float32) for dy [L, n] float32."""
-    L, K = gate.shape
-    n = dy.shape[1]
-    _req(o, "o", shape=(L * K, n))
-    _req(gate, "gate", torch.float32)
-    _req(dy, "dy", torch.float32, (L, n))
+    (L, K), n, dev = _matrix(gate, "gate"), _matrix(dy, "dy")[1], _device_of(o, "o")
     if do is None:
         do = torch.empty_like(o)
     if dgate is None:
         dgate = torch.empty_like(gate)
-    _req(do, "do", o.dtype, (L * K, n))
-    _req(dgate, "dgate", torch.float32, (L, K))
-    _same_device(o, gate, dy, do, dgate)
-    with torch.cuda.device(o.device):
-        _check("omni_expert_combine_backward", lib().omni_expert_combine_backward(
-            _dtype_code(o), L, K, n, _ptr(o), _ptr(gate), _ptr(dy), _ptr(do), _ptr(dgate),
-            _stream(stream)))
+    f32 = torch.float32
+    _tensors(dev, (o, "o", o.dtype, (L * K, n)), (gate, "gate", f32, (L, K)),
+             (dy, "dy", f32, (L, n)), (do, "do", o.dtype, (L * K, n)),
+             (dgate, "dgate", f32, (L, K)))
+    _call("omni_expert_combine_backward", dev, stream, _dtype_code(o), L, K, n, o.data_ptr(),
+          gate.data_ptr(), dy.data_ptr(), do.data_ptr(), dgate.data_ptr())
     return do, dgate
 
 
@@ -610,18 +646,15 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     """omni_quantize_rows: (q [R, k] int8, scale [R] float32), scale = max|row| / 127,
     q = row / scale to the nearest integer.  Tokens' activations, or weights by
     output channel (view [E, n, k] experts as [E*n, k])."""
-    R, k = x.shape
-    _req(x, "x")
+    (R, k), dev = _matrix(x, "x"), _device_of(x, "x")
     if q is None:
         q = torch.empty((R, k), dtype=torch.int8, device=x.device)
     if scale is None:
         scale = torch.empty(R, dtype=torch.float32, device=x.device)
-    _req(q, "q", torch.int8, (R, k))
-    _req(scale, "scale", torch.float32, (R,))
-    _same_device(x, q, scale)
-    with torch.cuda.device(x.device):
-        _check("omni_quantize_rows", lib().omni_quantize_rows(
-            _dtype_code(x), R, k, _ptr(x), _ptr(q), _ptr(scale), _stream(stream)))
+    _tensors(dev, (x, "x", x.dtype, (R, k)), (q, "q", torch.int8, (R, k)),
+             (scale, "scale", torch.float32, (R,)))
+    _call("omni_quantize_rows", dev, stream, _dtype_code(x), R, k, x.data_ptr(), q.data_ptr(),
+          scale.data_ptr())
     return q, scale
 
 
@@ -629,23 +662,19 @@ def quantized_matmul(xq, x_scale, wq, w_scale, out=None, out_dtype=torch.bfloat1
                      stream=None):
     """omni_quantized_matmul: out [M, n] = (xq wq^T) * x_scale[m] * w_scale[j] for int8
     xq [M, k], wq [n, k] (swiglu: [2n, k], out = silu(gate half) * up half)."""
-    M, k = xq.shape
-    rows = wq.shape[0]
+    (M, k), rows, dev = _matrix(xq, "xq"), _matrix(wq, "wq")[0], _device_of(xq, "xq")
     if swiglu and rows % 2:
         raise ValueError("swiglu needs an even number of weight rows")
-    n = rows // (2 if swiglu else 1)
-    _req(xq, "xq", torch.int8)
-    _req(wq, "wq", torch.int8, (rows, k))
-    _req(x_scale, "x_scale", torch.float32, (M,))
-    _req(w_scale, "w_scale", torch.float32, (rows,))
+    n = rows // 2 if swiglu else rows
     if out is None:
         out = torch.empty((M, n), dtype=out_dtype, device=xq.device)
-    _req(out, "out", shape=(M, n))
-    _same_device(xq, x_scale, wq, w_scale, out)
-    with torch.cuda.device(xq.device):
-        _check("omni_quantized_matmul", lib().omni_quantized_matmul(
-            _dtype_code(out), M, n, k, _ptr(xq), _ptr(x_scale), _ptr(wq), _ptr(w_scale),
-            int(bool(swiglu)), _ptr(out), _stream(stream)))
+    i8, f32 = torch.int8, torch.float32
+    _tensors(dev, (xq, "xq", i8, (M, k)), (wq, "wq", i8, (rows, k)),
+             (x_scale, "x_scale", f32, (M,)), (w_scale, "w_scale", f32, (rows,)),
+             (out, "out", out.dtype, (M, n)))
+    _call("omni_quantized_matmul", dev, stream, _dtype_code(out), M, n, k, xq.data_ptr(),
+          x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), 1 if swiglu else 0,
+          out.data_ptr())
     return out
 
 
@@ -653,24 +682,16 @@ def quantized_expert_matmul(xq, x_scale, wq, w_scale, offsets, x_row=None, out=N
                             out_row=None, out_dtype=torch.bfloat16, swiglu=False, stream=None):
     """omni_quantized_expert_matmul: expert_matmul over int8 rows xq [., k] with
     x_scale [.] and experts wq [E, n, k] with w_scale [E, n]."""
-    if wq.dim() != 3 or (swiglu and wq.shape[1] % 2):
-        raise ValueError("wq must be [E, n, k] ([E, 2n, k] with swiglu)")
-    E, rows, k = wq.shape
-    n = rows // (2 if swiglu else 1)
-    R = xq.shape[0]
-    _req(xq, "xq", torch.int8, (R, k))
-    _req(wq, "wq", torch.int8)
-    _req(x_scale, "x_scale", torch.float32, (R,))
-    _req(w_scale, "w_scale", torch.float32, (E, rows))
-    M = _tasks(R, offsets, x_row, out_row, "out_row")
-    _req(offsets, "offsets", torch.int32, (E + 1,))
+    E, n, k = _experts(wq, swiglu, "wq")
+    R, dev = _matrix(xq, "xq")[0], _device_of(xq, "xq")
+    M = _tasks(dev, R, x_row, out_row, "out_row")
     if out is None:
         out = torch.empty((M, n), dtype=out_dtype, device=xq.device)
-    _req(out, "out", shape=(out.shape[0], n))
-    _same_device(xq, x_scale, wq, w_scale, offsets, x_row, out, out_row)
-    with torch.cuda.device(xq.device):
-        _check("omni_quantized_expert_matmul", lib().omni_quantized_expert_matmul(
-            _dtype_code(out), M, E, n, k, R, out.shape[0], _ptr(xq), _ptr(x_scale), _ptr(x_row),
-            _ptr(wq), _ptr(w_scale), _ptr(offsets), int(bool(swiglu)), _ptr(out),
-            _ptr(out_row), _stream(stream)))
+    i8, f32, Ro = torch.int8, torch.float32, out.shape[0]
+    _tensors(dev, (xq, "xq", i8, (R, k)), (wq, "wq", i8, wq.shape),
+             (x_scale, "x_scale", f32, (R,)), (w_scale, "w_scale", f32, wq.shape[:2]),
+             (offsets, "offsets", torch.int32, (E + 1,)), (out, "out", out.dtype, (Ro, n)))
+    _call("omni_quantized_expert_matmul", dev, stream, _dtype_code(out), M, E, n, k, R, Ro,
+          xq.data_ptr(), x_scale.data_ptr(), _addr(x_row), wq.data_ptr(), w_scale.data_ptr(),
+          offsets.data_ptr(), 1 if swiglu else 0, out.data_ptr(), _addr(out_row))
     return out

@@ -91,24 +91,40 @@ __device__ __forceinline__ ExpertScan scan_experts(const int32_t* off, int E, in
   s.total = __builtin_amdgcn_readlane(s.upto, 63);
   return s;
 }
-__device__ __forceinline__ ExpertTile find_expert_tile(const ExpertScan& s, const int32_t* off,
-                                                       int E, int M, int bm, int rt) {
-  const int q = (E + kWave - 1) / kWave;
-  const uint64_t past = __ballot(s.upto > rt);
-  if (past == 0) return {0, 0, 0};
+// Tile `id` of the n_nt column tiles of every row tile.  An expert's tiles run
+// in bands of kBand column tiles, each down all its row tiles: the tiles that
+// an XCD works on at a time (32 of the largest) then form a block of about
+// kBand x kBand, whose rows and weights its L2 fetches once.
+constexpr int kBand = 6;
+struct TilePlace {
+  ExpertTile t;
+  int nt;
+};
+__device__ __forceinline__ TilePlace place_in_expert(int e, int lo, int hi, int bm, int n_nt,
+                                                     int id) {
+  const int mt = (hi - lo + bm - 1) / bm;
+  const int band = id / (mt * kBand), width = min(kBand, n_nt - band * kBand);
+  const int rest = id - band * mt * kBand, rt = rest / width;
+  return {{e, lo + rt * bm, min(hi, lo + (rt + 1) * bm)}, band * kBand + rest - rt * width};
+}
+__device__ __forceinline__ TilePlace find_tile(const ExpertScan& s, const int32_t* off, int E,
+                                               int M, int bm, int n_nt, int id) {
+  const int q = (E + kWave - 1) / kWave, row = id / n_nt;
+  const uint64_t past = __ballot(s.upto > row);
+  if (past == 0) return {{0, 0, 0}, 0};
   const int owner = __ffsll(static_cast<long long>(past)) - 1;
-  int left = rt - (__builtin_amdgcn_readlane(s.upto, owner) -
-                   __builtin_amdgcn_readlane(s.mine, owner));
+  int left = row - (__builtin_amdgcn_readlane(s.upto, owner) -
+                    __builtin_amdgcn_readlane(s.mine, owner));
   for (int i = 0; i < q; ++i) {
     const int e = owner * q + i;
     if (e >= E) break;
     int lo, hi;
     expert_range(off, e, M, lo, hi);
-    const int t = (hi - lo + bm - 1) / bm;
-    if (left < t) return {e, lo + left * bm, min(hi, lo + (left + 1) * bm)};
-    left -= t;
+    const int mt = (hi - lo + bm - 1) / bm;
+    if (left < mt) return place_in_expert(e, lo, hi, bm, n_nt, id - (row - left) * n_nt);
+    left -= mt;
   }
-  return {0, 0, 0};
+  return {{0, 0, 0}, 0};
 }
 // The expert at position pos when every run of 64 experts is put in order of
 // its task counts, most first (ties by id).
@@ -136,6 +152,15 @@ __device__ __forceinline__ int xcd_tile(int b, int total) {
 }
 __device__ __forceinline__ bool xcd_has(int b, int total) {
   return (b >> 3) < (total >> 3) + ((b & 7) < (total & 7) ? 1 : 0);
+}
+// The workgroup's tile; an empty one (m0 == m1) where there is none for it.
+__device__ __forceinline__ TilePlace my_tile(const ExpertMatmulArgs& a, int bm, int n_nt) {
+  if (!a.offsets)
+    return place_in_expert(0, 0, a.M, bm, n_nt, xcd_tile(blockIdx.x, gridDim.x));
+  const ExpertScan s = scan_experts(a.offsets, a.E, a.M, bm);
+  const int total = s.total * n_nt;
+  if (!xcd_has(blockIdx.x, total)) return {{0, 0, 0}, 0};
+  return find_tile(s, a.offsets, a.E, a.M, bm, n_nt, xcd_tile(blockIdx.x, total));
 }
 
 // ------------------------------------------------------------------ stages in LDS
@@ -244,7 +269,7 @@ __device__ __forceinline__ typename Op::Frag frag_strided(const uint8_t* st, int
 // reads are issued between the MFMAs, one row of tiles at a time: issued
 // together after the barrier they fill the load and LDS queues, and a wave
 // that waits for room there issues no MFMA.
-//   issue(kt, u, may_end): load u of stage kt; may_end: it may be the last
+//   issue(kt, u, may_end): load u of stage kt; may_end: it or the next may be the last
 //   read_p(kt, i), read_q(kt, j): fragments of stage kt
 // The steady loop has no branch between a read and the MFMAs that use it: a
 // join there makes the compiler wait for the reads just issued.
@@ -303,7 +328,7 @@ __device__ __forceinline__ void run_pipeline(int nk, Issue issue, ReadP read_p, 
 #pragma unroll
   for (int i = 0; i < TI; ++i) p0[i] = read_p(0, i);
   int kt = 0;
-  for (; kt + S + 2 < nk; kt += 2) {
+  for (; kt + S + 3 < nk; kt += 2) {
     steady(kt, p0, q0, p1, q1);
     steady(kt + 1, p1, q1, p0, q0);
   }
@@ -371,20 +396,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
   const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
   const int K = QT ? a.n : a.k, N = QT ? a.k : a.n;
   const int n_nt = (N + BNO - 1) / BNO;
-  ExpertTile t;
-  int n0;
-  if (a.offsets) {
-    const ExpertScan sc = scan_experts(a.offsets, a.E, a.M, BM);
-    const int total = sc.total * n_nt;
-    if (!xcd_has(blockIdx.x, total)) return;
-    const int id = xcd_tile(blockIdx.x, total), rt = id / n_nt;
-    n0 = (id - rt * n_nt) * BNO;
-    t = find_expert_tile(sc, a.offsets, a.E, a.M, BM, rt);
-  } else {
-    const int id = xcd_tile(blockIdx.x, gridDim.x), rt = id / n_nt;
-    n0 = (id - rt * n_nt) * BNO;
-    t = {0, rt * BM, min(a.M, (rt + 1) * BM)};
-  }
+  const TilePlace at = my_tile(a, BM, n_nt);
+  const ExpertTile t = at.t;
+  const int n0 = at.nt * BNO;
   if (t.m0 >= t.m1) return;
   const uint8_t* x = static_cast<const uint8_t*>(a.x);
   const uint8_t* w = static_cast<const uint8_t*>(a.w) +
@@ -410,7 +424,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
   for (int u = 0; u < IQ; ++u) {
     if constexpr (QT) {
       constexpr int CPR = BN * Op::kBytes / 16;  // chunks per step
-      const int at = (wv * IQ + u) * 64 + l, kk = at / CPR, c = (at % CPR) ^ swz_t<Op>(kk);
+      const int o = (wv * IQ + u) * 64 + l, kk = o / CPR, c = (o % CPR) ^ swz_t<Op>(kk);
       const int col = n0 + c * (16 / Op::kBytes);
       qc[u] = kk;
       qsrc[u] = w + (static_cast<size_t>(kk) * N + (col < N ? col : 0)) * Op::kBytes;
@@ -450,11 +464,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
   };
   auto read_q = [&](int kt, int j) {
     const uint8_t* st = smem + (kt % S) * STAGE + BM * 64;
-    const int at = wn * (BN / WN);
+    const int c = wn * (BN / WN);
     if constexpr (QT)
-      return frag_strided<Op, BN>(st, at + j * 16, l);
+      return frag_strided<Op, BN>(st, c + j * 16, l);
     else
-      return frag_rows<Op, true>(st, at + (j >> 1) * 32 + (j & 1) * 4 + (fr >> 2) * 8 + (fr & 3),
+      return frag_rows<Op, true>(st, c + (j >> 1) * 32 + (j & 1) * 4 + (fr >> 2) * 8 + (fr & 3),
                                  g);
   };
   Acc acc[TI][TJ] = {};
@@ -573,21 +587,23 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
   auto task = [&](int kt, int r) {
     return lo + kt * KE + (r < NP ? wv * NP + r : wv * NQ + r - NP);
   };
-  auto fetch_rows = [&](int kt) {
+  // may_end: the stage may reach past the expert's last task (or the lists' end)
+  auto fetch_rows = [&](int kt, bool may_end) {
 #pragma unroll
     for (int r = 0; r < NP + NQ; ++r) {
-      const int m = min(task(kt, r), a.M - 1);
+      const int m = may_end ? min(task(kt, r), a.M - 1) : task(kt, r);
       raw_y[r] = yl[a.dy_row ? m : 0];
       raw_x[r] = xl[a.x_row ? m : 0];
     }
   };
-  auto check_rows = [&](int kt) {
+  auto check_rows = [&](int kt, bool may_end) {
 #pragma unroll
     for (int r = 0; r < NP + NQ; ++r) {
       const int m = task(kt, r);
       const int ry = a.dy_row ? raw_y[r] : m, rx = a.x_row ? raw_x[r] : m;
-      const bool ok = m < hi && static_cast<unsigned>(ry) < static_cast<unsigned>(a.Ry) &&
-                      static_cast<unsigned>(rx) < static_cast<unsigned>(a.R);
+      const bool ok = (static_cast<unsigned>(ry) < static_cast<unsigned>(a.Ry)) &
+                      (static_cast<unsigned>(rx) < static_cast<unsigned>(a.R)) &
+                      (!may_end | (m < hi));
       if (r < NP) prow[r] = ok ? ry : -1;
       if (NQ == 0) qrow[r] = ok ? rx : -1;
       else if (r >= NP) qrow[r - NP] = ok ? rx : -1;
@@ -599,11 +615,11 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
     const void* src = m + (static_cast<size_t>(row) * width + (col < width ? col : 0)) * Op::kBytes;
     load_lds16(row < 0 ? kZeroChunk : src, dst);
   };
-  auto issue = [&](int kt, int u, bool) {
+  auto issue = [&](int kt, int u, bool may_end) {
     const uint32_t st = ring + (kt % S) * STAGE;
     if (u == 0) {
-      check_rows(kt);
-      fetch_rows(kt + 1);
+      check_rows(kt, may_end);
+      fetch_rows(kt + 1, may_end);
     }
     if (u < IP) {
       const int sub = l / PCPR, kk = (wv * IP + u) * PR + sub;
@@ -631,7 +647,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
   };
   Acc acc[TI][TJ] = {};
   if (nk > 0) {
-    fetch_rows(0);
+    fetch_rows(0, true);
     run_pipeline<Op, IP + IQ, S>(nk, issue, read_p, read_q, acc);
   }
 #pragma unroll
@@ -651,36 +667,27 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
 
 // ------------------------------------------------------------------ few rows per expert
 
-// 16 tasks x 16 CT columns per workgroup, the contraction split over its KS
-// waves: both operands go from memory to the MFMA's registers, U stages ahead,
-// and the waves' sums are added through LDS in wave order.
-template <class Op, typename TO, bool SWIGLU, int RT, int KS, int U>
+// 16 RT tasks x 16 CT rows of W per workgroup, the contraction split over its
+// KS waves: both operands go from memory to the MFMA's registers, U stages of
+// 64 bytes ahead, and the waves' sums are added through LDS in wave order.
+// SWIGLU: the first CT / 2 column tiles are gate rows, the others their up rows.
+template <class Op, typename TO, bool SWIGLU, int RT, int CT, int KS, int U>
 __global__ __launch_bounds__(KS * 64) void expert_rows_kernel(ExpertMatmulArgs a) {
   using Frag = typename Op::Frag;
   using Acc = typename Op::Acc;
-  constexpr int BM = 16 * RT, CT = SWIGLU ? 2 : 1;  // Q tiles: gate and up
+  constexpr int BM = 16 * RT, H = SWIGLU ? 2 : 1, CO = CT / H, BNO = 16 * CO;
+  static_assert(CT % H == 0, "gate and up tiles in pairs");
   __shared__ __attribute__((aligned(16))) Acc part[KS][RT * CT][64];
   const int wv = threadIdx.x >> 6, l = threadIdx.x & 63, fr = l & 15, g = l >> 4;
   const int K = a.k, N = a.n;
-  const int n_nt = (N + 15) / 16;
-  ExpertTile t;
-  int n0;
-  if (a.offsets) {
-    const ExpertScan sc = scan_experts(a.offsets, a.E, a.M, BM);
-    const int total = sc.total * n_nt;
-    if (!xcd_has(blockIdx.x, total)) return;
-    const int id = xcd_tile(blockIdx.x, total), rt = id / n_nt;
-    n0 = (id - rt * n_nt) * 16;
-    t = find_expert_tile(sc, a.offsets, a.E, a.M, BM, rt);
-  } else {
-    const int id = xcd_tile(blockIdx.x, gridDim.x), rt = id / n_nt;
-    n0 = (id - rt * n_nt) * 16;
-    t = {0, rt * BM, min(a.M, (rt + 1) * BM)};
-  }
+  const int n_nt = (N + BNO - 1) / BNO;
+  const TilePlace at = my_tile(a, BM, n_nt);
+  const ExpertTile t = at.t;
+  const int n0 = at.nt * BNO;
   if (t.m0 >= t.m1) return;
   const size_t row_bytes = static_cast<size_t>(K) * Op::kBytes;
   const uint8_t* w = static_cast<const uint8_t*>(a.w) +
-                     static_cast<size_t>(t.e) * CT * N * row_bytes;
+                     static_cast<size_t>(t.e) * H * N * row_bytes;
   const uint8_t* psrc[RT];
   const uint8_t* qsrc[CT];
 #pragma unroll
@@ -690,8 +697,9 @@ __global__ __launch_bounds__(KS * 64) void expert_rows_kernel(ExpertMatmulArgs a
     psrc[i] = static_cast<const uint8_t*>(a.x) + row * row_bytes + g * 16;
   }
 #pragma unroll
-  for (int h = 0; h < CT; ++h)
-    qsrc[h] = w + (min(n0 + fr, N - 1) + static_cast<size_t>(h) * N) * row_bytes + g * 16;
+  for (int j = 0; j < CT; ++j)
+    qsrc[j] = w + (min(n0 + j % CO * 16 + fr, N - 1) + static_cast<size_t>(j / CO) * N) * row_bytes +
+              g * 16;
 
   // chunks of 16 bytes; this wave's stages are [kb, ke)
   const int chunks = static_cast<int>(row_bytes / 16), nk = (chunks + 3) / 4;
@@ -708,7 +716,7 @@ __global__ __launch_bounds__(KS * 64) void expert_rows_kernel(ExpertMatmulArgs a
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int h = 0; h < CT; ++h) q[u][h] = fetch(qsrc[h], k0 + u);
+      for (int j = 0; j < CT; ++j) q[u][j] = fetch(qsrc[j], k0 + u);
 #pragma unroll
       for (int i = 0; i < RT; ++i) p[u][i] = fetch(psrc[i], k0 + u);
     }
@@ -717,22 +725,23 @@ __global__ __launch_bounds__(KS * 64) void expert_rows_kernel(ExpertMatmulArgs a
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int h = 0; h < CT; ++h) Op::mma(acc[i][h], q[u][h], p[u][i]);
+        for (int j = 0; j < CT; ++j) Op::mma(acc[i][j], q[u][j], p[u][i]);
   }
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int h = 0; h < CT; ++h) part[wv][i * CT + h][l] = acc[i][h];
+    for (int j = 0; j < CT; ++j) part[wv][i * CT + j][l] = acc[i][j];
   __syncthreads();
-  // wave wv finishes row tiles wv, wv + KS, ...
+  // the output tiles are finished by the waves in turn
   TO* out = static_cast<TO*>(a.out);
   const bool aligned = (N * sizeof(TO)) % 16 == 0;
-  for (int i = wv; i < RT; i += KS) {
-    Acc s[CT];
+  for (int o = wv; o < RT * CO; o += KS) {
+    const int i = o / CO, j = o % CO, c0 = n0 + j * 16 + g * 4;
+    Acc s[H];
 #pragma unroll
-    for (int h = 0; h < CT; ++h) {
-      s[h] = part[0][i * CT + h][l];
-      for (int z = 1; z < KS; ++z) s[h] += part[z][i * CT + h][l];
+    for (int h = 0; h < H; ++h) {
+      s[h] = part[0][i * CT + h * CO + j][l];
+      for (int z = 1; z < KS; ++z) s[h] += part[z][i * CT + h * CO + j][l];
     }
     const int m = t.m0 + i * 16 + fr;
     if (m >= t.m1) continue;
@@ -742,19 +751,17 @@ __global__ __launch_bounds__(KS * 64) void expert_rows_kernel(ExpertMatmulArgs a
     float v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float z[CT];
+      float z[H];
 #pragma unroll
-      for (int h = 0; h < CT; ++h) {
+      for (int h = 0; h < H; ++h) {
         z[h] = in ? static_cast<float>(s[h][q]) : 0.f;
-        if constexpr (Op::kBytes == 1) {
-          const int c = min(n0 + g * 4 + q, N - 1);
+        if constexpr (Op::kBytes == 1)
           z[h] = z[h] * (in ? a.x_scale[xr] : 0.f) *
-                 a.w_scale[static_cast<size_t>(t.e) * CT * N + static_cast<size_t>(h) * N + c];
-        }
+                 a.w_scale[(static_cast<size_t>(t.e) * H + h) * N + min(c0 + q, N - 1)];
       }
-      v[q] = SWIGLU ? silu_mul(z[0], z[CT - 1]) : z[0];
+      v[q] = SWIGLU ? silu_mul(z[0], z[H - 1]) : z[0];
     }
-    store_cols(out + static_cast<size_t>(row) * N, n0 + g * 4, N, aligned, v);
+    store_cols(out + static_cast<size_t>(row) * N, c0, N, aligned, v);
   }
 }
 
@@ -785,29 +792,73 @@ static hipError_t run_tiles(const ExpertMatmulArgs& a, hipStream_t s) {
   expert_product_kernel<Op, TO, QT, SW, BM, BN, WM, WN, S><<<nb, WM * WN * 64, 0, s>>>(a);
   return hipGetLastError();
 }
-template <class Op, typename TO, bool SW, int RT, int KS, int U>
+template <class Op, typename TO, bool SW, int RT, int CT, int KS, int U>
 static hipError_t run_rows(const ExpertMatmulArgs& a, hipStream_t s) {
-  const unsigned nb = static_cast<unsigned>(product_blocks(a, RT * 16, 16));
-  expert_rows_kernel<Op, TO, SW, RT, KS, U><<<nb, KS * 64, 0, s>>>(a);
+  const unsigned nb = static_cast<unsigned>(product_blocks(a, RT * 16, SW ? CT * 8 : CT * 16));
+  expert_rows_kernel<Op, TO, SW, RT, CT, KS, U><<<nb, KS * 64, 0, s>>>(a);
   return hipGetLastError();
 }
-// By the mean number of rows r of an expert that has tasks, and by the number
-// of tiles.  Measured with 64 experts, 2 x 704 outputs, 2048 inputs, bf16 (us):
-//   r           1     4     8    32    64   128   256   512
-//   16 rows    44    74    83   167   279   512   980  1914
-//   64 x 128   49    75    78    85   102   139   212   367
-//   128 x 128  51    78    81    89   100   117   181   290
-//   256 x 256  55   103   105   109   119   127   173   255
+// Tiles to expect: an expert's last row tile is half full on average.
+static double expected_tiles(const ExpertMatmulArgs& a, int bm, int bno) {
+  const int used = a.E < a.M ? a.E : a.M, N = a.transpose ? a.k : a.n;
+  const int rt = used == 1 ? (a.M + bm - 1) / bm
+                           : static_cast<int>((a.M + static_cast<long long>(used) * (bm / 2)) / bm);
+  return static_cast<double>(rt > used ? rt : used) * ((N + bno - 1) / bno);
+}
+// Which tile, for bf16 and int8: the one whose tiles take the least time,
+// in units of one round of 256 x 256 tiles (one per CU).  A 128 x 256 tile is
+// alone on a CU as well, of the two smaller ones two and three share one; a
+// large tile needs less LDS and L2 traffic per MFMA, a small one wastes less
+// where there are few tiles or few rows.  Fitted to (us, 2048 inputs):
+//   tiles of 256 x 256       64 (int8)  128 (int8)  80    144   1700
+//   256 x 256                30         32          28    29    407
+//   128 x 256                21         25          20    36    499
+//   128 x 128                17         27          22    32    503
+//   64 x 128                 19         32          23    34    712
+struct TileCosts {
+  double big, wide, mid, small;
+};
+static TileCosts tile_costs(const ExpertMatmulArgs& a, int swiglu) {
+  const int h = swiglu ? 2 : 1;
+  const double t1 = expected_tiles(a, 256, 256 / h), t2 = expected_tiles(a, 128, 256 / h),
+               t4 = expected_tiles(a, 128, 128 / h), t5 = expected_tiles(a, 64, 128 / h);
+  auto rounds = [](double t) { return t <= 1024 ? static_cast<int>((t + 255) / 256) : t / 256; };
+  TileCosts c;
+  c.big = rounds(t1);
+  c.wide = t2 <= 768 ? 0.72 * rounds(t2) : 0.61 * t2 / 256 + 0.3;
+  c.mid = t4 <= 256 ? 0.55 : t4 <= 512 ? 0.83 : 0.62 * t4 / 512 + 0.3;
+  c.small = t5 <= 256 ? 0.46 : 0.55 * t5 / 768 + 0.35;
+  return c;
+}
 template <class Op, typename TO, bool QT, bool SW>
 static hipError_t pick(const ExpertMatmulArgs& a, hipStream_t s) {
-  const int r = a.M / (a.E < a.M ? a.E : a.M);
-  const int bno = SW ? 128 : 256;
-  if constexpr (!QT)
-    if (r <= 4 || product_blocks(a, 64, bno / 2) < 64) return run_rows<Op, TO, SW, 1, 8, 4>(a, s);
-  if (r >= 192 && product_blocks(a, 256, bno) >= 192)
-    return run_tiles<Op, TO, QT, SW, 256, 256, 2, 4, 4>(a, s);
-  if (r >= 64 && product_blocks(a, 128, bno / 2) >= 192)
-    return run_tiles<Op, TO, QT, SW, 128, 128, 2, 2, 4>(a, s);
+  const int r = a.M / (a.E < a.M ? a.E : a.M);  // mean rows of an expert with tasks
+  if constexpr (!QT) {
+    // Few rows, or so few tiles that most CUs would idle (us; rows kernel with
+    // 16, 32 and 64 rows against 64 x 128 tiles):
+    //   64 experts, 1408 outputs, 2048 inputs, 1 / 4 / 8 rows    44 74 90 / 54 75 79
+    //   1 expert, 2048 outputs, 2048 inputs, 16 / 128 / 512      7.5 12.6 34 / 14 16 18
+    //   4 experts, 512 outputs, 1024 inputs, 8 / 64 / 256        5.5 8.0 16 / 9.5 10 11
+    //   16 experts, 1024 outputs, 1024 inputs, f32, 8 / 16 / 64  23 29 56 / 40 39 41
+    const double t5 = expected_tiles(a, 64, SW ? 64 : 128);
+    constexpr int C1 = SW ? 2 : 1;
+    if (t5 < (Op::kBytes == 4 ? 96 : 48)) {
+      if (r <= 32) return run_rows<Op, TO, SW, 1, C1, 8, 4>(a, s);
+      if (r <= 128) return run_rows<Op, TO, SW, 2, 2, 8, 4>(a, s);
+      return run_rows<Op, TO, SW, 4, 2, 8, 2>(a, s);
+    }
+    if (r <= (Op::kBytes == 4 ? 16 : t5 < 256 ? 8 : 2))
+      return run_rows<Op, TO, SW, 1, C1, 8, 4>(a, s);
+  }
+  // float32 is bound by its MFMAs at any tile: the small one balances best
+  if constexpr (Op::kBytes != 4) {
+    const TileCosts c = tile_costs(a, SW);
+    if (c.big <= c.wide && c.big <= c.mid && c.big <= c.small)
+      return run_tiles<Op, TO, QT, SW, 256, 256, 2, 4, 4>(a, s);
+    if (c.wide <= c.mid && c.wide <= c.small)
+      return run_tiles<Op, TO, QT, SW, 128, 256, 2, 4, 4>(a, s);
+    if (c.mid <= c.small) return run_tiles<Op, TO, QT, SW, 128, 128, 2, 2, 4>(a, s);
+  }
   return run_tiles<Op, TO, QT, SW, 64, 128, 2, 2, 4>(a, s);
 }
 template <class Op, typename TO>
