@@ -31,7 +31,8 @@ EXPORTS = (
     "omni_routed_backward", "omni_shared_mlp_workspace", "omni_shared_mlp",
     "omni_atomic_forward_glu", "omni_flat_router_workspace", "omni_flat_router_topk",
     "omni_product_topk_static",
-    "omni_expert_matmul", "omni_expert_weight_grad", "omni_expert_combine",
+    "omni_expert_matmul", "omni_expert_weight_grad_workspace", "omni_expert_weight_grad",
+    "omni_expert_combine",
     "omni_expert_combine_backward", "omni_quantize_rows", "omni_quantized_matmul",
     "omni_quantized_expert_matmul",
 )
@@ -77,7 +78,8 @@ _SIGS = {
     "omni_atomic_forward_glu": (_i, [_i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp,
                                      ctypes.POINTER(ScheduleStruct), _vp, _i, _vp, _sz, _vp]),
     "omni_expert_matmul": (_i, [_i] * 7 + [_vp] * 4 + [_i, _i] + [_vp] * 3),
-    "omni_expert_weight_grad": (_i, [_i] * 7 + [_vp] * 7),
+    "omni_expert_weight_grad_workspace": (_sz, [_i] * 5),
+    "omni_expert_weight_grad": (_i, [_i] * 7 + [_vp] * 7 + [_sz, _vp]),
     "omni_expert_combine": (_i, [_i] * 4 + [_vp] * 3 + [_i, _vp]),
     "omni_expert_combine_backward": (_i, [_i] * 4 + [_vp] * 6),
     "omni_quantize_rows": (_i, [_i] * 3 + [_vp] * 4),
@@ -533,6 +535,14 @@ def _call(fn, dev, stream, *args):
         _check(fn, code)
 
 
+def _empty(shape, dtype, like, stream):
+    """A fresh tensor, of the memory pool of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -578,7 +588,7 @@ def expert_matmul(x, w, offsets, x_row=None, out=None, out_row=None, transpose=F
     dev, dt, width = _device_of(x, "x"), x.dtype, k if transpose else n
     M = _tasks(dev, R, x_row, out_row, "out_row")
     if out is None:
-        out = torch.empty((M, width), dtype=dt, device=x.device)
+        out = _empty((M, width), dt, x, stream)
     Ro = out.shape[0]
     _tensors(dev, (x, "x", dt, (R, n if transpose else k)), (w, "w", dt, w.shape),
              (offsets, "offsets", torch.int32, (E + 1,)), (out, "out", dt, (Ro, width)))
@@ -588,7 +598,8 @@ def expert_matmul(x, w, offsets, x_row=None, out=None, out_row=None, transpose=F
     return out
 
 
-def expert_weight_grad(x, dy, offsets, x_row=None, dy_row=None, dw=None, stream=None):
+def expert_weight_grad(x, dy, offsets, x_row=None, dy_row=None, dw=None, workspace=None,
+                       stream=None):
     """omni_expert_weight_grad: dw [E, n, k] float32, dw[e] = sum over expert e's tasks
     of dy[dy_row]^T x[x_row] (x [., k], dy [., n]; zero for experts without tasks)."""
     (R, k), (Ry, n) = _matrix(x, "x"), _matrix(dy, "dy")
@@ -597,12 +608,17 @@ def expert_weight_grad(x, dy, offsets, x_row=None, dy_row=None, dw=None, stream=
     if dy_row is None and Ry < M:
         raise ValueError(f"{M} tasks, dy has {Ry} rows")
     if dw is None:
-        dw = torch.empty((E, n, k), dtype=torch.float32, device=x.device)
+        dw = _empty((E, n, k), torch.float32, x, stream)
     _tensors(dev, (x, "x", dt, (R, k)), (dy, "dy", dt, (Ry, n)),
              (offsets, "offsets", torch.int32, (E + 1,)), (dw, "dw", torch.float32, (E, n, k)))
-    _call("omni_expert_weight_grad", dev, stream, _dtype_code(x), M, E, n, k, R, Ry,
-          x.data_ptr(), _addr(x_row), dy.data_ptr(), _addr(dy_row), offsets.data_ptr(),
-          dw.data_ptr())
+    code = _dtype_code(x)
+    nws = lib().omni_expert_weight_grad_workspace(code, M, E, n, k)
+    ws = workspace
+    if nws and (ws is None or ws.numel() < nws):
+        ws = _empty(nws, torch.uint8, x, stream)
+    _call("omni_expert_weight_grad", dev, stream, code, M, E, n, k, R, Ry, x.data_ptr(),
+          _addr(x_row), dy.data_ptr(), _addr(dy_row), offsets.data_ptr(), dw.data_ptr(),
+          _addr(ws) if nws else None, nws)
     return dw
 
 
@@ -616,7 +632,7 @@ def expert_combine(o, K, gate=None, y=None, accumulate=False, stream=None):
     if y is None:
         if accumulate:
             raise ValueError("accumulate needs y")
-        y = torch.empty((L, n), dtype=torch.float32, device=o.device)
+        y = _empty((L, n), torch.float32, o, stream)
     _tensors(dev, (o, "o", o.dtype, (rows, n)), (y, "y", torch.float32, (L, n)))
     if gate is not None:
         _tensors(dev, (gate, "gate", torch.float32, (L, K)))
@@ -630,9 +646,9 @@ def expert_combine_backward(o, gate, dy, do=None, dgate=None, stream=None):
     float32) for dy [L, n] float32."""
     (L, K), n, dev = _matrix(gate, "gate"), _matrix(dy, "dy")[1], _device_of(o, "o")
     if do is None:
-        do = torch.empty_like(o)
+        do = _empty(o.shape, o.dtype, o, stream)
     if dgate is None:
-        dgate = torch.empty_like(gate)
+        dgate = _empty((L, K), torch.float32, o, stream)
     f32 = torch.float32
     _tensors(dev, (o, "o", o.dtype, (L * K, n)), (gate, "gate", f32, (L, K)),
              (dy, "dy", f32, (L, n)), (do, "do", o.dtype, (L * K, n)),
@@ -648,9 +664,9 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     output channel (view [E, n, k] experts as [E*n, k])."""
     (R, k), dev = _matrix(x, "x"), _device_of(x, "x")
     if q is None:
-        q = torch.empty((R, k), dtype=torch.int8, device=x.device)
+        q = _empty((R, k), torch.int8, x, stream)
     if scale is None:
-        scale = torch.empty(R, dtype=torch.float32, device=x.device)
+        scale = _empty(R, torch.float32, x, stream)
     _tensors(dev, (x, "x", x.dtype, (R, k)), (q, "q", torch.int8, (R, k)),
              (scale, "scale", torch.float32, (R,)))
     _call("omni_quantize_rows", dev, stream, _dtype_code(x), R, k, x.data_ptr(), q.data_ptr(),
@@ -667,7 +683,7 @@ def quantized_matmul(xq, x_scale, wq, w_scale, out=None, out_dtype=torch.bfloat1
         raise ValueError("swiglu needs an even number of weight rows")
     n = rows // 2 if swiglu else rows
     if out is None:
-        out = torch.empty((M, n), dtype=out_dtype, device=xq.device)
+        out = _empty((M, n), out_dtype, xq, stream)
     i8, f32 = torch.int8, torch.float32
     _tensors(dev, (xq, "xq", i8, (M, k)), (wq, "wq", i8, (rows, k)),
              (x_scale, "x_scale", f32, (M,)), (w_scale, "w_scale", f32, (rows,)),
@@ -686,7 +702,7 @@ def quantized_expert_matmul(xq, x_scale, wq, w_scale, offsets, x_row=None, out=N
     R, dev = _matrix(xq, "xq")[0], _device_of(xq, "xq")
     M = _tasks(dev, R, x_row, out_row, "out_row")
     if out is None:
-        out = torch.empty((M, n), dtype=out_dtype, device=xq.device)
+        out = _empty((M, n), out_dtype, xq, stream)
     i8, f32, Ro = torch.int8, torch.float32, out.shape[0]
     _tensors(dev, (xq, "xq", i8, (R, k)), (wq, "wq", i8, wq.shape),
              (x_scale, "x_scale", f32, (R,)), (w_scale, "w_scale", f32, wq.shape[:2]),

@@ -455,10 +455,16 @@ omni_status omni_expert_matmul(omni_dtype dt, int M, int E, int n, int k, int R,
   return expert_product(a, unit, unit, act, stream);
 }
 
+size_t omni_expert_weight_grad_workspace(omni_dtype dt, int M, int E, int n, int k) {
+  if (dt != OMNI_F32 && dt != OMNI_BF16) return 0;
+  if (M < 0 || E < 1 || n < 1 || k < 1) return 0;
+  return omni::expert_wgrad_ws_bytes(dt == OMNI_BF16, M, E, n, k);
+}
+
 omni_status omni_expert_weight_grad(omni_dtype dt, int M, int E, int n, int k, int R, int Ry,
                                     const void* x, const int32_t* x_row, const void* dy,
                                     const int32_t* dy_row, const int32_t* offsets, float* dw,
-                                    hipStream_t stream) {
+                                    void* ws, size_t ws_bytes, hipStream_t stream) {
   if (dt != OMNI_F32 && dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
   if (M < 0 || E < 1 || n < 1 || k < 1 || R < 0 || Ry < 0) return OMNI_ERR_INVALID_ARG;
   if (!offsets || !dw || !aligned16(dw)) return OMNI_ERR_INVALID_ARG;
@@ -466,10 +472,12 @@ omni_status omni_expert_weight_grad(omni_dtype dt, int M, int E, int n, int k, i
   if ((!x_row && R < M) || (!dy_row && Ry < M)) return OMNI_ERR_INVALID_ARG;
   const int unit = dt == OMNI_BF16 ? 8 : 4;
   if (n % unit != 0 || k % unit != 0) return OMNI_ERR_UNSUPPORTED;
-  const omni::ExpertWgradArgs a = {dt == OMNI_BF16, M, E, n, k, R, Ry, x, x_row, dy, dy_row,
-                                   offsets, dw};
+  const omni::ExpertWgradArgs a = {dt == OMNI_BF16, M,       E,  n, k,      R, Ry, x, x_row, dy,
+                                   dy_row,          offsets, dw, 0, 0, nullptr};
   if (!omni::expert_wgrad_grid_fits(a)) return OMNI_ERR_UNSUPPORTED;
-  return hip_status(omni::launch_expert_wgrad(a, stream));
+  const size_t need = omni_expert_weight_grad_workspace(dt, M, E, n, k);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned256(ws))) return OMNI_ERR_WORKSPACE;
+  return hip_status(omni::launch_expert_wgrad(a, static_cast<float*>(ws), stream));
 }
 
 static omni_status combine_args(omni_dtype dt, int L, int K, int n) {

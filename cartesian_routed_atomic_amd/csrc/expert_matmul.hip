@@ -180,9 +180,14 @@ __device__ __forceinline__ int swz_q(int r) { return ((r >> 1) & 1) | ((r >> 2) 
 // bf16: the eight steps 0-3, 8-11 that half a transposing read takes at once
 // land on eight 32-byte slots; float32: the steps 4 g + j of a read on four
 // 64-byte slots.
-template <class Op>
-__device__ __forceinline__ int swz_t(int kk) {
-  return Op::kBytes == 2 ? ((kk & 3) | ((kk >> 1) & 4)) << 1 : kk & 12;
+// (64 bf16 columns are 128 bytes: the step's lowest bit then picks a half of
+// the 256-byte bank window by itself.)
+template <class Op, int COLS>
+__device__ __forceinline__ int swz_cols(int kk) {
+  static_assert(COLS * Op::kBytes >= 128 && (Op::kBytes == 2 || COLS >= 64), "row length");
+  if (Op::kBytes == 4) return kk & 12;
+  if (COLS == 64) return (((kk >> 1) & 1) | ((kk >> 2) & 2)) << 1;
+  return ((kk & 3) | ((kk >> 1) & 4)) << 1;
 }
 
 template <int N>
@@ -227,38 +232,39 @@ __device__ __forceinline__ typename Op::Frag frag_rows(const uint8_t* st, int r,
       st + r * 64 + ((g ^ (Q ? swz_q(r) : swz_p(r))) << 4));
 }
 // fragment of a strided stage: columns c0 .. c0 + 15, this lane's steps
-template <int COLS>
+// (rows of COLS elements, ROW bytes apart)
+template <int COLS, int ROW>
 __device__ __forceinline__ bf16x8 frag_cols_bf16(const uint8_t* st, int c0, int l) {
   // a transposing read: lane 4 r + c of 16 names the 8 bytes of step r,
   // columns 4 c .. 4 c + 3, lane i receives the four steps of column i
   const int i = l & 15, g = l >> 4;
-  s16x4 h[2];
+  s16x4 v[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int kk = g * 8 + u * 4 + (i >> 2);
     const int chunk = (c0 >> 3) + ((i & 3) >> 1);
-    const uint8_t* p = st + kk * (COLS * 2) + ((chunk ^ swz_t<Bf16Op>(kk)) << 4) + (i & 1) * 8;
-    h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+    const uint8_t* p = st + kk * ROW + ((chunk ^ swz_cols<Bf16Op, COLS>(kk)) << 4) + (i & 1) * 8;
+    v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         (__attribute__((address_space(3))) s16x4*)(p));
   }
-  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
-template <int COLS>
+template <int COLS, int ROW>
 __device__ __forceinline__ f32x4 frag_cols_f32(const uint8_t* st, int c0, int l) {
   const int c = c0 + (l & 15), g = l >> 4;
   f32x4 v;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int kk = 4 * g + j;
-    v[j] = *reinterpret_cast<const float*>(st + kk * (COLS * 4) + (((c >> 2) ^ swz_t<F32Op>(kk)) << 4) +
-                                           (c & 3) * 4);
+    v[j] = *reinterpret_cast<const float*>(
+        st + kk * ROW + (((c >> 2) ^ swz_cols<F32Op, COLS>(kk)) << 4) + (c & 3) * 4);
   }
   return v;
 }
-template <class Op, int COLS>
+template <class Op, int COLS, int ROW>
 __device__ __forceinline__ typename Op::Frag frag_strided(const uint8_t* st, int c0, int l) {
-  if constexpr (Op::kBytes == 2) return frag_cols_bf16<COLS>(st, c0, l);
-  else return frag_cols_f32<COLS>(st, c0, l);
+  if constexpr (Op::kBytes == 2) return frag_cols_bf16<COLS, ROW>(st, c0, l);
+  else return frag_cols_f32<COLS, ROW>(st, c0, l);
 }
 
 // The pipeline of a tile: a ring of S stages in LDS, filled by direct
@@ -424,7 +430,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
   for (int u = 0; u < IQ; ++u) {
     if constexpr (QT) {
       constexpr int CPR = BN * Op::kBytes / 16;  // chunks per step
-      const int o = (wv * IQ + u) * 64 + l, kk = o / CPR, c = (o % CPR) ^ swz_t<Op>(kk);
+      const int o = (wv * IQ + u) * 64 + l, kk = o / CPR, c = (o % CPR) ^ swz_cols<Op, BN>(kk);
       const int col = n0 + c * (16 / Op::kBytes);
       qc[u] = kk;
       qsrc[u] = w + (static_cast<size_t>(kk) * N + (col < N ? col : 0)) * Op::kBytes;
@@ -466,7 +472,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
     const uint8_t* st = smem + (kt % S) * STAGE + BM * 64;
     const int c = wn * (BN / WN);
     if constexpr (QT)
-      return frag_strided<Op, BN>(st, c + j * 16, l);
+      return frag_strided<Op, BN, BN * Op::kBytes>(st, c + j * 16, l);
     else
       return frag_rows<Op, true>(st, c + (j >> 1) * 32 + (j & 1) * 4 + (fr >> 2) * 8 + (fr & 3),
                                  g);
@@ -542,119 +548,163 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
 
 // ------------------------------------------------------------------ the weight gradient
 
+// Where a workgroup's sum goes: dW itself, or a partial sum of one part of the
+// expert's tasks (experts with more tasks than a part has are cut into parts).
+struct WgradPart {
+  int e, lo, hi;
+  int slot;  // partial sum, -1: dW
+};
+// Slots of the experts in several parts come one after the other, by id.
+__device__ __forceinline__ int parts_of(int count, int part) {
+  return (count + part - 1) / part;
+}
+// first partial slot of expert e
+__device__ __forceinline__ int first_slot(const int32_t* off, int E, int M, int part, int e) {
+  const int l = lane(), q = (E + kWave - 1) / kWave;
+  int before = 0;  // slots of this lane's experts below e
+  for (int i = 0; i < q; ++i) {
+    const int f = l * q + i;
+    if (f < e) {
+      int lo, hi;
+      expert_range(off, f, M, lo, hi);
+      const int n = parts_of(hi - lo, part);
+      before += n > 1 ? n : 0;
+    }
+  }
+  return __builtin_amdgcn_readlane(wave_prefix_sum(before), 63);
+}
+
 // Tile BM output features (columns of dy) x BN inputs (columns of x) of one
 // expert; the contraction runs over its tasks in order, whose rows of dy and x
-// are gathered by the same ring of direct loads.  The row numbers of a stage
-// are read one stage ahead through scalar loads (a wave's direct load covers
-// whole rows, so they are uniform), which leaves the vector-memory counter to
-// the ring.
-template <class Op, int BM, int BN, int WM, int WN, int S>
+// are gathered by the same ring of direct loads: a stage holds, task by task,
+// BM columns of the task's dy row and then BN columns of its x row, so that a
+// load takes both of one task (BM = BN = 256, bf16) or of a few.  The row
+// numbers are read one stage ahead as constants at uniform addresses (scalar
+// loads: the vector-memory counter stays with the ring), and the address work
+// is kept to a few instructions per load: at two waves per SIMD the
+// instructions between the MFMAs are what bounds this kernel: 65536 tasks, 64
+// experts of 1408 x 2048 take 543 us (0.70 PFLOP/s) with 44 scalar and 74
+// vector ones per stage and wave, and took 630 with 105 scalar ones.
+// A row out of range is fetched as zeros, which removes its task's term.
+template <class Op, int BM, int BN, int WM, int WN, int S, bool LISTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgradArgs a) {
   using Acc = typename Op::Acc;
   constexpr int NW = WM * WN, KE = 64 / Op::kBytes;
   constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
-  constexpr int IP = BM / 16 / NW, IQ = BN / 16 / NW;
-  constexpr int STAGE = (BM + BN) * 64;
-  constexpr int PR = 1024 / (BM * Op::kBytes), QR = 1024 / (BN * Op::kBytes);  // rows per load
-  static_assert(PR >= 1 && QR >= 1, "a load covers whole rows");
+  constexpr int TASK = (BM + BN) * Op::kBytes;  // bytes of a task in a stage
+  constexpr int STAGE = KE * TASK;
+  constexpr int I = STAGE / 1024 / NW;          // loads per wave and stage
+  constexpr int TPI = 1024 / TASK;              // tasks of a load
+  constexpr int NT = I * TPI;                   // tasks of a wave and stage
+  static_assert(TPI >= 1 && I >= 1 && I * NW * 1024 == STAGE, "loads split evenly");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
 
   const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
   const int n_nt = (a.n + BM - 1) / BM, n_kt = (a.k + BN - 1) / BN;
-  // The n_kt tiles of one expert and one dy column block are a group: they
-  // share dy's columns and x's rows in an L2.  Groups are dealt to the XCDs in
-  // turn, the experts with the most tasks first (of every 64), so that long
-  // contractions neither pile up on one XCD nor start last.
-  const int slot = blockIdx.x >> 3, group = slot / n_kt * 8 + (blockIdx.x & 7);
-  if (group >= a.E * n_nt) return;
-  const int e = expert_by_size(a.offsets, a.E, a.M, group / n_nt);
-  const int n0 = group % n_nt * BM, c0 = slot % n_kt * BN;
-  int lo, hi;
-  expert_range(a.offsets, e, a.M, lo, hi);
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  hi = __builtin_amdgcn_readfirstlane(hi);
-  const uint8_t* x = static_cast<const uint8_t*>(a.x);
-  const uint8_t* dy = static_cast<const uint8_t*>(a.dy);
+  WgradPart w;
+  int n0, c0;
+  if (a.part > 0) {
+    const ExpertScan sc = scan_experts(a.offsets, a.E, a.M, a.part);
+    const int tiles = n_nt * n_kt, total = sc.total * tiles;
+    if (!xcd_has(blockIdx.x, total)) return;
+    const int id = xcd_tile(blockIdx.x, total), p = id / tiles, tile = id - p * tiles;
+    // a part is a row tile of `part` rows; with one column tile each
+    const TilePlace at = find_tile(sc, a.offsets, a.E, a.M, a.part, 1, p);
+    if (at.t.m0 >= at.t.m1) return;
+    w = {at.t.e, at.t.m0, at.t.m1, -1};
+    int lo, hi;
+    expert_range(a.offsets, w.e, a.M, lo, hi);
+    if (hi - lo > a.part)
+      w.slot = first_slot(a.offsets, a.E, a.M, a.part, w.e) + (w.lo - lo) / a.part;
+    if (w.slot >= a.slots) return;  // offsets that overlap
+    n0 = tile / n_kt * BM;
+    c0 = tile % n_kt * BN;
+  } else {
+    // The n_kt tiles of one expert and one dy column block are a group: they
+    // share dy's columns and x's rows in an L2.  Groups are dealt to the XCDs
+    // in turn, the experts with the most tasks first (of every 64), so that
+    // long contractions neither pile up on one XCD nor start last.
+    const int slot = blockIdx.x >> 3, group = slot / n_kt * 8 + (blockIdx.x & 7);
+    if (group >= a.E * n_nt) return;
+    w.e = expert_by_size(a.offsets, a.E, a.M, group / n_nt);
+    expert_range(a.offsets, w.e, a.M, w.lo, w.hi);
+    w.slot = -1;
+    n0 = group % n_nt * BM;
+    c0 = slot % n_kt * BN;
+  }
+  const int lo = __builtin_amdgcn_readfirstlane(w.lo), hi = __builtin_amdgcn_readfirstlane(w.hi);
   const int nk = (hi - lo + KE - 1) / KE;
 
-  // Row numbers of dy and x: read for the next stage as constants at uniform
-  // addresses (scalar loads), checked when that stage is issued; -1: none.
+  // This lane's part of a load: which of the load's rows, and where in it.  The
+  // tasks of a wave's load u are TPI (wv I + u) .. + TPI - 1 of the stage.
+  const int sub = l * 16 / TASK, in = l * 16 % TASK;
+  const bool is_x = in >= BM * Op::kBytes;
+  const int pos = is_x ? in - BM * Op::kBytes : in;  // byte in its operand's part of the row
+  const uint32_t limit = is_x ? a.R : a.Ry;
+  const uint32_t stride = (is_x ? a.k : a.n) * Op::kBytes;
+  const uint8_t* base[I];
+#pragma unroll
+  for (int u = 0; u < I; ++u) {
+    const int kk = (wv * I + u) * TPI + sub;
+    const int col = (is_x ? c0 : n0) + ((pos >> 4) ^ swz_cols<Op, BM>(kk)) * (16 / Op::kBytes);
+    base[u] = static_cast<const uint8_t*>(is_x ? a.x : a.dy) +
+              (col < (is_x ? a.k : a.n) ? col : 0) * static_cast<size_t>(Op::kBytes);
+  }
+  static_assert(BM == BN, "one swizzle for both halves of a task");
+
   typedef const int32_t __attribute__((address_space(4))) ConstInt;
-  ConstInt* xl = (ConstInt*)reinterpret_cast<uintptr_t>(a.x_row ? a.x_row : a.offsets);
-  ConstInt* yl = (ConstInt*)reinterpret_cast<uintptr_t>(a.dy_row ? a.dy_row : a.offsets);
-  constexpr int NP = IP * PR, NQ = BM == BN ? 0 : IQ * QR;  // BM == BN: the same tasks
-  int raw_y[NP + NQ], raw_x[NP + NQ], prow[NP], qrow[IQ * QR];
-  auto task = [&](int kt, int r) {
-    return lo + kt * KE + (r < NP ? wv * NP + r : wv * NQ + r - NP);
-  };
-  // may_end: the stage may reach past the expert's last task (or the lists' end)
+  ConstInt* xl = (ConstInt*)reinterpret_cast<uintptr_t>(a.x_row);
+  ConstInt* yl = (ConstInt*)reinterpret_cast<uintptr_t>(a.dy_row);
+  int raw_y[NT], raw_x[NT];
+  // may_end: the stage may reach past the last task (or the lists' end)
   auto fetch_rows = [&](int kt, bool may_end) {
+    const int first = lo + kt * KE + wv * NT;
 #pragma unroll
-    for (int r = 0; r < NP + NQ; ++r) {
-      const int m = may_end ? min(task(kt, r), a.M - 1) : task(kt, r);
-      raw_y[r] = yl[a.dy_row ? m : 0];
-      raw_x[r] = xl[a.x_row ? m : 0];
+    for (int r = 0; r < NT; ++r) {
+      const int m = may_end ? min(first + r, a.M - 1) : first + r;
+      if constexpr (LISTS) {
+        raw_y[r] = yl[m];
+        raw_x[r] = xl[m];
+      } else {
+        raw_y[r] = a.dy_row ? yl[m] : m;
+        raw_x[r] = a.x_row ? xl[m] : m;
+      }
+      if (may_end && first + r >= hi) raw_y[r] = raw_x[r] = -1;
     }
   };
-  auto check_rows = [&](int kt, bool may_end) {
-#pragma unroll
-    for (int r = 0; r < NP + NQ; ++r) {
-      const int m = task(kt, r);
-      const int ry = a.dy_row ? raw_y[r] : m, rx = a.x_row ? raw_x[r] : m;
-      const bool ok = (static_cast<unsigned>(ry) < static_cast<unsigned>(a.Ry)) &
-                      (static_cast<unsigned>(rx) < static_cast<unsigned>(a.R)) &
-                      (!may_end | (m < hi));
-      if (r < NP) prow[r] = ok ? ry : -1;
-      if (NQ == 0) qrow[r] = ok ? rx : -1;
-      else if (r >= NP) qrow[r - NP] = ok ? rx : -1;
-    }
-  };
-  constexpr int PCPR = 64 / PR, QCPR = 64 / QR;  // chunks per row
   const uint32_t ring = lds_address(smem);
-  auto load_rows = [&](const uint8_t* m, int width, int col, int row, uint32_t dst) {
-    const void* src = m + (static_cast<size_t>(row) * width + (col < width ? col : 0)) * Op::kBytes;
-    load_lds16(row < 0 ? kZeroChunk : src, dst);
-  };
   auto issue = [&](int kt, int u, bool may_end) {
-    const uint32_t st = ring + (kt % S) * STAGE;
-    if (u == 0) {
-      check_rows(kt, may_end);
-      fetch_rows(kt + 1, may_end);
-    }
-    if (u < IP) {
-      const int sub = l / PCPR, kk = (wv * IP + u) * PR + sub;
-      int row = prow[u * PR];
+    uint32_t row = 0;
 #pragma unroll
-      for (int r = 1; r < PR; ++r) row = sub == r ? prow[u * PR + r] : row;
-      load_rows(dy, a.n, n0 + ((l % PCPR) ^ swz_t<Op>(kk)) * (16 / Op::kBytes), row,
-                st + (wv * IP + u) * 1024);
-    } else {
-      u -= IP;
-      const int sub = l / QCPR, kk = (wv * IQ + u) * QR + sub;
-      int row = qrow[u * QR];
-#pragma unroll
-      for (int r = 1; r < QR; ++r) row = sub == r ? qrow[u * QR + r] : row;
-      load_rows(x, a.k, c0 + ((l % QCPR) ^ swz_t<Op>(kk)) * (16 / Op::kBytes), row,
-                st + BM * 64 + (wv * IQ + u) * 1024);
+    for (int r = 0; r < TPI; ++r) {
+      const uint32_t ry = raw_y[u * TPI + r], rx = raw_x[u * TPI + r], mine = is_x ? rx : ry;
+      row = r == 0 || sub == r ? mine : row;
     }
+    const uint8_t* src = base[u] + static_cast<uint64_t>(row) * stride;
+    load_lds16(row < limit ? src : reinterpret_cast<const uint8_t*>(kZeroChunk),
+               ring + (kt % S) * STAGE + (wv * I + u) * 1024);
+    if (u == I - 1) fetch_rows(kt + 1, may_end);
   };
   const int wm = wv / WN, wn = wv % WN, fr = l & 15, g = l >> 4;
   auto read_p = [&](int kt, int i) {
-    return frag_strided<Op, BM>(smem + (kt % S) * STAGE, wm * (BM / WM) + i * 16, l);
+    return frag_strided<Op, BM, TASK>(smem + (kt % S) * STAGE, wm * (BM / WM) + i * 16, l);
   };
   auto read_q = [&](int kt, int j) {
-    return frag_strided<Op, BN>(smem + (kt % S) * STAGE + BM * 64, wn * (BN / WN) + j * 16, l);
+    return frag_strided<Op, BN, TASK>(smem + (kt % S) * STAGE + BM * Op::kBytes,
+                                      wn * (BN / WN) + j * 16, l);
   };
   Acc acc[TI][TJ] = {};
   if (nk > 0) {
     fetch_rows(0, true);
-    run_pipeline<Op, IP + IQ, S>(nk, issue, read_p, read_q, acc);
+    run_pipeline<Op, I, S>(nk, issue, read_p, read_q, acc);
   }
+  float* out = w.slot < 0 ? a.dw + static_cast<size_t>(w.e) * a.n * a.k
+                          : a.partial + static_cast<size_t>(w.slot) * a.n * a.k;
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const int r = n0 + wm * (BM / WM) + i * 16 + fr;
     if (r >= a.n) continue;
-    float* dst = a.dw + (static_cast<size_t>(e) * a.n + r) * a.k;
+    float* dst = out + static_cast<size_t>(r) * a.k;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int c = c0 + wn * (BN / WN) + j * 16 + g * 4;
@@ -663,6 +713,31 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
                                                           acc[i][j][2], acc[i][j][3]);
     }
   }
+}
+
+// Experts cut into parts: dW = the sum of their partial sums in part order;
+// zeros for experts without tasks.
+__global__ __launch_bounds__(256) void expert_wgrad_reduce_kernel(ExpertWgradArgs a) {
+  const int e = blockIdx.y;
+  int lo, hi;
+  expert_range(a.offsets, e, a.M, lo, hi);
+  const int parts = parts_of(hi - lo, a.part);
+  if (parts == 1) return;
+  const size_t size = static_cast<size_t>(a.n) * a.k;
+  const size_t at = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  const int first = parts > 1 ? max(first_slot(a.offsets, a.E, a.M, a.part, e), 0) : 0;
+  if (at >= size) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int n = min(parts, a.slots - first);  // fewer: offsets that overlap
+#pragma unroll 8
+  for (int z = 0; z < n; ++z) {
+    const float4 v = *reinterpret_cast<const float4*>(a.partial + (first + z) * size + at);
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  *reinterpret_cast<float4*>(a.dw + e * size + at) = s;
 }
 
 // ------------------------------------------------------------------ few rows per expert
@@ -776,15 +851,8 @@ static long long product_blocks(const ExpertMatmulArgs& a, int bm, int bno) {
   const int N = a.transpose ? a.k : a.n;
   return expert_row_tiles(a.M, a.E, bm) * ((N + bno - 1) / bno);
 }
-static long long wgrad_blocks(const ExpertWgradArgs& a, int bm, int bn) {
-  const long long groups = static_cast<long long>(a.E) * ((a.n + bm - 1) / bm);
-  return (groups + 7) / 8 * 8 * ((a.k + bn - 1) / bn);
-}
 bool expert_matmul_grid_fits(const ExpertMatmulArgs& a) {
   return product_blocks(a, 16, 16) < (1ll << 32) / 512;
-}
-bool expert_wgrad_grid_fits(const ExpertWgradArgs& a) {
-  return wgrad_blocks(a, 64, 64) < (1ll << 32) / 512;
 }
 template <class Op, typename TO, bool QT, bool SW, int BM, int BN, int WM, int WN, int S>
 static hipError_t run_tiles(const ExpertMatmulArgs& a, hipStream_t s) {
@@ -876,19 +944,83 @@ hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s) {
                              : run_product<F32Op, float>(a, s);
 }
 
-template <class Op, int BM, int BN, int WM, int WN, int S>
+// How a weight gradient runs: its square tile, and the tasks of a part (0: no
+// parts).  A tile of 256 where experts and parts of 1024 tasks give enough of
+// them for the chip, else the smaller ones; float32, bound by its MFMAs, always
+// takes the smallest, and experts of few tasks, bound by writing dW, not the
+// largest (us, tiles of 64 / 128 / 256):
+//   64 experts, 1408 x 2048, 1024 tasks each, bf16       - / 688 / 543
+//   1 expert, 512 x 512, 8192 tasks, bf16                26 / 32 / 41
+//   100 experts, 256 x 1024, 4 tasks each, bf16          41 / 29 / 36
+//   16 experts, 512 x 512, 500 tasks each, float32       73 / 139 / -
+// Parts where the tiles are fewer than four times those that run at a time:
+// long enough that one round of them holds all tasks, and at least 32 stages
+// (their partial sums and the second launch cost about what 30 stages do).
+struct WgradPlan {
+  int tile, part, slots;
+};
+static WgradPlan plan_wgrad(int bf16, int M, int E, int n, int k) {
+  auto tiles = [&](int b) {
+    return static_cast<long long>((n + b - 1) / b) * ((k + b - 1) / b);
+  };
+  const long long used = E < M ? E : M, least = bf16 ? 1024 : 512;
+  const long long units = used > M / least ? used : M / least;
+  WgradPlan p = {64, 0, 0};
+  if (bf16 && units * tiles(256) >= 192 && M >= 64 * used) p.tile = 256;
+  else if (bf16 && units * tiles(128) >= 256) p.tile = 128;
+  const long long t = tiles(p.tile), round = p.tile == 256 ? 256 : p.tile == 128 ? 512 : 1024;
+  if (M > 0 && used * t < 4 * round) {
+    long long part = (M * t + round - 1) / round;
+    if (part < least) part = least;
+    part = (part + 127) / 128 * 128;
+    if (part < M) {
+      p.part = static_cast<int>(part);
+      const long long most = M / part + used, twice = 2ll * M / part;
+      p.slots = static_cast<int>(most < twice ? most : twice);
+    }
+  }
+  return p;
+}
+static long long wgrad_blocks(const ExpertWgradArgs& a, int tile) {
+  const long long nt = (a.n + tile - 1) / tile, kt = (a.k + tile - 1) / tile;
+  if (a.part > 0) return expert_row_tiles(a.M, a.E, a.part) * nt * kt;
+  return (a.E * nt + 7) / 8 * 8 * kt;
+}
+size_t expert_wgrad_ws_bytes(int bf16, int M, int E, int n, int k) {
+  return static_cast<size_t>(plan_wgrad(bf16, M, E, n, k).slots) * n * k * 4;
+}
+bool expert_wgrad_grid_fits(const ExpertWgradArgs& a) {
+  ExpertWgradArgs b = a;
+  const WgradPlan p = plan_wgrad(a.bf16, a.M, a.E, a.n, a.k);
+  b.part = p.part;
+  return wgrad_blocks(b, p.tile) < (1ll << 32) / 512 && a.E < (p.part ? 65536 : 1 << 30) &&
+         static_cast<long long>(a.n) * a.k / 4 < (1ll << 32) - 1024;
+}
+
+template <class Op, int B, int WM, int WN>
 static hipError_t run_wgrad(const ExpertWgradArgs& a, hipStream_t s) {
-  const unsigned nb = static_cast<unsigned>(wgrad_blocks(a, BM, BN));
-  expert_wgrad_kernel<Op, BM, BN, WM, WN, S><<<nb, WM * WN * 64, 0, s>>>(a);
+  const unsigned nb = static_cast<unsigned>(wgrad_blocks(a, B));
+  if (a.x_row && a.dy_row)
+    expert_wgrad_kernel<Op, B, B, WM, WN, 4, true><<<nb, WM * WN * 64, 0, s>>>(a);
+  else
+    expert_wgrad_kernel<Op, B, B, WM, WN, 4, false><<<nb, WM * WN * 64, 0, s>>>(a);
   return hipGetLastError();
 }
-template <class Op>
-static hipError_t pick_wgrad(const ExpertWgradArgs& a, hipStream_t s) {
-  if (wgrad_blocks(a, 256, 256) >= 256) return run_wgrad<Op, 256, 256, 2, 4, 4>(a, s);
-  return run_wgrad<Op, 128, 128, 2, 2, 4>(a, s);
-}
-hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t s) {
-  return a.bf16 ? pick_wgrad<Bf16Op>(a, s) : pick_wgrad<F32Op>(a, s);
+hipError_t launch_expert_wgrad(const ExpertWgradArgs& args, float* ws, hipStream_t s) {
+  ExpertWgradArgs a = args;
+  const WgradPlan p = plan_wgrad(a.bf16, a.M, a.E, a.n, a.k);
+  a.part = p.part;
+  a.slots = p.slots;
+  a.partial = ws;
+  hipError_t e;
+  if (p.tile == 256) e = run_wgrad<Bf16Op, 256, 2, 4>(a, s);
+  else if (p.tile == 128) e = run_wgrad<Bf16Op, 128, 2, 2>(a, s);
+  else
+    e = a.bf16 ? run_wgrad<Bf16Op, 64, 2, 2>(a, s) : run_wgrad<F32Op, 64, 2, 2>(a, s);
+  if (e != hipSuccess || a.part == 0) return e;
+  const unsigned nb = static_cast<unsigned>((static_cast<size_t>(a.n) * a.k / 4 + 255) / 256);
+  expert_wgrad_reduce_kernel<<<dim3(nb, a.E), 256, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace omni

@@ -144,12 +144,16 @@ struct ExpertWgradArgs {
   const int32_t* dy_row;
   const int32_t* offsets;
   float* dw;
+  int part, slots;  // set by the launch: tasks of a part (0: no parts), partial sums
+  float* partial;   // [slots, n, k]
 };
 // work-items of a launch dimension are counted in 32 bits
 bool expert_matmul_grid_fits(const ExpertMatmulArgs& a);
 bool expert_wgrad_grid_fits(const ExpertWgradArgs& a);
 hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s);
-hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t s);
+// ws: expert_wgrad_ws_bytes of them, partial sums of experts cut into parts
+size_t expert_wgrad_ws_bytes(int bf16, int M, int E, int n, int k);
+hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, float* ws, hipStream_t s);
 
 // expert_combine.hip
 hipError_t launch_expert_combine(int bf16, int L, int K, int n, const void* o, const float* gate,

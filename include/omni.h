@@ -499,14 +499,19 @@ omni_status omni_expert_matmul(omni_dtype dt, int M, int E, int n, int k, int R,
  *
  * x [R, k], dy [Ry, n] of dt; x_row, dy_row [M] int32 or NULL; dw [E, n, k]
  * float32, overwritten (zero for experts without tasks; M == 0 writes zeros).
- * A task with either row out of range adds nothing.  Requires n and k
- * multiples of 8 (bf16) or 4 (float32), else UNSUPPORTED; x, dy, dw 16-byte
- * aligned.  Deterministic: every sum runs in a fixed order, in float32.
+ * A task with either row out of range adds nothing.  ws / ws_bytes: at
+ * least omni_expert_weight_grad_workspace(...) bytes, 256-byte aligned, or
+ * NULL with 0 when that is 0 (few tiles of dw: experts with many tasks are cut
+ * into parts, whose partial sums it holds).  Requires n and k multiples of 8
+ * (bf16) or 4 (float32), else UNSUPPORTED, as is a launch of 2^32 work-items or
+ * more; x, dy, dw 16-byte aligned.  Deterministic: every sum runs in a fixed
+ * order, in float32.
  */
+size_t omni_expert_weight_grad_workspace(omni_dtype dt, int M, int E, int n, int k);
 omni_status omni_expert_weight_grad(omni_dtype dt, int M, int E, int n, int k, int R, int Ry,
                                     const void* x, const int32_t* x_row, const void* dy,
                                     const int32_t* dy_row, const int32_t* offsets, float* dw,
-                                    hipStream_t stream);
+                                    void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
  * omni_expert_combine — the experts' rows of every token summed with its gates:

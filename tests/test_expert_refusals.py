@@ -34,8 +34,8 @@ def test_expert_weight_grad_argument_checks():
     f = B.lib().omni_expert_weight_grad
 
     def call(dt=1, M=4, E=2, n=8, k=16, R=4, Ry=4, x=FAKE, xr=None, dy=FAKE, yr=None, off=FAKE,
-             dw=FAKE):
-        return f(dt, M, E, n, k, R, Ry, x, xr, dy, yr, off, dw, None)
+             dw=FAKE, ws=None, nws=0):
+        return f(dt, M, E, n, k, R, Ry, x, xr, dy, yr, off, dw, ws, nws, None)
     for bad in (dict(dt=2), dict(M=-1), dict(E=0), dict(n=0), dict(k=0), dict(x=None),
                 dict(dy=None), dict(off=None), dict(dw=None), dict(x=MIS), dict(dy=MIS),
                 dict(dw=MIS), dict(R=3), dict(Ry=3)):
@@ -44,6 +44,15 @@ def test_expert_weight_grad_argument_checks():
     assert call(k=12) == UNS
     assert call(dt=0, n=6) == UNS
     assert call(E=1 << 30, n=1 << 15, k=1 << 15) == UNS
+    # few tiles, many tasks: partial sums in a workspace
+    need = B.lib().omni_expert_weight_grad_workspace
+    assert need(1, 4, 2, 8, 16) == 0 and need(2, 4, 2, 8, 16) == 0 and need(1, 4, 2, 0, 16) == 0
+    assert need(1, 65536, 64, 1408, 2048) == 0
+    big = dict(M=8192, E=1, n=512, k=512, R=8192, Ry=8192)
+    n = need(1, 8192, 1, 512, 512)
+    assert n >= 2 * 512 * 512 * 4
+    for bad in (dict(), dict(ws=FAKE, nws=n - 1), dict(ws=ctypes.c_void_p((1 << 20) + 16), nws=n)):
+        assert call(**big, **bad) == B.OMNI_ERR_WORKSPACE, bad
 
 
 def test_combine_argument_checks():

@@ -156,6 +156,30 @@ def test_expert_weight_grad(name, dt):
 
 @gpu
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,n,k", [
+    ([3000], 72, 136),                        # one expert in parts, ragged last part
+    ([0, 2500, 0, 1024, 1025, 1, 300, 0], 64, 64),  # parts, one part, none
+    ([i * 7 % 90 + (3100 if i % 50 == 1 else 0) for i in range(130)], 24, 16),  # > 64 lanes
+    ([5000, 40, 17], 640, 520)])
+def test_expert_weight_grad_in_parts(counts, n, k, dt):
+    rng = np.random.default_rng(6)
+    off = offsets(counts)
+    M = int(off[-1]) + PAD
+    assert B.lib().omni_expert_weight_grad_workspace(dt == "bf16", M, len(counts), n, k) > 0
+    x, dy = rand(rng, (M // 2 + 1, k), dt), rand(rng, (M, n), dt)
+    xr = rng.integers(0, x.shape[0], M).astype(np.int32)
+    xr[7] = -1
+    yr = rng.permutation(M).astype(np.int32)
+    want, mass = OE.expert_weight_grad_f64(x, dy, off, M, xr, yr)
+    dw = torch.full(want.shape, float("nan"), device="cuda")
+    B.expert_weight_grad(dev(x), dev(dy), dev(off), x_row=dev(xr), dy_row=dev(yr), dw=dw)
+    tol = sum_tol(max(counts), mass, want, "f32")
+    tol[mass == 0] = 0
+    close(host(dw), want, tol, "dw in parts")
+
+
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_rows_out_of_range(dt):
     """x rows out of range count as zeros, output rows out of range are dropped,
     and their tasks add nothing to the weight gradient."""
