@@ -272,23 +272,35 @@ __device__ __forceinline__ typename Op::Frag frag_strided(const uint8_t* st, int
 // stage kt + 1 has landed, barrier, then run stage kt's MFMAs (its fragments
 // are in registers) while the slot of stage kt is refilled with stage kt + S
 // and stage kt + 1's fragments are read into the other register set.  Loads and
-// reads are issued between the MFMAs, one row of tiles at a time: issued
-// together after the barrier they fill the load and LDS queues, and a wave
-// that waits for room there issues no MFMA.
+// reads are issued between the MFMAs, one row of tiles at a time, the loads in
+// the first half and the reads ahead of the last rows: issued together after
+// the barrier they fill the load and LDS queues, and a wave that waits for room
+// there issues no MFMA (up_train's shape: 442 us, spread as here 422).
 //   issue(kt, u, may_end): load u of stage kt; may_end: it or the next may be the last
 //   read_p(kt, i), read_q(kt, j): fragments of stage kt
+// ACTIVE false: a wave whose part of the tile is empty; it only loads.
 // The steady loop has no branch between a read and the MFMAs that use it: a
 // join there makes the compiler wait for the reads just issued.
-template <class Op, int I, int S, int TI, int TJ, class Issue, class ReadP, class ReadQ>
-__device__ __forceinline__ void run_pipeline(int nk, Issue issue, ReadP read_p, ReadQ read_q,
-                                             typename Op::Acc (&acc)[TI][TJ]) {
+template <class Op, int I, int S, bool ACTIVE, int TI, int TJ, class Issue, class ReadP,
+          class ReadQ>
+__device__ __forceinline__ void run_stages(int nk, Issue issue, ReadP read_p, ReadQ read_q,
+                                           typename Op::Acc (&acc)[TI][TJ]) {
   using Frag = typename Op::Frag;
+  constexpr int H = TI > 1 ? TI / 2 : 1, D = TI > 2 ? TI - 2 : 1;
   Frag p0[TI], q0[TJ], p1[TI], q1[TJ];
   auto mma_row = [&](int i, const Frag (&p)[TI], const Frag (&q)[TJ]) {
+    if constexpr (!ACTIVE) return;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < TJ; ++j) Op::mma(acc[i][j], q[j], p[i]);
     __builtin_amdgcn_sched_barrier(0);
+  };
+  auto read = [&](int kt, int i, int of, Frag (&np)[TI], Frag (&nq)[TJ]) {  // share i of `of`
+    if constexpr (!ACTIVE) return;
+#pragma unroll
+    for (int j = i * TJ / of; j < (i + 1) * TJ / of; ++j) nq[j] = read_q(kt, j);
+#pragma unroll
+    for (int r = i * TI / of; r < (i + 1) * TI / of; ++r) np[r] = read_p(kt, r);
   };
   auto steady = [&](int kt, const Frag (&p)[TI], const Frag (&q)[TJ], Frag (&np)[TI],
                     Frag (&nq)[TJ]) {
@@ -296,11 +308,11 @@ __device__ __forceinline__ void run_pipeline(int nk, Issue issue, ReadP read_p, 
     lds_barrier();
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
+      if (i < H) {
 #pragma unroll
-      for (int u = i * I / TI; u < (i + 1) * I / TI; ++u) issue(kt + S, u, false);
-#pragma unroll
-      for (int j = i * TJ / TI; j < (i + 1) * TJ / TI; ++j) nq[j] = read_q(kt + 1, j);
-      np[i] = read_p(kt + 1, i);
+        for (int u = i * I / H; u < (i + 1) * I / H; ++u) issue(kt + S, u, false);
+      }
+      if (i < D) read(kt + 1, i, D, np, nq);
       mma_row(i, p, q);
     }
   };
@@ -313,26 +325,12 @@ __device__ __forceinline__ void run_pipeline(int nk, Issue issue, ReadP read_p, 
 #pragma unroll
         for (int u = 0; u < I; ++u) issue(kt + S, u, true);
       }
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) nq[j] = read_q(kt + 1, j);
-#pragma unroll
-      for (int i = 0; i < TI; ++i) np[i] = read_p(kt + 1, i);
+      read(kt + 1, 0, 1, np, nq);
     }
 #pragma unroll
     for (int i = 0; i < TI; ++i) mma_row(i, p, q);
   };
-#pragma unroll
-  for (int v = 0; v < S; ++v)
-    if (v < nk) {
-#pragma unroll
-      for (int u = 0; u < I; ++u) issue(v, u, true);
-    }
-  wait_stages<I, S + 1>(min(S, nk) - 1);
-  lds_barrier();
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) q0[j] = read_q(0, j);
-#pragma unroll
-  for (int i = 0; i < TI; ++i) p0[i] = read_p(0, i);
+  read(0, 0, 1, p0, q0);
   int kt = 0;
   for (; kt + S + 3 < nk; kt += 2) {
     steady(kt, p0, q0, p1, q1);
@@ -342,6 +340,30 @@ __device__ __forceinline__ void run_pipeline(int nk, Issue issue, ReadP read_p, 
     tail(kt, p0, q0, p1, q1);
     if (kt + 1 < nk) tail(kt + 1, p1, q1, p0, q0);
   }
+}
+// active: uniform in a wave.  A tile of a ragged expert's last rows or of the
+// last columns leaves waves without work; the other wave of their SIMD then
+// has the matrix core to itself.
+template <class Op, int I, int S, int TI, int TJ, class Issue, class ReadP, class ReadQ>
+__device__ __forceinline__ void run_pipeline(int nk, bool active, Issue issue, ReadP read_p,
+                                             ReadQ read_q, typename Op::Acc (&acc)[TI][TJ]) {
+#pragma unroll
+  for (int v = 0; v < S; ++v)
+    if (v < nk) {
+#pragma unroll
+      for (int u = 0; u < I; ++u) issue(v, u, true);
+    }
+  wait_stages<I, S + 1>(min(S, nk) - 1);
+  lds_barrier();
+  if (active) run_stages<Op, I, S, true>(nk, issue, read_p, read_q, acc);
+  else run_stages<Op, I, S, false>(nk, issue, read_p, read_q, acc);
+}
+// Waves w and w + 4 share a SIMD: of 2 x 4 waves the pair differs in both
+// halves of the tile, so that where a half is empty every SIMD keeps one.
+template <int WM, int WN>
+__device__ __forceinline__ void wave_place(int wv, int& wm, int& wn) {
+  wm = wv / WN;
+  wn = WM == 2 && WN == 4 ? (wv + 2 * wm) % WN : wv % WN;
 }
 
 // ------------------------------------------------------------------ outputs
@@ -464,7 +486,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
     }
   };
 
-  const int wm = wv / WN, wn = wv % WN, fr = l & 15, g = l >> 4;
+  const int fr = l & 15, g = l >> 4;
+  int wm, wn;
+  wave_place<WM, WN>(wv, wm, wn);
   auto read_p = [&](int kt, int i) {
     return frag_rows<Op, false>(smem + (kt % S) * STAGE, wm * (BM / WM) + i * 16 + fr, g);
   };
@@ -478,7 +502,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
                                  g);
   };
   Acc acc[TI][TJ] = {};
-  run_pipeline<Op, IP + IQ, S>(nk, issue, read_p, read_q, acc);
+  const bool active = t.m0 + wm * (BM / WM) < t.m1 && n0 + wn * (BNO / WN) < N;
+  run_pipeline<Op, IP + IQ, S>(nk, active, issue, read_p, read_q, acc);
+  if (!active) return;
 
   // lane (fr, g) holds row i * 16 + fr; columns: QT 16 j + 4 g + 0..3, else
   // 32 (j / 2) + 8 g + 0..7 of tiles j, j + 1
@@ -685,7 +711,9 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
                ring + (kt % S) * STAGE + (wv * I + u) * 1024);
     if (u == I - 1) fetch_rows(kt + 1, may_end);
   };
-  const int wm = wv / WN, wn = wv % WN, fr = l & 15, g = l >> 4;
+  const int fr = l & 15, g = l >> 4;
+  int wm, wn;
+  wave_place<WM, WN>(wv, wm, wn);
   auto read_p = [&](int kt, int i) {
     return frag_strided<Op, BM, TASK>(smem + (kt % S) * STAGE, wm * (BM / WM) + i * 16, l);
   };
@@ -696,7 +724,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
   Acc acc[TI][TJ] = {};
   if (nk > 0) {
     fetch_rows(0, true);
-    run_pipeline<Op, I, S>(nk, issue, read_p, read_q, acc);
+    run_pipeline<Op, I, S>(nk, n0 + wm * (BM / WM) < a.n && c0 + wn * (BN / WN) < a.k, issue, read_p,
+                           read_q, acc);
   }
   float* out = w.slot < 0 ? a.dw + static_cast<size_t>(w.e) * a.n * a.k
                           : a.partial + static_cast<size_t>(w.slot) * a.n * a.k;
