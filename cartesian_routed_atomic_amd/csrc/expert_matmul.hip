@@ -75,16 +75,16 @@ __device__ __forceinline__ void expert_range(const int32_t* off, int e, int M, i
 }
 struct ExpertScan {
   int mine, upto, total;
+  int lo, hi;  // tasks of this lane's last expert (its only one up to 64 experts)
 };
 __device__ __forceinline__ ExpertScan scan_experts(const int32_t* off, int E, int M, int bm) {
   const int l = lane(), q = (E + kWave - 1) / kWave;
-  ExpertScan s{0, 0, 0};
+  ExpertScan s{0, 0, 0, 0, 0};
   for (int i = 0; i < q; ++i) {
     const int e = l * q + i;
     if (e < E) {
-      int lo, hi;
-      expert_range(off, e, M, lo, hi);
-      s.mine += (hi - lo + bm - 1) / bm;
+      expert_range(off, e, M, s.lo, s.hi);
+      s.mine += (s.hi - s.lo + bm - 1) / bm;
     }
   }
   s.upto = wave_prefix_sum(s.mine);
@@ -115,6 +115,10 @@ __device__ __forceinline__ TilePlace find_tile(const ExpertScan& s, const int32_
   const int owner = __ffsll(static_cast<long long>(past)) - 1;
   int left = row - (__builtin_amdgcn_readlane(s.upto, owner) -
                     __builtin_amdgcn_readlane(s.mine, owner));
+  if (q == 1)
+    return place_in_expert(owner, __builtin_amdgcn_readlane(s.lo, owner),
+                           __builtin_amdgcn_readlane(s.hi, owner), bm, n_nt,
+                           id - (row - left) * n_nt);
   for (int i = 0; i < q; ++i) {
     const int e = owner * q + i;
     if (e >= E) break;
@@ -127,22 +131,23 @@ __device__ __forceinline__ TilePlace find_tile(const ExpertScan& s, const int32_
   return {{0, 0, 0}, 0};
 }
 // The expert at position pos when every run of 64 experts is put in order of
-// its task counts, most first (ties by id).
-__device__ __forceinline__ int expert_by_size(const int32_t* off, int E, int M, int pos) {
+// its task counts, most first (ties by id), and its tasks.
+__device__ __forceinline__ int expert_by_size(const int32_t* off, int E, int M, int pos, int& lo,
+                                              int& hi) {
   const int first = pos & ~63, e = first + lane();
-  int count = -1;
-  if (e < E) {
-    int lo, hi;
-    expert_range(off, e, M, lo, hi);
-    count = hi - lo;
-  }
+  int l = 0, h = -1;  // past the last expert: behind those without tasks
+  if (e < E) expert_range(off, e, M, l, h);
+  const int count = h - l;
   int rank = 0;
 #pragma unroll 8
   for (int j = 0; j < 64; ++j) {
     const int c = __builtin_amdgcn_readlane(count, j);
     rank += c > count || (c == count && j < lane()) ? 1 : 0;
   }
-  return first + __ffsll(static_cast<long long>(__ballot(rank == pos - first))) - 1;
+  const int at = __ffsll(static_cast<long long>(__ballot(rank == pos - first))) - 1;
+  lo = __builtin_amdgcn_readlane(l, at);
+  hi = __builtin_amdgcn_readlane(h, at);
+  return first + at;
 }
 // Workgroup b runs on XCD b % 8: give every XCD a contiguous run of the tiles
 // there are, so that neighbours share rows and weights in that XCD's L2.
@@ -652,8 +657,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
     // long contractions neither pile up on one XCD nor start last.
     const int slot = blockIdx.x >> 3, group = slot / n_kt * 8 + (blockIdx.x & 7);
     if (group >= a.E * n_nt) return;
-    w.e = expert_by_size(a.offsets, a.E, a.M, group / n_nt);
-    expert_range(a.offsets, w.e, a.M, w.lo, w.hi);
+    w.e = expert_by_size(a.offsets, a.E, a.M, group / n_nt, w.lo, w.hi);
     w.slot = -1;
     n0 = group % n_nt * BM;
     c0 = slot % n_kt * BN;
@@ -876,34 +880,42 @@ static long long expert_row_tiles(int M, int E, int bm) {
   const long long used = E < M ? E : M;
   return (M + used * (bm - 1)) / bm;
 }
-static long long product_blocks(const ExpertMatmulArgs& a, int bm, int bno) {
-  const int N = a.transpose ? a.k : a.n;
-  return expert_row_tiles(a.M, a.E, bm) * ((N + bno - 1) / bno);
-}
-bool expert_matmul_grid_fits(const ExpertMatmulArgs& a) {
-  return product_blocks(a, 16, 16) < (1ll << 32) / 512;
-}
-template <class Op, typename TO, bool QT, bool SW, int BM, int BN, int WM, int WN, int S>
-static hipError_t run_tiles(const ExpertMatmulArgs& a, hipStream_t s) {
-  const unsigned nb = static_cast<unsigned>(product_blocks(a, BM, SW ? BN / 2 : BN));
-  expert_product_kernel<Op, TO, QT, SW, BM, BN, WM, WN, S><<<nb, WM * WN * 64, 0, s>>>(a);
-  return hipGetLastError();
-}
-template <class Op, typename TO, bool SW, int RT, int CT, int KS, int U>
-static hipError_t run_rows(const ExpertMatmulArgs& a, hipStream_t s) {
-  const unsigned nb = static_cast<unsigned>(product_blocks(a, RT * 16, SW ? CT * 8 : CT * 16));
-  expert_rows_kernel<Op, TO, SW, RT, CT, KS, U><<<nb, KS * 64, 0, s>>>(a);
-  return hipGetLastError();
-}
+static int output_width(const ExpertMatmulArgs& a) { return a.transpose ? a.k : a.n; }
+static int used_experts(const ExpertMatmulArgs& a) { return a.E < a.M ? a.E : a.M; }
 // Tiles to expect: an expert's last row tile is half full on average.
 static double expected_tiles(const ExpertMatmulArgs& a, int bm, int bno) {
-  const int used = a.E < a.M ? a.E : a.M, N = a.transpose ? a.k : a.n;
-  const int rt = used == 1 ? (a.M + bm - 1) / bm
-                           : static_cast<int>((a.M + static_cast<long long>(used) * (bm / 2)) / bm);
-  return static_cast<double>(rt > used ? rt : used) * ((N + bno - 1) / bno);
+  const int used = used_experts(a);
+  const long long rt = used == 1 ? (a.M + bm - 1ll) / bm
+                                 : (a.M + static_cast<long long>(used) * (bm / 2)) / bm;
+  return static_cast<double>(rt > used ? rt : used) * ((output_width(a) + bno - 1) / bno);
 }
-// Which tile, for bf16 and int8: the one whose tiles take the least time,
-// in units of one round of 256 x 256 tiles (one per CU).  A 128 x 256 tile is
+
+// The forms of the product: rows kernels of 16 x 16, 32 x 32 and 64 x 32, and
+// tiles, each tasks x rows of W (with SWIGLU half as many outputs, the 16 x 16
+// one then 16 x 32 rows of W).
+enum ProductForm { kRows16, kRows32, kRows64, kTileSmall, kTileMid, kTileWide, kTileBig };
+struct FormShape {
+  int bm, bn, threads;
+};
+static FormShape form_shape(ProductForm f, int swiglu) {
+  switch (f) {
+    case kRows16: return {16, swiglu ? 32 : 16, 512};
+    case kRows32: return {32, 32, 512};
+    case kRows64: return {64, 32, 512};
+    case kTileSmall: return {64, 128, 256};
+    case kTileMid: return {128, 128, 256};
+    case kTileWide: return {128, 256, 512};
+    default: return {256, 256, 512};
+  }
+}
+static long long form_blocks(const ExpertMatmulArgs& a, ProductForm f) {
+  const FormShape h = form_shape(f, a.swiglu);
+  const int bno = a.swiglu ? h.bn / 2 : h.bn;
+  return expert_row_tiles(a.M, a.E, h.bm) * ((output_width(a) + bno - 1) / bno);
+}
+
+// Which tile, for bf16 and int8: the one whose tiles take the least time, in
+// units of one round of 256 x 256 tiles (one per CU).  A 128 x 256 tile is
 // alone on a CU as well, of the two smaller ones two and three share one; a
 // large tile needs less LDS and L2 traffic per MFMA, a small one wastes less
 // where there are few tiles or few rows.  Fitted to (us, 2048 inputs):
@@ -912,58 +924,73 @@ static double expected_tiles(const ExpertMatmulArgs& a, int bm, int bno) {
 //   128 x 256                21         25          20    36    499
 //   128 x 128                17         27          22    32    503
 //   64 x 128                 19         32          23    34    712
-struct TileCosts {
-  double big, wide, mid, small;
-};
-static TileCosts tile_costs(const ExpertMatmulArgs& a, int swiglu) {
-  const int h = swiglu ? 2 : 1;
+static ProductForm pick_tile(const ExpertMatmulArgs& a) {
+  const int h = a.swiglu ? 2 : 1;
   const double t1 = expected_tiles(a, 256, 256 / h), t2 = expected_tiles(a, 128, 256 / h),
                t4 = expected_tiles(a, 128, 128 / h), t5 = expected_tiles(a, 64, 128 / h);
   auto rounds = [](double t) { return t <= 1024 ? static_cast<int>((t + 255) / 256) : t / 256; };
-  TileCosts c;
-  c.big = rounds(t1);
-  c.wide = t2 <= 768 ? 0.72 * rounds(t2) : 0.61 * t2 / 256 + 0.3;
-  c.mid = t4 <= 256 ? 0.55 : t4 <= 512 ? 0.83 : 0.62 * t4 / 512 + 0.3;
-  c.small = t5 <= 256 ? 0.46 : 0.55 * t5 / 768 + 0.35;
-  return c;
+  const double big = rounds(t1);
+  const double wide = t2 <= 768 ? 0.72 * rounds(t2) : 0.61 * t2 / 256 + 0.3;
+  const double mid = t4 <= 256 ? 0.55 : t4 <= 512 ? 0.83 : 0.62 * t4 / 512 + 0.3;
+  const double small = t5 <= 256 ? 0.46 : 0.55 * t5 / 768 + 0.35;
+  if (big <= wide && big <= mid && big <= small) return kTileBig;
+  if (wide <= mid && wide <= small) return kTileWide;
+  return mid <= small ? kTileMid : kTileSmall;
 }
-template <class Op, typename TO, bool QT, bool SW>
-static hipError_t pick(const ExpertMatmulArgs& a, hipStream_t s) {
-  const int r = a.M / (a.E < a.M ? a.E : a.M);  // mean rows of an expert with tasks
-  if constexpr (!QT) {
-    // Few rows, or so few tiles that most CUs would idle (us; rows kernel with
-    // 16, 32 and 64 rows against 64 x 128 tiles):
+static ProductForm pick_form(const ExpertMatmulArgs& a) {
+  const bool f32 = a.type == kRowsF32;
+  if (!a.transpose) {
+    // Few rows r of an expert, or so few tiles that most CUs would idle (us;
+    // the rows kernel taken against 64 x 128 tiles):
     //   64 experts, 1408 outputs, 2048 inputs, 1 / 4 / 8 rows    44 74 90 / 54 75 79
     //   1 expert, 2048 outputs, 2048 inputs, 16 / 128 / 512      7.5 12.6 34 / 14 16 18
     //   4 experts, 512 outputs, 1024 inputs, 8 / 64 / 256        5.5 8.0 16 / 9.5 10 11
     //   16 experts, 1024 outputs, 1024 inputs, f32, 8 / 16 / 64  23 29 56 / 40 39 41
-    const double t5 = expected_tiles(a, 64, SW ? 64 : 128);
-    constexpr int C1 = SW ? 2 : 1;
-    if (t5 < (Op::kBytes == 4 ? 96 : 48)) {
-      if (r <= 32) return run_rows<Op, TO, SW, 1, C1, 8, 4>(a, s);
-      if (r <= 128) return run_rows<Op, TO, SW, 2, 2, 8, 4>(a, s);
-      return run_rows<Op, TO, SW, 4, 2, 8, 2>(a, s);
-    }
-    if (r <= (Op::kBytes == 4 ? 16 : t5 < 256 ? 8 : 2))
-      return run_rows<Op, TO, SW, 1, C1, 8, 4>(a, s);
+    //   32 experts, 128 outputs, 344 inputs, f32, 16 / 64 / 256  6.1 9.8 23 / 17 18 18
+    const int r = a.M / used_experts(a);
+    const double t5 = expected_tiles(a, 64, a.swiglu ? 64 : 128);
+    if (t5 < (f32 ? 96 : 48)) return r <= 32 ? kRows16 : r <= 128 ? kRows32 : kRows64;
+    if (r <= (f32 ? 16 : t5 < 256 ? 8 : 2)) return kRows16;
   }
   // float32 is bound by its MFMAs at any tile: the small one balances best
-  if constexpr (Op::kBytes != 4) {
-    const TileCosts c = tile_costs(a, SW);
-    if (c.big <= c.wide && c.big <= c.mid && c.big <= c.small)
-      return run_tiles<Op, TO, QT, SW, 256, 256, 2, 4, 4>(a, s);
-    if (c.wide <= c.mid && c.wide <= c.small)
-      return run_tiles<Op, TO, QT, SW, 128, 256, 2, 4, 4>(a, s);
-    if (c.mid <= c.small) return run_tiles<Op, TO, QT, SW, 128, 128, 2, 2, 4>(a, s);
+  return f32 ? kTileSmall : pick_tile(a);
+}
+bool expert_matmul_grid_fits(const ExpertMatmulArgs& a) {
+  if (a.M == 0) return true;
+  const ProductForm f = pick_form(a);
+  return form_blocks(a, f) < (1ll << 32) / form_shape(f, a.swiglu).threads;
+}
+template <class Op, typename TO, bool QT, bool SW>
+static hipError_t run_form(const ExpertMatmulArgs& a, hipStream_t s) {
+  ProductForm f = pick_form(a);
+  const unsigned nb = static_cast<unsigned>(form_blocks(a, f));
+  const int nt = form_shape(f, SW).threads;
+  if constexpr (!QT) {
+    if (f == kRows16)
+      expert_rows_kernel<Op, TO, SW, 1, SW ? 2 : 1, 8, 4><<<nb, nt, 0, s>>>(a);
+    else if (f == kRows32)
+      expert_rows_kernel<Op, TO, SW, 2, 2, 8, 4><<<nb, nt, 0, s>>>(a);
+    else if (f == kRows64)
+      expert_rows_kernel<Op, TO, SW, 4, 2, 8, 2><<<nb, nt, 0, s>>>(a);
   }
-  return run_tiles<Op, TO, QT, SW, 64, 128, 2, 2, 4>(a, s);
+  if constexpr (Op::kBytes != 4) {
+    if (f == kTileBig)
+      expert_product_kernel<Op, TO, QT, SW, 256, 256, 2, 4, 4><<<nb, nt, 0, s>>>(a);
+    else if (f == kTileWide)
+      expert_product_kernel<Op, TO, QT, SW, 128, 256, 2, 4, 4><<<nb, nt, 0, s>>>(a);
+    else if (f == kTileMid)
+      expert_product_kernel<Op, TO, QT, SW, 128, 128, 2, 2, 4><<<nb, nt, 0, s>>>(a);
+  }
+  if (f == kTileSmall)
+    expert_product_kernel<Op, TO, QT, SW, 64, 128, 2, 2, 4><<<nb, nt, 0, s>>>(a);
+  return hipGetLastError();
 }
 template <class Op, typename TO>
 static hipError_t run_product(const ExpertMatmulArgs& a, hipStream_t s) {
-  if (a.swiglu) return pick<Op, TO, false, true>(a, s);
+  if (a.swiglu) return run_form<Op, TO, false, true>(a, s);
   if constexpr (Op::kBytes != 1)
-    if (a.transpose) return pick<Op, TO, true, false>(a, s);
-  return pick<Op, TO, false, false>(a, s);
+    if (a.transpose) return run_form<Op, TO, true, false>(a, s);
+  return run_form<Op, TO, false, false>(a, s);
 }
 
 hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s) {

@@ -123,6 +123,36 @@ def test_expert_matmul_swiglu(name, dt):
     check_matmul(name, dt, gather=True, scatter=True, swiglu=True)
 
 
+# enough tiles for every tile size: counts, outputs, inputs
+WIDE = {
+    "rows_32": ([64, 65], 512, 520),
+    "rows_64": ([129, 200], 256, 264),
+    "small": ([510, 3], 2048, 72),
+    "mid": ([1020, 5], 4096, 40),
+    "wide": ([2041], 4096, 40),
+    "big": ([2041, 1800], 4096, 40),
+    "big_last_rows": ([5, 3830], 3848, 136),   # a tile with 5 rows, one with 8 columns
+}
+
+
+@gpu
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_float32_tiles(swiglu, monkeypatch):
+    monkeypatch.setitem(SHAPES, "f32_tiles", ([100, 0, 99, 101, 61], 1032 if swiglu else 2056, 72))
+    check_matmul("f32_tiles", "f32", gather=True, scatter=True, swiglu=swiglu)
+
+
+@gpu
+@pytest.mark.parametrize("swiglu,transpose", [(False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("name", list(WIDE))
+def test_every_tile_size(name, swiglu, transpose, monkeypatch):
+    counts, n, k = WIDE[name]
+    if transpose:
+        n, k = k, n
+    monkeypatch.setitem(SHAPES, name, (counts, n // 2 if swiglu else n, k))
+    check_matmul(name, "bf16", gather=True, scatter=True, swiglu=swiglu, transpose=transpose)
+
+
 @gpu
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [1, 7, 33, 255])
@@ -152,6 +182,27 @@ def test_expert_weight_grad(name, dt):
         tol = sum_tol(max(counts), mass, want, "f32")
         tol[mass == 0] = 0
         close(host(dw), want, tol, name)
+
+
+@gpu
+@pytest.mark.parametrize("counts,n,k", [
+    ([70 + e for e in range(13)], 1032, 760),      # 256 x 256 tiles, short experts
+    ([700, 0, 130, 64, 1, 33], 1536, 1280),
+    ([9] * 40, 520, 264)])                         # 128 x 128 tiles
+def test_expert_weight_grad_large_tiles(counts, n, k):
+    rng = np.random.default_rng(16)
+    off = offsets(counts)
+    M = int(off[-1]) + PAD
+    x, dy = rand(rng, (M // 2 + 1, k), "bf16"), rand(rng, (M, n), "bf16")
+    xr = rng.integers(0, x.shape[0], M).astype(np.int32)
+    yr = rng.permutation(M).astype(np.int32)
+    for b in (yr, None):
+        want, mass = OE.expert_weight_grad_f64(x, dy, off, M, xr, b)
+        dw = torch.full(want.shape, float("nan"), device="cuda")
+        B.expert_weight_grad(dev(x), dev(dy), dev(off), x_row=dev(xr), dy_row=dev(b), dw=dw)
+        tol = sum_tol(max(counts), mass, want, "f32")
+        tol[mass == 0] = 0
+        close(host(dw), want, tol, "dw")
 
 
 @gpu
@@ -248,7 +299,8 @@ def test_combine(L, K, n, dt):
 
 @gpu
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("R,k", [(1, 16), (3, 48), (7, 1040), (2, 8208), (65, 128)])
+@pytest.mark.parametrize("R,k", [(1, 16), (3, 48), (7, 1040), (2, 2064), (2, 4112), (2, 8208),
+                                 (2, 16400), (65, 128)])
 def test_quantize_rows(R, k, dt):
     rng = np.random.default_rng(R + k)
     x = f32(rand(rng, (R, k), dt))
@@ -279,7 +331,8 @@ def q_tol(mass, want, dt, swiglu):
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("swiglu", [False, True])
 @pytest.mark.parametrize("M,n,k", [(1, 8, 16), (1, 264, 2064), (3, 5, 80), (17, 130, 64),
-                                   (130, 136, 144), (257, 520, 96), (64, 1000, 272)])
+                                   (130, 136, 144), (257, 520, 96), (64, 1000, 272),
+                                   (1030, 2056, 48), (2050, 4096, 16), (4090, 4096, 16)])
 def test_quantized_matmul(M, n, k, swiglu, dt):
     rng = np.random.default_rng(M + n + k)
     rows = n * (2 if swiglu else 1)
@@ -327,3 +380,109 @@ def test_quantized_expert_matmul(name, swiglu, dt):
     np.testing.assert_array_equal(got[idle], out0[idle])
     busy = orow[:int(off[-1])]
     close(got[busy], want[busy], q_tol(mass[busy], want[busy], dt, swiglu), name)
+
+
+@gpu
+def test_values_of_no_task_do_not_matter():
+    """NaN in rows that no task reads, in experts without tasks and behind the
+    last task reaches no output."""
+    rng = np.random.default_rng(21)
+    counts, n, k = [37, 0, 260, 3], 136, 72
+    off = offsets(counts)
+    M, nan = int(off[-1]) + 40, 0x7FC0
+    x, w = rand(rng, (M + 5, k), "bf16"), rand(rng, (4, n, k), "bf16", k ** -0.5)
+    dy = rand(rng, (M, n), "bf16")
+    xr = rng.permutation(M + 5)[:M].astype(np.int32)
+    used = np.zeros(M + 5, bool)
+    used[xr[:int(off[-1])]] = True
+    x[~used], w[1], dy[int(off[-1]):] = nan, nan, nan
+    clean = [np.where(a == nan, 0, a).astype(np.uint16) for a in (x, w, dy)]
+    want, mass = OE.expert_matmul_f64(clean[0], clean[1], off, M, np.zeros((M, n)), xr)
+    out = torch.zeros((M, n), dtype=torch.bfloat16, device="cuda")
+    B.expert_matmul(dev(x), dev(w), dev(off), x_row=dev(xr), out=out)
+    close(host(out), want, sum_tol(k, mass, want, "bf16") * (mass > 0), "out")
+    want, mass = OE.expert_weight_grad_f64(clean[0], clean[2], off, M, xr)
+    dw = B.expert_weight_grad(dev(x), dev(dy), dev(off), x_row=dev(xr))
+    close(host(dw), want, sum_tol(max(counts), mass, want, "f32"), "dw")
+    want, mass = OE.expert_matmul_f64(clean[2], clean[1], off, M, np.zeros((M, k)),
+                                      transpose=True)
+    dx = torch.zeros((M, k), dtype=torch.bfloat16, device="cuda")
+    B.expert_matmul(dev(dy), dev(w), dev(off), out=dx, transpose=True)
+    close(host(dx), want, sum_tol(n, mass, want, "bf16") * (mass > 0), "dx")
+
+
+@gpu
+def test_no_tasks():
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.ones((3, 32, 64), dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    assert B.expert_matmul(x, w, off).shape == (0, 32)
+    dw = torch.full((3, 32, 64), float("nan"), device="cuda")
+    B.expert_weight_grad(x, x[:, :32].contiguous(), off, dw=dw)
+    assert (dw == 0).all()
+    q, s = B.quantize_rows(x)
+    assert B.quantized_matmul(q, s, torch.ones((8, 64), dtype=torch.int8, device="cuda"),
+                              torch.ones(8, device="cuda")).shape == (0, 8)
+    assert B.expert_combine(x, 4).shape == (0, 64)
+
+
+@gpu
+def test_rows_behind_4_gib():
+    """Byte offsets of x rows, output rows and experts past 32 bits."""
+    rng = np.random.default_rng(22)
+    k, n, R = 2048, 2048, (1 << 32) // 4096 + 300
+    x = torch.empty((R, k), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty((R, n), dtype=torch.bfloat16, device="cuda")
+    counts = [40, 33]
+    off, M = offsets(counts), 73
+    rows = np.concatenate([[0, R - 1], rng.integers((1 << 32) // 4096 - 5, R - 1, M - 2)])
+    rows = np.unique(rows)
+    rows = np.concatenate([rows, rng.choice(rows, M - rows.size)]).astype(np.int32)
+    dst = (R - 1 - rng.permutation(M)).astype(np.int32)
+    data = rand(rng, (M, k), "bf16")
+    x[torch.from_numpy(rows).long().cuda()] = dev(data)
+    data = host(x[torch.from_numpy(rows).long().cuda()].contiguous())  # repeated rows: one value
+    w = rand(rng, (2, n, k), "bf16", k ** -0.5)
+    want, mass = OE.expert_matmul_f64(data, w, off, M, np.zeros((M, n)))
+    B.expert_matmul(x, dev(w), dev(off), x_row=dev(rows), out=out, out_row=dev(dst))
+    got = host(out[torch.from_numpy(dst).long().cuda()].contiguous())
+    close(got, want, sum_tol(k, mass, want, "bf16"), "far rows")
+    want, mass = OE.expert_weight_grad_f64(data, got, off, M)
+    dw = B.expert_weight_grad(x, out, dev(off), x_row=dev(rows), dy_row=dev(dst))
+    close(host(dw), want, sum_tol(40, mass, want, "f32"), "far dw")
+    del x, out, dw
+    # experts: the last of 600 weights of 8 MiB
+    w = torch.zeros((600, n, k), dtype=torch.bfloat16, device="cuda")
+    w[599] = dev(rand(rng, (n, k), "bf16", k ** -0.5))
+    off = torch.zeros(601, dtype=torch.int32, device="cuda")
+    off[600] = 5
+    a = rand(rng, (5, k), "bf16")
+    want, mass = OE.expert_matmul_f64(a, host(w[599:].contiguous()), [0, 5], 5, np.zeros((5, n)))
+    close(host(B.expert_matmul(dev(a), w, off)), want, sum_tol(k, mass, want, "bf16"), "far w")
+
+
+@gpu
+def test_strides_and_types_are_refused():
+    x = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros((2, 32, 64), dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="contiguous"):
+        B.expert_matmul(x, w.transpose(1, 2).contiguous().transpose(1, 2), off)
+    with pytest.raises(ValueError, match="contiguous"):
+        B.expert_matmul(x.t().contiguous().t(), w, off)
+    with pytest.raises(TypeError):
+        B.expert_matmul(x.half(), w.half(), off)
+    with pytest.raises(TypeError, match="w must be"):
+        B.expert_matmul(x, w.float(), off)
+    with pytest.raises(TypeError, match="offsets"):
+        B.expert_matmul(x, w, off.long())
+    with pytest.raises(ValueError, match="expected"):
+        B.expert_matmul(x, w, off[:2].contiguous())
+    with pytest.raises(ValueError, match="expected"):
+        B.expert_matmul(x[:, :32].contiguous(), w, off)
+    with pytest.raises(ValueError, match="lists 9 tasks"):
+        B.expert_matmul(x, w, off, out_row=torch.zeros(9, dtype=torch.int32, device="cuda"))
+    with pytest.raises(B.OmniError):
+        B.expert_matmul(x, w, off, out=x.new_zeros((4, 32)))   # fewer output rows than tasks
+    with pytest.raises(B.OmniError):
+        B.quantize_rows(x[:, :24].contiguous())
