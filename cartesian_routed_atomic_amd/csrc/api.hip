@@ -434,7 +434,7 @@ static omni_status expert_product(omni::ExpertMatmulArgs& a, int k_unit, int n_u
     return OMNI_ERR_INVALID_ARG;
   if (a.k % k_unit != 0 || (a.transpose && a.n % n_unit != 0)) return OMNI_ERR_UNSUPPORTED;
   if (a.type == omni::kRowsI8 && a.k > 131071) return OMNI_ERR_UNSUPPORTED;
-  if (!omni::expert_matmul_grid_fits(a)) return OMNI_ERR_UNSUPPORTED;
+  if (!omni::expert_matmul_fits(a)) return OMNI_ERR_UNSUPPORTED;
   if (a.M == 0) return OMNI_OK;
   return hip_status(omni::launch_expert_matmul(a, stream));
 }

@@ -225,6 +225,14 @@ __device__ __forceinline__ void load_lds16(const void* src, uint32_t dst) {
                    : "v"(src), "s"(dst)
                    : "memory");
 }
+// the same from a uniform base and a lane's offset (a base that a vector
+// instruction has just written needs five wait states)
+__device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t offset, uint32_t dst) {
+  __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1"
+                   :
+                   : "v"(offset), "s"(base), "s"(dst)
+                   : "memory");
+}
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) const void*)(p)));
@@ -442,52 +450,62 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
   // stored as zeros).  Contraction steps past the end fetch zeros.
   const int nk = (K + KE - 1) / KE;
   const int left = (K - (nk - 1) * KE) * Op::kBytes / 16;  // chunks of the last stage
-  const uint8_t* psrc[IP];
-  const uint8_t* qsrc[IQ];
-  int pc[IP], qc[IQ];  // this lane's chunk (or step) of the stage
+  const uint8_t* psrc[IP];  // rows may lie anywhere: whole addresses
 #pragma unroll
   for (int u = 0; u < IP; ++u) {
     const int r = (wv * IP + u) * 16 + (l >> 2);
     const int m = min(t.m0 + r, t.m1 - 1);
     const int row = min(max(a.x_row ? a.x_row[m] : m, 0), a.R - 1);
-    pc[u] = (l & 3) ^ swz_p(r);
-    psrc[u] = x + static_cast<size_t>(row) * K * Op::kBytes + pc[u] * 16;
+    psrc[u] = x + static_cast<size_t>(row) * K * Op::kBytes + ((l & 3) ^ swz_p(r)) * 16;
   }
+  // W: a uniform base (the tile's first row; with SWIGLU the 16 rows of a load
+  // are all of one half) and the lane's offset from it
+  constexpr int CPR = BN * Op::kBytes / 16;  // QT: chunks per step
+  const uint8_t* qbase[SWIGLU ? IQ : 1];
+  uint32_t qoff[IQ];
+  const size_t row_bytes = static_cast<size_t>(K) * Op::kBytes;
 #pragma unroll
   for (int u = 0; u < IQ; ++u) {
     if constexpr (QT) {
-      constexpr int CPR = BN * Op::kBytes / 16;  // chunks per step
       const int o = (wv * IQ + u) * 64 + l, kk = o / CPR, c = (o % CPR) ^ swz_cols<Op, BN>(kk);
       const int col = n0 + c * (16 / Op::kBytes);
-      qc[u] = kk;
-      qsrc[u] = w + (static_cast<size_t>(kk) * N + (col < N ? col : 0)) * Op::kBytes;
+      qoff[u] = (kk * static_cast<uint32_t>(N) + (col < N ? col : 0)) * Op::kBytes;
     } else {
-      const int r = (wv * IQ + u) * 16 + (l >> 2);
-      int row;
-      if constexpr (SWIGLU) {
-        row = min(n0 + (r >> 6) * 32 + (r & 31), N - 1) + ((r >> 5) & 1) * N;
-      } else {
-        row = min(n0 + r, N - 1);
-      }
-      qc[u] = (l & 3) ^ swz_q(r);
-      qsrc[u] = w + static_cast<size_t>(row) * K * Op::kBytes + qc[u] * 16;
+      const int first = (wv * IQ + u) * 16, r = first + (l >> 2);
+      const int row = SWIGLU ? (r >> 6) * 32 + (r & 31) : r;
+      qoff[u] = static_cast<uint32_t>(min(row, N - 1 - n0)) * static_cast<uint32_t>(row_bytes) +
+                ((l & 3) ^ swz_q(r)) * 16;
+      if constexpr (SWIGLU)
+        qbase[u] = w + (n0 + static_cast<size_t>((first >> 5) & 1) * N) * row_bytes;
     }
   }
+  if constexpr (!SWIGLU) qbase[0] = QT ? w : w + n0 * row_bytes;
   const int q_left = QT ? K - (nk - 1) * KE : left;
   const size_t q_step = QT ? static_cast<size_t>(KE) * N * Op::kBytes : 64;
   const uint32_t ring = lds_address(smem);
   auto issue = [&](int kt, int u, bool may_end) {
     const uint32_t st = ring + (kt % S) * STAGE;
+    // the lane, opaque where the last stage needs it: what follows from it
+    // there would otherwise be kept in registers throughout
+    int ll = l;
+    if (may_end) __asm__ volatile("" : "+v"(ll));
     const bool last = may_end && kt == nk - 1;
     if (u < IP) {
       const void* src = psrc[u] + static_cast<size_t>(kt) * 64;
-      if (last && pc[u] >= left) src = kZeroChunk;
+      if (last && ((ll & 3) ^ swz_p((wv * IP + u) * 16 + (ll >> 2))) >= left) src = kZeroChunk;
       load_lds16(src, st + (wv * IP + u) * 1024);
     } else {
       u -= IP;
-      const void* src = qsrc[u] + kt * q_step;
-      if (last && qc[u] >= q_left) src = kZeroChunk;
-      load_lds16(src, st + BM * 64 + (wv * IQ + u) * 1024);
+      const uint8_t* base = qbase[SWIGLU ? u : 0] + kt * q_step;
+      const uint32_t dst = st + BM * 64 + (wv * IQ + u) * 1024;
+      if (last) {
+        const int part = QT ? ((wv * IQ + u) * 64 + ll) / CPR
+                            : (ll & 3) ^ swz_q((wv * IQ + u) * 16 + (ll >> 2));
+        const void* src = base + qoff[u];
+        load_lds16(part >= q_left ? static_cast<const void*>(kZeroChunk) : src, dst);
+      } else {
+        load_lds16(base, qoff[u], dst);
+      }
     }
   };
 
@@ -893,7 +911,9 @@ static double expected_tiles(const ExpertMatmulArgs& a, int bm, int bno) {
 // The forms of the product: rows kernels of 16 x 16, 32 x 32 and 64 x 32, and
 // tiles, each tasks x rows of W (with SWIGLU half as many outputs, the 16 x 16
 // one then 16 x 32 rows of W).
-enum ProductForm { kRows16, kRows32, kRows64, kTileSmall, kTileMid, kTileWide, kTileBig };
+enum ProductForm {
+  kRows16, kRows32, kRows64, kTileF32, kTileSmall, kTileMid, kTileWide, kTileBig
+};
 struct FormShape {
   int bm, bn, threads;
 };
@@ -902,6 +922,7 @@ static FormShape form_shape(ProductForm f, int swiglu) {
     case kRows16: return {16, swiglu ? 32 : 16, 512};
     case kRows32: return {32, 32, 512};
     case kRows64: return {64, 32, 512};
+    case kTileF32: return {64, 64, 256};
     case kTileSmall: return {64, 128, 256};
     case kTileMid: return {128, 128, 256};
     case kTileWide: return {128, 256, 512};
@@ -945,17 +966,22 @@ static ProductForm pick_form(const ExpertMatmulArgs& a) {
     //   64 experts, 1408 outputs, 2048 inputs, 1 / 4 / 8 rows    44 74 90 / 54 75 79
     //   1 expert, 2048 outputs, 2048 inputs, 16 / 128 / 512      7.5 12.6 34 / 14 16 18
     //   4 experts, 512 outputs, 1024 inputs, 8 / 64 / 256        5.5 8.0 16 / 9.5 10 11
-    //   16 experts, 1024 outputs, 1024 inputs, f32, 8 / 16 / 64  23 29 56 / 40 39 41
-    //   32 experts, 128 outputs, 344 inputs, f32, 16 / 64 / 256  6.1 9.8 23 / 17 18 18
+    // float32 against its 64 x 64 tiles:
+    //   16 experts, 1024 outputs, 1024 inputs, 1 / 8 / 16        14 23 28 / 22 22 23
+    //   4 experts, 512 outputs, 512 inputs, 30 / 200             7.6 13.3 / 13.7 14.2
+    //   32 experts, 128 outputs, 344 inputs, 64 / 128            9.1 13.8 / 11.2 11.4
     const int r = a.M / used_experts(a);
-    const double t5 = expected_tiles(a, 64, a.swiglu ? 64 : 128);
-    if (t5 < (f32 ? 96 : 48)) return r <= 32 ? kRows16 : r <= 128 ? kRows32 : kRows64;
-    if (r <= (f32 ? 16 : t5 < 256 ? 8 : 2)) return kRows16;
+    const double t = expected_tiles(a, 64, (f32 ? 64 : 128) / (a.swiglu ? 2 : 1));
+    if (t < (f32 ? 128 : 48)) return r <= 32 ? kRows16 : r <= 128 ? kRows32 : kRows64;
+    if (r <= (f32 ? 4 : t < 256 ? 8 : 2)) return kRows16;
   }
-  // float32 is bound by its MFMAs at any tile: the small one balances best
-  return f32 ? kTileSmall : pick_tile(a);
+  // float32 is bound by its MFMAs at any tile: a small one balances best (64 x
+  // 64 against 64 x 128: 20-40 % less time up to 1000 tiles, the same beyond)
+  return f32 ? kTileF32 : pick_tile(a);
 }
-bool expert_matmul_grid_fits(const ExpertMatmulArgs& a) {
+bool expert_matmul_fits(const ExpertMatmulArgs& a) {
+  // a tile's offsets within W are 32 bits
+  if (a.n > 1 << 22 || a.k > 1 << 22) return false;
   if (a.M == 0) return true;
   const ProductForm f = pick_form(a);
   return form_blocks(a, f) < (1ll << 32) / form_shape(f, a.swiglu).threads;
@@ -981,8 +1007,13 @@ static hipError_t run_form(const ExpertMatmulArgs& a, hipStream_t s) {
     else if (f == kTileMid)
       expert_product_kernel<Op, TO, QT, SW, 128, 128, 2, 2, 4><<<nb, nt, 0, s>>>(a);
   }
-  if (f == kTileSmall)
-    expert_product_kernel<Op, TO, QT, SW, 64, 128, 2, 2, 4><<<nb, nt, 0, s>>>(a);
+  if constexpr (Op::kBytes == 4) {
+    if (f == kTileF32)
+      expert_product_kernel<Op, TO, QT, SW, 64, 64, 4, 1, 4><<<nb, nt, 0, s>>>(a);
+  } else {
+    if (f == kTileSmall)
+      expert_product_kernel<Op, TO, QT, SW, 64, 128, 2, 2, 4><<<nb, nt, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 template <class Op, typename TO>
@@ -1026,7 +1057,9 @@ static WgradPlan plan_wgrad(int bf16, int M, int E, int n, int k) {
   else if (bf16 && units * tiles(128) >= 256) p.tile = 128;
   const long long t = tiles(p.tile), round = p.tile == 256 ? 256 : p.tile == 128 ? 512 : 1024;
   if (M > 0 && used * t < 4 * round) {
-    long long part = (M * t + round - 1) / round;
+    // one large tile per CU: room in the round for every expert's short part
+    const long long full = p.tile == 256 ? round - used * t / 2 : 0;
+    long long part = (M * t + round - 1) / (full > round / 4 ? full : round);
     if (part < least) part = least;
     part = (part + 127) / 128 * 128;
     if (part < M) {

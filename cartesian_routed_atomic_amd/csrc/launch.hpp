@@ -147,8 +147,8 @@ struct ExpertWgradArgs {
   int part, slots;  // set by the launch: tasks of a part (0: no parts), partial sums
   float* partial;   // [slots, n, k]
 };
-// work-items of a launch dimension are counted in 32 bits
-bool expert_matmul_grid_fits(const ExpertMatmulArgs& a);
+// work-items of a launch dimension, and offsets within a tile, are 32 bits
+bool expert_matmul_fits(const ExpertMatmulArgs& a);
 bool expert_wgrad_grid_fits(const ExpertWgradArgs& a);
 hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s);
 // ws: expert_wgrad_ws_bytes of them, partial sums of experts cut into parts

@@ -483,8 +483,8 @@ typedef enum omni_activation {
  * [E + 1] int32; out [Ro, n] of dt (transpose: [Ro, k]); x_row, out_row [M]
  * int32 or NULL.  Sums are float32, rounded once to dt.
  * Requires M, R, Ro >= 0, E, n, k >= 1; k (transpose: n and k) a multiple of
- * 8 (bf16) or 4 (float32), else UNSUPPORTED, as is a launch of 2^32
- * work-items or more; x, w, out 16-byte aligned.  transpose with SWIGLU is
+ * 8 (bf16) or 4 (float32), else UNSUPPORTED, as are n or k past 2^22 and a
+ * launch of 2^32 work-items or more; x, w, out 16-byte aligned.  transpose with SWIGLU is
  * INVALID_ARG.  M == 0 enqueues nothing.  Deterministic.
  */
 omni_status omni_expert_matmul(omni_dtype dt, int M, int E, int n, int k, int R, int Ro,

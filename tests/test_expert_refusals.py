@@ -27,6 +27,8 @@ def test_expert_matmul_argument_checks():
     assert call(dt=0, k=6) == UNS                  # float32 rows of 4
     assert call(n=12, tr=1) == UNS
     assert call(M=1 << 30, R=1 << 30, Ro=1 << 30, n=1 << 20) == UNS  # work-items past 32 bits
+    assert call(n=(1 << 22) + 1) == UNS
+    assert call(k=(1 << 22) + 8) == UNS
     assert call(M=0, R=0, Ro=0, x=None, out=None) == OK
 
 
