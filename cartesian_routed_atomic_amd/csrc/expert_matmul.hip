@@ -419,7 +419,14 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + 
 
 // ------------------------------------------------------------------ the product
 
-// Tile BM tasks x BN columns, WM x WN waves, ring of S stages.
+// Tile BM tasks x BN columns, WM x WN waves, ring of S stages.  MFMA-bound with
+// many rows per expert: 256 x 256 tiles of waves with 128 x 64 each read 12 KiB
+// of fragments from LDS per 32 MFMAs, which the LDS just keeps up with (tiles
+// of 64 x 64 per wave read 16 KiB); the matrix cores are busy 56 % of the
+// kernel's cycles and the card lowers its clock under them.  65536 tasks of 61
+// experts, 1408 x 2048, bf16: 390 us, 0.96 PFLOP/s; 8192 x 8192 x 8192: 829 us,
+// 1.33 PFLOP/s (int8 439 us, 2.5 POP/s).  HBM-bound with few rows: 2048 tasks of
+// 64 experts, 2 x 704 x 2048, 64 x 128 tiles: 78 us, 4.8 TB/s.
 // QT: W is read as [contraction][columns] (the input gradient).
 // SWIGLU: every 64 columns of Q are 32 gate rows, then the same 32 up rows.
 template <class Op, typename TO, bool QT, bool SWIGLU, int BM, int BN, int WM, int WN, int S>
@@ -640,10 +647,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
   using Acc = typename Op::Acc;
   constexpr int NW = WM * WN, KE = 64 / Op::kBytes;
   constexpr int TI = BM / WM / 16, TJ = BN / WN / 16;
-  constexpr int TASK = (BM + BN) * Op::kBytes;  // bytes of a task in a stage
-  constexpr int STAGE = KE * TASK;
+  constexpr int ROW = (BM + BN) * Op::kBytes;  // bytes of a task in a stage
+  constexpr int STAGE = KE * ROW;
   constexpr int I = STAGE / 1024 / NW;          // loads per wave and stage
-  constexpr int TPI = 1024 / TASK;              // tasks of a load
+  constexpr int TPI = 1024 / ROW;               // tasks of a load
   constexpr int NT = I * TPI;                   // tasks of a wave and stage
   static_assert(TPI >= 1 && I >= 1 && I * NW * 1024 == STAGE, "loads split evenly");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE];
@@ -685,7 +692,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
 
   // This lane's part of a load: which of the load's rows, and where in it.  The
   // tasks of a wave's load u are TPI (wv I + u) .. + TPI - 1 of the stage.
-  const int sub = l * 16 / TASK, in = l * 16 % TASK;
+  const int sub = l * 16 / ROW, in = l * 16 % ROW;
   const bool is_x = in >= BM * Op::kBytes;
   const int pos = is_x ? in - BM * Op::kBytes : in;  // byte in its operand's part of the row
   const uint32_t limit = is_x ? a.R : a.Ry;
@@ -737,10 +744,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
   int wm, wn;
   wave_place<WM, WN>(wv, wm, wn);
   auto read_p = [&](int kt, int i) {
-    return frag_strided<Op, BM, TASK>(smem + (kt % S) * STAGE, wm * (BM / WM) + i * 16, l);
+    return frag_strided<Op, BM, ROW>(smem + (kt % S) * STAGE, wm * (BM / WM) + i * 16, l);
   };
   auto read_q = [&](int kt, int j) {
-    return frag_strided<Op, BN, TASK>(smem + (kt % S) * STAGE + BM * Op::kBytes,
+    return frag_strided<Op, BN, ROW>(smem + (kt % S) * STAGE + BM * Op::kBytes,
                                       wn * (BN / WN) + j * 16, l);
   };
   Acc acc[TI][TJ] = {};
@@ -797,6 +804,11 @@ __global__ __launch_bounds__(256) void expert_wgrad_reduce_kernel(ExpertWgradArg
 // KS waves: both operands go from memory to the MFMA's registers, U stages of
 // 64 bytes ahead, and the waves' sums are added through LDS in wave order.
 // SWIGLU: the first CT / 2 column tiles are gate rows, the others their up rows.
+// Bound by HBM latency and bandwidth: no barrier stands between a wave's loads,
+// and splitting the contraction gives one token's eight experts 2816 waves.
+// That token's gate and up halves (2 x 704 x 2048, bf16, 46 MB): 12 us, 3.8 TB/s,
+// of which about 4 us are the launch and finding the tile; 4 or 8 waves and 2 to
+// 16 stages ahead measure the same.
 template <class Op, typename TO, bool SWIGLU, int RT, int CT, int KS, int U>
 __global__ __launch_bounds__(KS * 64) void expert_rows_kernel(ExpertMatmulArgs a) {
   using Frag = typename Op::Frag;
@@ -941,10 +953,10 @@ static long long form_blocks(const ExpertMatmulArgs& a, ProductForm f) {
 // large tile needs less LDS and L2 traffic per MFMA, a small one wastes less
 // where there are few tiles or few rows.  Fitted to (us, 2048 inputs):
 //   tiles of 256 x 256       64 (int8)  128 (int8)  80    144   1700
-//   256 x 256                30         32          28    29    407
-//   128 x 256                21         25          20    36    499
-//   128 x 128                17         27          22    32    503
-//   64 x 128                 19         32          23    34    712
+//   256 x 256                30         32          28    30    425
+//   128 x 256                21         25          20    37    490
+//   128 x 128                17         27          22    34    518
+//   64 x 128                 19         32          23    34    650
 static ProductForm pick_tile(const ExpertMatmulArgs& a) {
   const int h = a.swiglu ? 2 : 1;
   const double t1 = expected_tiles(a, 256, 256 / h), t2 = expected_tiles(a, 128, 256 / h),

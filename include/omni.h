@@ -22,6 +22,13 @@
  *                           expert-centric or token-centric (same result);
  *   5. omni_routed_backward gradients of the whole routed layer.
  *
+ * Next to them: the shared dense MLP (omni_shared_mlp), variants
+ * (omni_atomic_forward_glu, omni_flat_router_topk), and experts that are
+ * matrices, with the same schedule: their ragged products and gradients
+ * (omni_expert_matmul, omni_expert_weight_grad), the combination of a token's
+ * experts (omni_expert_combine) and products in 8-bit integers
+ * (omni_quantize_rows, omni_quantized_matmul, omni_quantized_expert_matmul).
+ *
  * Conventions shared by every call
  *   - All pointers except the `omni_schedule` descriptor itself are DEVICE
  *     pointers owned by the caller.  The library never allocates, frees or
