@@ -474,7 +474,7 @@ omni_status omni_expert_weight_grad(omni_dtype dt, int M, int E, int n, int k, i
   if (n % unit != 0 || k % unit != 0) return OMNI_ERR_UNSUPPORTED;
   const omni::ExpertWgradArgs a = {dt == OMNI_BF16, M,       E,  n, k,      R, Ry, x, x_row, dy,
                                    dy_row,          offsets, dw, 0, 0, nullptr};
-  if (!omni::expert_wgrad_grid_fits(a)) return OMNI_ERR_UNSUPPORTED;
+  if (!omni::expert_wgrad_fits(a)) return OMNI_ERR_UNSUPPORTED;
   const size_t need = omni_expert_weight_grad_workspace(dt, M, E, n, k);
   if (need > 0 && (!ws || ws_bytes < need || !aligned256(ws))) return OMNI_ERR_WORKSPACE;
   return hip_status(omni::launch_expert_wgrad(a, static_cast<float*>(ws), stream));

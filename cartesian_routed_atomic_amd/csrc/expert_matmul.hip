@@ -181,7 +181,7 @@ __device__ __forceinline__ TilePlace my_tile(const ExpertMatmulArgs& a, int bm, 
 __device__ __forceinline__ int swz_p(int r) { return (r >> 1) & 3; }
 __device__ __forceinline__ int swz_q(int r) { return ((r >> 1) & 1) | ((r >> 2) & 2); }
 // A stage of an operand whose contraction is strided: one row of `cols`
-// elements per contraction step, 16-byte chunk c of step kk at c ^ swz_t<Op>(kk).
+// elements per contraction step, 16-byte chunk c of step kk at c ^ swz_cols(kk).
 // bf16: the eight steps 0-3, 8-11 that half a transposing read takes at once
 // land on eight 32-byte slots; float32: the steps 4 g + j of a read on four
 // 64-byte slots.
@@ -238,46 +238,53 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
       (__attribute__((address_space(3))) const void*)(p)));
 }
 
-// fragment of a K-contiguous stage: row r, chunk g
-template <class Op, bool Q>
-__device__ __forceinline__ typename Op::Frag frag_rows(const uint8_t* st, int r, int g) {
-  return *reinterpret_cast<const typename Op::Frag*>(
-      st + r * 64 + ((g ^ (Q ? swz_q(r) : swz_p(r))) << 4));
+// A fragment is read at the ring's address of its stage plus an offset that the
+// lane keeps for the whole tile (and that the compiler is kept from taking
+// apart again: one addition per fragment and stage instead of two or three).
+// Fragments whose swizzle is the same are constants apart.
+template <class Frag>
+__device__ __forceinline__ Frag lds_read(uint32_t at) {
+  return *(__attribute__((address_space(3))) const Frag*)static_cast<uintptr_t>(at);
 }
-// fragment of a strided stage: columns c0 .. c0 + 15, this lane's steps
-// (rows of COLS elements, ROW bytes apart)
-template <int COLS, int ROW>
-__device__ __forceinline__ bf16x8 frag_cols_bf16(const uint8_t* st, int c0, int l) {
-  // a transposing read: lane 4 r + c of 16 names the 8 bytes of step r,
-  // columns 4 c .. 4 c + 3, lane i receives the four steps of column i
-  const int i = l & 15, g = l >> 4;
-  s16x4 v[2];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int kk = g * 8 + u * 4 + (i >> 2);
-    const int chunk = (c0 >> 3) + ((i & 3) >> 1);
-    const uint8_t* p = st + kk * ROW + ((chunk ^ swz_cols<Bf16Op, COLS>(kk)) << 4) + (i & 1) * 8;
-    v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (__attribute__((address_space(3))) s16x4*)(p));
-  }
-  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-}
-template <int COLS, int ROW>
-__device__ __forceinline__ f32x4 frag_cols_f32(const uint8_t* st, int c0, int l) {
-  const int c = c0 + (l & 15), g = l >> 4;
-  f32x4 v;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int kk = 4 * g + j;
-    v[j] = *reinterpret_cast<const float*>(
-        st + kk * ROW + (((c >> 2) ^ swz_cols<F32Op, COLS>(kk)) << 4) + (c & 3) * 4);
-  }
+__device__ __forceinline__ uint32_t kept(uint32_t v) {
+  __asm__("" : "+v"(v));
   return v;
 }
+// K-contiguous stage: row r, chunk g
+template <bool Q>
+__device__ __forceinline__ uint32_t row_offset(int r, int g) {
+  return kept(r * 64 + ((g ^ (Q ? swz_q(r) : swz_p(r))) << 4));
+}
+// Strided stage, rows of COLS elements, ROW bytes apart: columns c0 .. c0 + 15.
+// bf16: a transposing read; lane 4 r + c of 16 names the 8 bytes of step r,
+// columns 4 c .. 4 c + 3, and lane i receives the four steps of column i (the
+// second read, four steps on, has the same swizzle).  float32: the lane's
+// column at its first step; its others are ROW apart with the same swizzle.
 template <class Op, int COLS, int ROW>
-__device__ __forceinline__ typename Op::Frag frag_strided(const uint8_t* st, int c0, int l) {
-  if constexpr (Op::kBytes == 2) return frag_cols_bf16<COLS, ROW>(st, c0, l);
-  else return frag_cols_f32<COLS, ROW>(st, c0, l);
+__device__ __forceinline__ uint32_t column_offset(int c0, int l) {
+  const int i = l & 15, g = l >> 4;
+  if constexpr (Op::kBytes == 2) {
+    const int kk = g * 8 + (i >> 2), chunk = (c0 >> 3) + ((i & 3) >> 1);
+    return kept(kk * ROW + ((chunk ^ swz_cols<Op, COLS>(kk)) << 4) + (i & 1) * 8);
+  } else {
+    const int c = c0 + i, kk = 4 * g;
+    return kept(kk * ROW + (((c >> 2) ^ swz_cols<Op, COLS>(kk)) << 4) + (c & 3) * 4);
+  }
+}
+template <class Op, int ROW>
+__device__ __forceinline__ typename Op::Frag read_column(uint32_t at) {
+  if constexpr (Op::kBytes == 2) {
+    typedef __attribute__((address_space(3))) s16x4* Lds;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)static_cast<uintptr_t>(at));
+    const s16x4 b =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)static_cast<uintptr_t>(at + 4 * ROW));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  } else {
+    f32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = lds_read<float>(at + j * ROW);
+    return v;
+  }
 }
 
 // The pipeline of a tile: a ring of S stages in LDS, filled by direct
@@ -519,17 +526,23 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
   const int fr = l & 15, g = l >> 4;
   int wm, wn;
   wave_place<WM, WN>(wv, wm, wn);
+  const uint32_t poff = row_offset<false>(wm * (BM / WM) + fr, g);
+  uint32_t toff[QT ? TJ : 1];
+  if constexpr (QT) {
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+      toff[j] = column_offset<Op, BN, BN * Op::kBytes>(wn * (BN / WN) + j * 16, l);
+  } else {
+    toff[0] = row_offset<true>(wn * (BN / WN) + (fr >> 2) * 8 + (fr & 3), g);
+  }
+  using Frag = typename Op::Frag;
   auto read_p = [&](int kt, int i) {
-    return frag_rows<Op, false>(smem + (kt % S) * STAGE, wm * (BM / WM) + i * 16 + fr, g);
+    return lds_read<Frag>(ring + (kt % S) * STAGE + poff + i * 16 * 64);
   };
   auto read_q = [&](int kt, int j) {
-    const uint8_t* st = smem + (kt % S) * STAGE + BM * 64;
-    const int c = wn * (BN / WN);
-    if constexpr (QT)
-      return frag_strided<Op, BN, BN * Op::kBytes>(st, c + j * 16, l);
-    else
-      return frag_rows<Op, true>(st, c + (j >> 1) * 32 + (j & 1) * 4 + (fr >> 2) * 8 + (fr & 3),
-                                 g);
+    const uint32_t st = ring + (kt % S) * STAGE + BM * 64;
+    if constexpr (QT) return read_column<Op, BN * Op::kBytes>(st + toff[j]);
+    else return lds_read<Frag>(st + toff[0] + ((j >> 1) * 32 + (j & 1) * 4) * 64);
   };
   Acc acc[TI][TJ] = {};
   const bool active = t.m0 + wm * (BM / WM) < t.m1 && n0 + wn * (BNO / WN) < N;
@@ -743,12 +756,18 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
   const int fr = l & 15, g = l >> 4;
   int wm, wn;
   wave_place<WM, WN>(wv, wm, wn);
+  uint32_t poff[TI], toff[TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+    poff[i] = column_offset<Op, BM, ROW>(wm * (BM / WM) + i * 16, l);
+#pragma unroll
+  for (int j = 0; j < TJ; ++j)
+    toff[j] = column_offset<Op, BN, ROW>(wn * (BN / WN) + j * 16, l);
   auto read_p = [&](int kt, int i) {
-    return frag_strided<Op, BM, ROW>(smem + (kt % S) * STAGE, wm * (BM / WM) + i * 16, l);
+    return read_column<Op, ROW>(ring + (kt % S) * STAGE + poff[i]);
   };
   auto read_q = [&](int kt, int j) {
-    return frag_strided<Op, BN, ROW>(smem + (kt % S) * STAGE + BM * Op::kBytes,
-                                      wn * (BN / WN) + j * 16, l);
+    return read_column<Op, ROW>(ring + (kt % S) * STAGE + BM * Op::kBytes + toff[j]);
   };
   Acc acc[TI][TJ] = {};
   if (nk > 0) {
@@ -1090,7 +1109,8 @@ static long long wgrad_blocks(const ExpertWgradArgs& a, int tile) {
 size_t expert_wgrad_ws_bytes(int bf16, int M, int E, int n, int k) {
   return static_cast<size_t>(plan_wgrad(bf16, M, E, n, k).slots) * n * k * 4;
 }
-bool expert_wgrad_grid_fits(const ExpertWgradArgs& a) {
+bool expert_wgrad_fits(const ExpertWgradArgs& a) {
+  if (a.n > 1 << 22 || a.k > 1 << 22) return false;  // row lengths in bytes are 32 bits
   ExpertWgradArgs b = a;
   const WgradPlan p = plan_wgrad(a.bf16, a.M, a.E, a.n, a.k);
   b.part = p.part;

@@ -149,7 +149,7 @@ struct ExpertWgradArgs {
 };
 // work-items of a launch dimension, and offsets within a tile, are 32 bits
 bool expert_matmul_fits(const ExpertMatmulArgs& a);
-bool expert_wgrad_grid_fits(const ExpertWgradArgs& a);
+bool expert_wgrad_fits(const ExpertWgradArgs& a);
 hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s);
 // ws: expert_wgrad_ws_bytes of them, partial sums of experts cut into parts
 size_t expert_wgrad_ws_bytes(int bf16, int M, int E, int n, int k);

@@ -509,9 +509,9 @@ omni_status omni_expert_matmul(omni_dtype dt, int M, int E, int n, int k, int R,
  * A task with either row out of range adds nothing.  ws / ws_bytes: at
  * least omni_expert_weight_grad_workspace(...) bytes, 256-byte aligned, or
  * NULL with 0 when that is 0 (few tiles of dw: experts with many tasks are cut
- * into parts, whose partial sums it holds).  Requires n and k multiples of 8
- * (bf16) or 4 (float32), else UNSUPPORTED, as is a launch of 2^32 work-items or
- * more; x, dy, dw 16-byte aligned.  Deterministic: every sum runs in a fixed
+ * into parts, whose partial sums it holds; one workspace serves one call at a
+ * time).  Requires n and k multiples of 8 (bf16) or 4 (float32) up to 2^22, else
+ * UNSUPPORTED, as is a launch of 2^32 work-items or more; x, dy, dw 16-byte aligned.  Deterministic: every sum runs in a fixed
  * order, in float32.
  */
 size_t omni_expert_weight_grad_workspace(omni_dtype dt, int M, int E, int n, int k);

@@ -46,6 +46,8 @@ def test_expert_weight_grad_argument_checks():
     assert call(k=12) == UNS
     assert call(dt=0, n=6) == UNS
     assert call(E=1 << 30, n=1 << 15, k=1 << 15) == UNS
+    assert call(n=(1 << 22) + 8) == UNS
+    assert call(k=(1 << 22) + 8) == UNS
     # few tiles, many tasks: partial sums in a workspace
     need = B.lib().omni_expert_weight_grad_workspace
     assert need(1, 4, 2, 8, 16) == 0 and need(2, 4, 2, 8, 16) == 0 and need(1, 4, 2, 0, 16) == 0
