@@ -1071,7 +1071,8 @@ hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s) {
 //   1 expert, 512 x 512, 8192 tasks, bf16                26 / 32 / 41
 //   100 experts, 256 x 1024, 4 tasks each, bf16          41 / 29 / 36
 //   16 experts, 512 x 512, 500 tasks each, float32       73 / 139 / -
-// Parts where the tiles are fewer than four times those that run at a time:
+// Parts where the tiles are fewer than four times those that run at a time and
+// experts have tasks enough (half a part's on average):
 // long enough that one round of them holds all tasks, and at least 32 stages
 // (their partial sums and the second launch cost about what 30 stages do).
 struct WgradPlan {
@@ -1087,7 +1088,7 @@ static WgradPlan plan_wgrad(int bf16, int M, int E, int n, int k) {
   if (bf16 && units * tiles(256) >= 192 && M >= 64 * used) p.tile = 256;
   else if (bf16 && units * tiles(128) >= 256) p.tile = 128;
   const long long t = tiles(p.tile), round = p.tile == 256 ? 256 : p.tile == 128 ? 512 : 1024;
-  if (M > 0 && used * t < 4 * round) {
+  if (M >= used * least / 2 && M > 0 && used * t < 4 * round) {
     // one large tile per CU: room in the round for every expert's short part
     const long long full = p.tile == 256 ? round - used * t / 2 : 0;
     long long part = (M * t + round - 1) / (full > round / 4 ? full : round);

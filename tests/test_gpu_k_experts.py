@@ -210,7 +210,7 @@ def test_expert_weight_grad_large_tiles(counts, n, k):
 @pytest.mark.parametrize("counts,n,k", [
     ([3000], 72, 136),                        # one expert in parts, ragged last part
     ([0, 2500, 0, 1024, 1025, 1, 300, 0], 64, 64),  # parts, one part, none
-    ([i * 7 % 90 + (3100 if i % 50 == 1 else 0) for i in range(130)], 24, 16),  # > 64 lanes
+    ([490 + i * 7 % 90 + (3100 if i % 50 == 1 else 0) for i in range(130)], 24, 16),  # > 64 lanes
     ([5000, 40, 17], 640, 520)])
 def test_expert_weight_grad_in_parts(counts, n, k, dt):
     rng = np.random.default_rng(6)
