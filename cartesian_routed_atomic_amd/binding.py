@@ -503,10 +503,11 @@ def routed_backward(x, wr_t, wc_t, w, v, expert_idx, gate, dy, out=None, workspa
 def _tensors(dev, *specs):
     """Check (tensor, name, dtype, shape) of arguments on device index dev."""
     for t, name, dtype, shape in specs:
-        if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
-                or not t.is_contiguous()):
-            _req(t, name, dtype, shape)
-            raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            continue
+        _req(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
 
 
 def _device_of(t, name):
@@ -526,7 +527,7 @@ def _call(fn, dev, stream, *args):
     else:
         raw = stream.cuda_stream
     f = getattr(_lib or lib(), fn)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         code = f(*args, raw)
     else:
         with torch.cuda.device(dev):
