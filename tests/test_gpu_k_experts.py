@@ -412,6 +412,22 @@ def test_values_of_no_task_do_not_matter():
 
 
 @gpu
+def test_thousands_of_experts():
+    rng = np.random.default_rng(23)
+    counts = rng.integers(0, 3, 3001)
+    counts[[0, 700, 3000]] = [0, 400, 90]
+    n, k, off = 24, 40, offsets(counts)
+    M = int(off[-1])
+    x, w, dy = rand(rng, (M, k), "bf16"), rand(rng, (3001, n, k), "bf16"), rand(rng, (M, n), "bf16")
+    want, mass = OE.expert_matmul_f64(x, w, off, M, np.zeros((M, n)))
+    close(host(B.expert_matmul(dev(x), dev(w), dev(off))), want, sum_tol(k, mass, want, "bf16"),
+          "out")
+    want, mass = OE.expert_weight_grad_f64(x, dy, off, M)
+    close(host(B.expert_weight_grad(dev(x), dev(dy), dev(off))), want,
+          sum_tol(400, mass, want, "f32"), "dw")
+
+
+@gpu
 def test_no_tasks():
     x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     w = torch.ones((3, 32, 64), dtype=torch.bfloat16, device="cuda")
