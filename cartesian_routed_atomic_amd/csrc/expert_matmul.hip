@@ -652,8 +652,9 @@ __device__ __forceinline__ int first_slot(const int32_t* off, int E, int M, int 
 // loads: the vector-memory counter stays with the ring), and the address work
 // is kept to a few instructions per load: at two waves per SIMD the
 // instructions between the MFMAs are what bounds this kernel: 65536 tasks, 64
-// experts of 1408 x 2048 take 543 us (0.70 PFLOP/s) with 44 scalar and 74
-// vector ones per stage and wave, and took 630 with 105 scalar ones.
+// experts of 1408 x 2048 take 510 us (0.74 PFLOP/s) with 46 scalar and 60
+// vector ones per stage and wave (the whole kernel's by its stages), took 543
+// with 74 vector ones and 630 with 105 scalar ones besides.
 // A row out of range is fetched as zeros, which removes its task's term.
 template <class Op, int BM, int BN, int WM, int WN, int S, bool LISTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgradArgs a) {
@@ -1073,7 +1074,7 @@ hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s) {
 // them for the chip, else the smaller ones; float32, bound by its MFMAs, always
 // takes the smallest, and experts of few tasks, bound by writing dW, not the
 // largest (us, tiles of 64 / 128 / 256):
-//   64 experts, 1408 x 2048, 1024 tasks each, bf16       - / 688 / 543
+//   64 experts, 1408 x 2048, 1024 tasks each, bf16       - / 688 / 510
 //   1 expert, 512 x 512, 8192 tasks, bf16                26 / 32 / 41
 //   100 experts, 256 x 1024, 4 tasks each, bf16          41 / 29 / 36
 //   16 experts, 512 x 512, 500 tasks each, float32       73 / 139 / -
