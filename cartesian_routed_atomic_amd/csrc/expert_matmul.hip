@@ -655,7 +655,8 @@ __device__ __forceinline__ int first_slot(const int32_t* off, int E, int M, int 
 // experts of 1408 x 2048 take 510 us (0.74 PFLOP/s) with 46 scalar and 60
 // vector ones per stage and wave (the whole kernel's by its stages), took 543
 // with 74 vector ones and 630 with 105 scalar ones besides.
-// A row out of range is fetched as zeros, which removes its task's term.
+// Where either row is out of range both are fetched as zeros, which removes the
+// task's term whatever the other row holds.
 template <class Op, int BM, int BN, int WM, int WN, int S, bool LISTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgradArgs a) {
   using Acc = typename Op::Acc;
@@ -709,7 +710,6 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
   const int sub = l * 16 / ROW, in = l * 16 % ROW;
   const bool is_x = in >= BM * Op::kBytes;
   const int pos = is_x ? in - BM * Op::kBytes : in;  // byte in its operand's part of the row
-  const uint32_t limit = is_x ? a.R : a.Ry;
   const uint32_t stride = (is_x ? a.k : a.n) * Op::kBytes;
   const uint8_t* base[I];
 #pragma unroll
@@ -746,11 +746,13 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
     uint32_t row = 0;
 #pragma unroll
     for (int r = 0; r < TPI; ++r) {
-      const uint32_t ry = raw_y[u * TPI + r], rx = raw_x[u * TPI + r], mine = is_x ? rx : ry;
+      uint32_t ry = raw_y[u * TPI + r], rx = raw_x[u * TPI + r];
+      const bool both = ry < static_cast<uint32_t>(a.Ry) && rx < static_cast<uint32_t>(a.R);
+      const uint32_t mine = both ? (is_x ? rx : ry) : ~0u;
       row = r == 0 || sub == r ? mine : row;
     }
     const uint8_t* src = base[u] + static_cast<uint64_t>(row) * stride;
-    load_lds16(row < limit ? src : reinterpret_cast<const uint8_t*>(kZeroChunk),
+    load_lds16(row != ~0u ? src : reinterpret_cast<const uint8_t*>(kZeroChunk),
                ring + (kt % S) * STAGE + (wv * I + u) * 1024);
     if (u == I - 1) fetch_rows(kt + 1, may_end);
   };

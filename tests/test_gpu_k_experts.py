@@ -412,6 +412,33 @@ def test_values_of_no_task_do_not_matter():
 
 
 @gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,n,k", [
+    ([300, 0, 5, 61], 72, 136),
+    ([9] * 40, 520, 264),
+    ([700, 0, 130, 64, 1, 33], 1536, 1280)])
+def test_weight_grad_of_tasks_without_a_row(counts, n, k, dt):
+    """A task with one row out of range adds nothing, whatever its other row holds."""
+    rng = np.random.default_rng(24)
+    off = offsets(counts)
+    M = int(off[-1])
+    x, dy = rand(rng, (M, k), dt), rand(rng, (M, n), dt)
+    xr, yr = rng.permutation(M).astype(np.int32), rng.permutation(M).astype(np.int32)
+    lost = rng.permutation(M)[:M // 3]
+    bad_x, bad_y = lost[::2], lost[1::2]
+    nan, inf = (0x7FC0, 0x7F80) if dt == "bf16" else (np.nan, np.inf)
+    cx, cy = x.copy(), dy.copy()
+    x[xr[bad_y]], dy[yr[bad_x]] = nan, inf
+    cx[xr[bad_y]], cy[yr[bad_x]] = 0, 0
+    xr[bad_x], yr[bad_y] = -1, M
+    want, mass = OE.expert_weight_grad_f64(cx, cy, off, M, xr, yr)
+    dw = B.expert_weight_grad(dev(x), dev(dy), dev(off), x_row=dev(xr), dy_row=dev(yr))
+    tol = sum_tol(max(counts), mass, want, "f32")
+    tol[mass == 0] = 0
+    close(host(dw), want, tol, "dw")
+
+
+@gpu
 def test_thousands_of_experts():
     rng = np.random.default_rng(23)
     counts = rng.integers(0, 3, 3001)
