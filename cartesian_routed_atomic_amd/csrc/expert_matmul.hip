@@ -710,6 +710,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
   const int sub = l * 16 / ROW, in = l * 16 % ROW;
   const bool is_x = in >= BM * Op::kBytes;
   const int pos = is_x ? in - BM * Op::kBytes : in;  // byte in its operand's part of the row
+  const uint32_t limit = is_x ? a.R : a.Ry;
   const uint32_t stride = (is_x ? a.k : a.n) * Op::kBytes;
   const uint8_t* base[I];
 #pragma unroll
@@ -746,13 +747,19 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
     uint32_t row = 0;
 #pragma unroll
     for (int r = 0; r < TPI; ++r) {
-      uint32_t ry = raw_y[u * TPI + r], rx = raw_x[u * TPI + r];
-      const bool both = ry < static_cast<uint32_t>(a.Ry) && rx < static_cast<uint32_t>(a.R);
-      const uint32_t mine = both ? (is_x ? rx : ry) : ~0u;
+      const uint32_t ry = raw_y[u * TPI + r], rx = raw_x[u * TPI + r], mine = is_x ? rx : ry;
       row = r == 0 || sub == r ? mine : row;
     }
     const uint8_t* src = base[u] + static_cast<uint64_t>(row) * stride;
-    load_lds16(row != ~0u ? src : reinterpret_cast<const uint8_t*>(kZeroChunk),
+    // lanes whose row and whose task's other row are in range
+    constexpr int W = BM * Op::kBytes / 16;  // lanes of a task's dy row; as many of its x row
+    static_assert(W == 8 || W == 16 || W == 32, "a wave holds whole tasks");
+    constexpr uint64_t kDy = W == 32 ? 0xffffffffull : W == 16 ? 0x0000ffff0000ffffull
+                                                               : 0x00ff00ff00ff00ffull;
+    const uint64_t in_range = __builtin_amdgcn_ballot_w64(row < limit);
+    const uint64_t both = in_range & in_range >> W & kDy;
+    const bool ok = __builtin_amdgcn_inverse_ballot_w64(both | both << W);
+    load_lds16(ok ? src : reinterpret_cast<const uint8_t*>(kZeroChunk),
                ring + (kt % S) * STAGE + (wv * I + u) * 1024);
     if (u == I - 1) fetch_rows(kt + 1, may_end);
   };
