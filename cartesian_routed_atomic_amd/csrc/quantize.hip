@@ -7,6 +7,9 @@
 // rare (quotients within float32 rounding of a half), so that part runs only
 // where a lane of the wave needs it.
 //
+// The maximum keeps a NaN: a row with a NaN or an infinity has that as its scale
+// and q 0, so that its products are NaN instead of a finite number.
+//
 // HBM-bound: a row is read once, kept in registers and written once.  8192 x
 // 2048 takes 15.1 us from bf16 (3.3 TB/s; the VALU work per element is as long
 // as the loads) and 16.1 us from float32 (5.2 TB/s).
@@ -86,7 +89,7 @@ __device__ __forceinline__ void store_unit(int8_t* p, const float (&x)[kUnit], c
     t[i] = __float_as_uint(m);
     worst = fmaxf(worst, fabsf(fmaf(kMagic - m, s.s, x[i])));
   }
-  if (__any(worst >= 0.5f * s.s || s.lift != 1.f)) {
+  if (__any(!(worst < 0.5f * s.s) || s.lift != 1.f)) {  // a NaN scale as well
     exact_unit(x, s, w);
   } else {
 #pragma unroll
@@ -101,7 +104,7 @@ __device__ __forceinline__ void store_unit(int8_t* p, const float (&x)[kUnit], c
 
 __device__ __forceinline__ float unit_max(const float (&v)[kUnit], float top) {
 #pragma unroll
-  for (int i = 0; i < kUnit; ++i) top = fmaxf(top, fabsf(v[i]));
+  for (int i = 0; i < kUnit; ++i) top = __builtin_elementwise_maximum(top, fabsf(v[i]));
   return top;
 }
 
@@ -136,11 +139,13 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* __restrict_
       top = unit_max(v[0], top);
     }
   }
-  top = wave_max(top);
+  const bool any_nan = __any(top != top);
+  top = any_nan ? __builtin_nanf("") : wave_max(top);
   if constexpr (NT > kWave) {
     if (lane() == 0) part[threadIdx.x >> 6] = top;
     __syncthreads();
-    top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    top = __builtin_elementwise_maximum(__builtin_elementwise_maximum(part[0], part[1]),
+                                        __builtin_elementwise_maximum(part[2], part[3]));
   }
   const RowScale s = row_scale(top);
   if (t == 0) scale[row] = s.s;

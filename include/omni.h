@@ -556,7 +556,9 @@ omni_status omni_expert_combine_backward(omni_dtype dt, int L, int K, int n, con
  *
  *   scale[r] = max_c |x[r, c]| / 127 (float32),  q[r, c] = x[r, c] / scale[r]
  *   rounded to the nearest integer (ties to even, of the exact quotient),
- *   within [-127, 127]; rows of zeros have scale 0 and q 0
+ *   within [-127, 127]; rows of zeros have scale 0 and q 0, rows with a NaN or
+ *   an infinity have that as their scale (NaN first) and q 0: their products
+ *   are NaN
  *
  * x [R, k] of dt, q [R, k] int8, scale [R] float32.  Activations are rows of
  * tokens, weights rows of output channels.  Requires k a multiple of 16, else

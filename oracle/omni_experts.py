@@ -110,13 +110,14 @@ def expert_combine_backward_f64(o, gate, dy):
 def quantize_rows(x):
     """(q int8, scale float32): scale = max|row| / 127 rounded to float32, q the
     integer nearest to the exact quotient, ties to even, decided with whole
-    numbers: both operands are float32, so 2^k multiples of integers."""
+    numbers: both operands are float32, so 2^k multiples of integers.  A row with
+    a NaN or an infinity has that as its scale and q 0."""
     x = np.asarray(widen(x), dtype=np.float32)
     scale = (np.abs(x).max(axis=1).astype(np.float64) / 127.0).astype(np.float32)
     q = np.zeros(x.shape, dtype=np.int8)
     for r in range(x.shape[0]):
         s = float(scale[r])
-        if s == 0.0:
+        if s == 0.0 or not np.isfinite(s):
             continue
         for c in range(x.shape[1]):
             xn, xd = float(x[r, c]).as_integer_ratio()

@@ -322,6 +322,31 @@ def test_quantize_rows(R, k, dt):
     np.testing.assert_array_equal(host(gq), q)
 
 
+@gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [16, 1040, 2064, 4112, 8208, 16400])
+def test_quantize_rows_not_finite(k, dt):
+    """A NaN or an infinity anywhere in a row is its scale, q is 0 and a product
+    with the row is NaN; the rows beside it are as ever."""
+    rng = np.random.default_rng(k)
+    x = rng.standard_normal((9, k)).astype(np.float32)
+    x[1, 0], x[3, k - 1], x[5, k // 2], x[7, 0], x[7, k - 1] = np.nan, np.inf, -np.inf, np.inf, np.nan
+    if dt == "f32":
+        x[8, k // 3] = np.array([0xFFFFFFFF], np.uint32).view(np.float32)[0]
+        xd = x
+    else:
+        xd = f32_to_bf16_bits(x)
+        xd[1, 0] = xd[7, k - 1] = 0x7FFF
+    q, s = OE.quantize_rows(xd)
+    assert np.isnan(s[[1, 7]]).all() and np.isinf(s[[3, 5]]).all() and not q[[1, 3, 5, 7]].any()
+    gq, gs = B.quantize_rows(dev(xd))
+    np.testing.assert_array_equal(host(gs), s)
+    np.testing.assert_array_equal(host(gq), q)
+    y = B.quantized_matmul(gq, gs, dev(np.ones((8, k), np.int8)), dev(np.ones(8, np.float32)),
+                           out_dtype=torch.float32)
+    np.testing.assert_array_equal(np.isnan(host(y)).all(axis=1), ~np.isfinite(s))
+
+
 def q_tol(mass, want, dt, swiglu):
     t = 4 * 2.0 ** -24 * mass + HALF[dt] * np.abs(want) * 1.001 + 1e-38
     return t + 2.0 ** -16 * np.abs(want) if swiglu else t

@@ -118,3 +118,10 @@ def test_ties_go_to_even():
     q, s = OE.quantize_rows(x)
     assert s[0] == 1.0
     np.testing.assert_array_equal(q[0], [127, 0, 2, 2, 0, -2, -2, 3])
+
+
+def test_rows_that_are_not_finite():
+    x = np.array([[1, np.nan, 2, np.inf], [1, -np.inf, 2, 3], [1, 0, 0, 2]], dtype=np.float32)
+    q, s = OE.quantize_rows(x)
+    assert np.isnan(s[0]) and s[1] == np.inf and not q[:2].any()
+    np.testing.assert_array_equal(q[2], [64, 0, 0, 127])   # 1 / scale = 63.5000002
