@@ -28,7 +28,7 @@ struct Bf16Op {
   using Frag = bf16x8;
   using Acc = f32x4;
   using T = uint16_t;
-  static constexpr int kBytes = 2;
+  static constexpr int kBytes = 2, kSumBlock = 0;
   static __device__ __forceinline__ void mma(Acc& c, Frag q, Frag p) {
     c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q, p, c, 0, 0, 0);
   }
@@ -37,7 +37,7 @@ struct I8Op {
   using Frag = i32x4;
   using Acc = i32x4;
   using T = int8_t;
-  static constexpr int kBytes = 1;
+  static constexpr int kBytes = 1, kSumBlock = 0;
   static __device__ __forceinline__ void mma(Acc& c, Frag q, Frag p) {
     c = __builtin_amdgcn_mfma_i32_16x16x64_i8(q, p, c, 0, 0, 0);
   }
@@ -49,7 +49,7 @@ struct F32Op {
   using Frag = f32x4;
   using Acc = f32x4;
   using T = float;
-  static constexpr int kBytes = 4;
+  static constexpr int kBytes = 4, kSumBlock = 8;
   static __device__ __forceinline__ void mma(Acc& c, Frag q, Frag p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(q[j], p[j], c, 0, 0, 0);
@@ -301,18 +301,37 @@ __device__ __forceinline__ typename Op::Frag read_column(uint32_t at) {
 // ACTIVE false: a wave whose part of the tile is empty; it only loads.
 // The steady loop has no branch between a read and the MFMAs that use it: a
 // join there makes the compiler wait for the reads just issued.
+// float32 sums run in blocks of kSumBlock stages, each added to the total when
+// it is full: a long sum of one accumulator rounds at its own size at every
+// step (3696 steps: 1.1e-6 of the result, a library product 5.5e-7).
 template <class Op, int I, int S, bool ACTIVE, int TI, int TJ, class Issue, class ReadP,
           class ReadQ>
 __device__ __forceinline__ void run_stages(int nk, Issue issue, ReadP read_p, ReadQ read_q,
                                            typename Op::Acc (&acc)[TI][TJ]) {
   using Frag = typename Op::Frag;
   constexpr int H = TI > 1 ? TI / 2 : 1, D = TI > 2 ? TI - 2 : 1;
+  constexpr int kBlock = Op::kSumBlock;
   Frag p0[TI], q0[TJ], p1[TI], q1[TJ];
+  typename Op::Acc block[kBlock ? TI : 1][kBlock ? TJ : 1] = {};
+  auto fold = [&]() {
+    if constexpr (kBlock > 0 && ACTIVE) {
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          acc[i][j] += block[i][j];
+          block[i][j] = typename Op::Acc{};
+        }
+    }
+  };
   auto mma_row = [&](int i, const Frag (&p)[TI], const Frag (&q)[TJ]) {
     if constexpr (!ACTIVE) return;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) Op::mma(acc[i][j], q[j], p[i]);
+    for (int j = 0; j < TJ; ++j) {
+      if constexpr (kBlock > 0) Op::mma(block[i][j], q[j], p[i]);
+      else Op::mma(acc[i][j], q[j], p[i]);
+    }
     __builtin_amdgcn_sched_barrier(0);
   };
   auto read = [&](int kt, int i, int of, Frag (&np)[TI], Frag (&nq)[TJ]) {  // share i of `of`
@@ -352,14 +371,19 @@ __device__ __forceinline__ void run_stages(int nk, Issue issue, ReadP read_p, Re
   };
   read(0, 0, 1, p0, q0);
   int kt = 0;
-  for (; kt + S + 3 < nk; kt += 2) {
-    steady(kt, p0, q0, p1, q1);
-    steady(kt + 1, p1, q1, p0, q0);
+  while (kt + S + 3 < nk) {
+    const int end = kBlock ? min(nk - S - 3, kt + kBlock) : nk - S - 3;
+    for (; kt < end; kt += 2) {
+      steady(kt, p0, q0, p1, q1);
+      steady(kt + 1, p1, q1, p0, q0);
+    }
+    fold();
   }
   for (; kt < nk; kt += 2) {
     tail(kt, p0, q0, p1, q1);
     if (kt + 1 < nk) tail(kt + 1, p1, q1, p0, q0);
   }
+  fold();
 }
 // active: uniform in a wave.  A tile of a ragged expert's last rows or of the
 // last columns leaves waves without work; the other wave of their SIMD then
@@ -652,11 +676,12 @@ __device__ __forceinline__ int first_slot(const int32_t* off, int E, int M, int 
 // loads: the vector-memory counter stays with the ring), and the address work
 // is kept to a few instructions per load: at two waves per SIMD the
 // instructions between the MFMAs are what bounds this kernel: 65536 tasks, 64
-// experts of 1408 x 2048 take 510 us (0.74 PFLOP/s) with 46 scalar and 60
+// experts of 1408 x 2048 take 512 us (0.74 PFLOP/s) with 54 scalar and 60
 // vector ones per stage and wave (the whole kernel's by its stages), took 543
 // with 74 vector ones and 630 with 105 scalar ones besides.
 // Where either row is out of range both are fetched as zeros, which removes the
-// task's term whatever the other row holds.
+// task's term whatever the other row holds: the comparison's lane mask is folded
+// onto both halves of the task (a test of each task's two row numbers took 525 us).
 template <class Op, int BM, int BN, int WM, int WN, int S, bool LISTS>
 __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgradArgs a) {
   using Acc = typename Op::Acc;
@@ -1083,7 +1108,7 @@ hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s) {
 // them for the chip, else the smaller ones; float32, bound by its MFMAs, always
 // takes the smallest, and experts of few tasks, bound by writing dW, not the
 // largest (us, tiles of 64 / 128 / 256):
-//   64 experts, 1408 x 2048, 1024 tasks each, bf16       - / 688 / 510
+//   64 experts, 1408 x 2048, 1024 tasks each, bf16       - / 688 / 512
 //   1 expert, 512 x 512, 8192 tasks, bf16                26 / 32 / 41
 //   100 experts, 256 x 1024, 4 tasks each, bf16          41 / 29 / 36
 //   16 experts, 512 x 512, 500 tasks each, float32       73 / 139 / -
