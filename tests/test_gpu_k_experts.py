@@ -464,6 +464,29 @@ def test_weight_grad_of_tasks_without_a_row(counts, n, k, dt):
 
 
 @gpu
+@pytest.mark.parametrize("steps", [1000, 3424])
+def test_long_float32_sums(steps):
+    """float32 sums of terms of random sign run in blocks of 128 steps (the last
+    up to 240).  A sum's rounding at step i is at most 2^-24 of sqrt(i) terms:
+    over a block of b steps b^2 / 2 in squares, over the totals steps^2 / 256; in
+    all 64 + steps / 256 + 240^2 / (2 steps), relative to the sum's own steps.
+    One accumulator throughout would have steps / 2."""
+    bound = 2.0 ** -24 * (64 + steps / 256 + 240 ** 2 / (2 * steps)) ** 0.5
+    rng = np.random.default_rng(steps)
+    off, M, wide = offsets([150, 170, 90, 200]), 610, 200
+    rel = lambda got, want: np.linalg.norm(host(got) - want) / np.linalg.norm(want)
+    x, w = rand(rng, (M, steps), "f32"), rand(rng, (4, wide, steps), "f32")
+    want, _ = OE.expert_matmul_f64(x, w, off, M, np.zeros((M, wide)))
+    assert rel(B.expert_matmul(dev(x), dev(w), dev(off)), want) <= bound
+    w = np.ascontiguousarray(w.transpose(0, 2, 1))
+    want, _ = OE.expert_matmul_f64(x, w, off, M, np.zeros((M, wide)), transpose=True)
+    assert rel(B.expert_matmul(dev(x), dev(w), dev(off), transpose=True), want) <= bound
+    x, dy = rand(rng, (steps, 64), "f32"), rand(rng, (steps, 72), "f32")
+    want, _ = OE.expert_weight_grad_f64(x, dy, [0, steps], steps)
+    assert rel(B.expert_weight_grad(dev(x), dev(dy), dev(offsets([steps]))), want) <= bound
+
+
+@gpu
 def test_thousands_of_experts():
     rng = np.random.default_rng(23)
     counts = rng.integers(0, 3, 3001)
