@@ -11,6 +11,8 @@
 // (32 bf16, 64 int8 or 16 float32) of both.  Q is the MFMA's first operand and
 // P its second, so a lane holds four consecutive columns of one output row and
 // stores them without a pass through LDS.
+#include <type_traits>
+
 #include "device.hpp"
 #include "launch.hpp"
 
@@ -301,9 +303,12 @@ __device__ __forceinline__ typename Op::Frag read_column(uint32_t at) {
 // ACTIVE false: a wave whose part of the tile is empty; it only loads.
 // The steady loop has no branch between a read and the MFMAs that use it: a
 // join there makes the compiler wait for the reads just issued.
-// float32 sums run in blocks of kSumBlock stages, each added to the total when
-// it is full: a long sum of one accumulator rounds at its own size at every
-// step (3696 steps: 1.1e-6 of the result, a library product 5.5e-7).
+// float32 sums run in blocks of kSumBlock stages, each added to the total as the
+// next begins, tile by tile between the MFMAs: a long sum of one accumulator
+// rounds at its own size at every step (3424 steps: 1.0e-6 of the result, a
+// library product 5.3e-7, blocks 2.3e-7).  That costs 3 % of a short product and
+// 8 % of a long one (22 stages: 10.9 us without, 11.2 with, 11.6 with the blocks
+// added between two stages).
 template <class Op, int I, int S, bool ACTIVE, int TI, int TJ, class Issue, class ReadP,
           class ReadQ>
 __device__ __forceinline__ void run_stages(int nk, Issue issue, ReadP read_p, ReadQ read_q,
@@ -313,24 +318,21 @@ __device__ __forceinline__ void run_stages(int nk, Issue issue, ReadP read_p, Re
   constexpr int kBlock = Op::kSumBlock;
   Frag p0[TI], q0[TJ], p1[TI], q1[TJ];
   typename Op::Acc block[kBlock ? TI : 1][kBlock ? TJ : 1] = {};
-  auto fold = [&]() {
-    if constexpr (kBlock > 0 && ACTIVE) {
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-          acc[i][j] += block[i][j];
-          block[i][j] = typename Op::Acc{};
-        }
-    }
-  };
-  auto mma_row = [&](int i, const Frag (&p)[TI], const Frag (&q)[TJ]) {
+  // fresh: the first stage of a block
+  auto mma_row = [&](int i, const Frag (&p)[TI], const Frag (&q)[TJ], auto fresh) {
     if constexpr (!ACTIVE) return;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-      if constexpr (kBlock > 0) Op::mma(block[i][j], q[j], p[i]);
-      else Op::mma(acc[i][j], q[j], p[i]);
+      if constexpr (kBlock == 0) {
+        Op::mma(acc[i][j], q[j], p[i]);
+      } else {
+        if constexpr (fresh) {
+          acc[i][j] += block[i][j];
+          block[i][j] = typename Op::Acc{};
+        }
+        Op::mma(block[i][j], q[j], p[i]);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -342,7 +344,7 @@ __device__ __forceinline__ void run_stages(int nk, Issue issue, ReadP read_p, Re
     for (int r = i * TI / of; r < (i + 1) * TI / of; ++r) np[r] = read_p(kt, r);
   };
   auto steady = [&](int kt, const Frag (&p)[TI], const Frag (&q)[TJ], Frag (&np)[TI],
-                    Frag (&nq)[TJ]) {
+                    Frag (&nq)[TJ], auto fresh) {
     wait_vm_lds<(S - 2) * I>();
     lds_barrier();
 #pragma unroll
@@ -352,7 +354,7 @@ __device__ __forceinline__ void run_stages(int nk, Issue issue, ReadP read_p, Re
         for (int u = i * I / H; u < (i + 1) * I / H; ++u) issue(kt + S, u, false);
       }
       if (i < D) read(kt + 1, i, D, np, nq);
-      mma_row(i, p, q);
+      mma_row(i, p, q, fresh);
     }
   };
   auto tail = [&](int kt, const Frag (&p)[TI], const Frag (&q)[TJ], Frag (&np)[TI],
@@ -367,23 +369,33 @@ __device__ __forceinline__ void run_stages(int nk, Issue issue, ReadP read_p, Re
       read(kt + 1, 0, 1, np, nq);
     }
 #pragma unroll
-    for (int i = 0; i < TI; ++i) mma_row(i, p, q);
+    for (int i = 0; i < TI; ++i) mma_row(i, p, q, std::false_type{});
   };
   read(0, 0, 1, p0, q0);
   int kt = 0;
   while (kt + S + 3 < nk) {
-    const int end = kBlock ? min(nk - S - 3, kt + kBlock) : nk - S - 3;
-    for (; kt < end; kt += 2) {
-      steady(kt, p0, q0, p1, q1);
-      steady(kt + 1, p1, q1, p0, q0);
+    int end = nk - S - 3;
+    if constexpr (kBlock > 0) {
+      end = min(end, kt + kBlock);
+      steady(kt, p0, q0, p1, q1, std::true_type{});
+      steady(kt + 1, p1, q1, p0, q0, std::false_type{});
+      kt += 2;
     }
-    fold();
+    for (; kt < end; kt += 2) {
+      steady(kt, p0, q0, p1, q1, std::false_type{});
+      steady(kt + 1, p1, q1, p0, q0, std::false_type{});
+    }
   }
   for (; kt < nk; kt += 2) {
     tail(kt, p0, q0, p1, q1);
     if (kt + 1 < nk) tail(kt + 1, p1, q1, p0, q0);
   }
-  fold();
+  if constexpr (kBlock > 0 && ACTIVE) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] += block[i][j];
+  }
 }
 // active: uniform in a wave.  A tile of a ragged expert's last rows or of the
 // last columns leaves waves without work; the other wave of their SIMD then
@@ -1111,7 +1123,7 @@ hipError_t launch_expert_matmul(const ExpertMatmulArgs& a, hipStream_t s) {
 //   64 experts, 1408 x 2048, 1024 tasks each, bf16       - / 688 / 512
 //   1 expert, 512 x 512, 8192 tasks, bf16                26 / 32 / 41
 //   100 experts, 256 x 1024, 4 tasks each, bf16          41 / 29 / 36
-//   16 experts, 512 x 512, 500 tasks each, float32       73 / 139 / -
+//   16 experts, 512 x 512, 500 tasks each, float32       79 / 139 / -
 // Parts where the tiles are fewer than four times those that run at a time and
 // experts have tasks enough (half a part's on average):
 // long enough that one round of them holds all tasks, and at least 32 stages
