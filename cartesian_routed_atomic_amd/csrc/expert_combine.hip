@@ -57,7 +57,8 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(const T* o, const
   const size_t t = m / K;
   const float g = gate ? gate[m] : 1.f;
   float dot = 0.f;
-  for (int c = lane() * 4; c < n; c += kWave * 4) {
+  // unsigned: rows may have up to 2^31 - 8 columns, and the last step ends past them
+  for (uint32_t c = lane() * 4; c < static_cast<uint32_t>(n); c += kWave * 4) {
     const float4 d = load4(dy + t * n + c);
     store4(dout + m * n + c, make_float4(g * d.x, g * d.y, g * d.z, g * d.w));
     if (dgate) {

@@ -134,7 +134,8 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* __restrict_
 #pragma unroll
     for (int u = 0; u < NV; ++u) top = unit_max(v[u], top);
   } else {
-    for (int c = t * kUnit; c < k; c += NT * kUnit) {
+    // unsigned: rows may have up to 2^31 - 16 columns, and the last step ends past them
+    for (uint32_t c = t * kUnit; c < static_cast<uint32_t>(k); c += NT * kUnit) {
       load_unit(xr + c, v[0]);
       top = unit_max(v[0], top);
     }
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* __restrict_
       if (c < k) store_unit(qr + c, v[u], s);
     }
   } else {
-    for (int c = t * kUnit; c < k; c += NT * kUnit) {
+    for (uint32_t c = t * kUnit; c < static_cast<uint32_t>(k); c += NT * kUnit) {
       load_unit(xr + c, v[0]);
       store_unit(qr + c, v[0], s);
     }
