@@ -144,6 +144,22 @@ def _req(t, name, dtype=None, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _workspace(given, nbytes, like, stream=None):
+    """The caller's workspace if it holds nbytes, else a fresh one (None where none is
+    needed); the kernels take its address, so it has to be memory of like's device."""
+    if given is not None:
+        dev = given.get_device()
+        if dev < 0:
+            raise ValueError("workspace must be a device tensor")
+        if dev != like.get_device():
+            raise ValueError(f"workspace is on {given.device}, not on {like.device}")
+        if not given.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        if given.numel() * given.element_size() >= nbytes:
+            return given
+    return _empty((nbytes,), torch.uint8, like, stream) if nbytes else given
+
+
 # ------------------------------------------------------------------ calls
 
 
@@ -165,9 +181,7 @@ def router_logits(x, wr_t, wc_t, row_bias=None, col_bias=None, row_logits=None,
     _req(row_logits, "row_logits", torch.float32, (L, Nr))
     _req(col_logits, "col_logits", torch.float32, (L, Nc))
     nws = lib().omni_router_logits_workspace(_dtype_code(x), L, d, Nr, Nc)
-    ws = workspace
-    if nws and (ws is None or ws.numel() < nws):
-        ws = torch.empty(nws, dtype=torch.uint8, device=x.device)
+    ws = _workspace(workspace, nws, x)
     _check("omni_router_logits", lib().omni_router_logits(
         _dtype_code(x), L, d, Nr, Nc, _ptr(x), _ptr(wr_t), _ptr(wc_t), _ptr(row_bias),
         _ptr(col_bias), _ptr(row_logits), _ptr(col_logits), _ptr(ws) if nws else None, nws,
@@ -200,9 +214,7 @@ def product_topk(row_logits, col_logits, kprime, K, want_sel=True, want_logp=Tru
     rsel = get("row_sel", (L, kprime), torch.int32) if want_sel else None
     csel = get("col_sel", (L, kprime), torch.int32) if want_sel else None
     nws = lib().omni_product_topk_workspace(L, Nr, Nc, kprime, K)
-    ws = o.get("workspace")
-    if nws and (ws is None or ws.numel() < nws):
-        ws = torch.empty(nws, dtype=torch.uint8, device=dev)
+    ws = _workspace(o.get("workspace"), nws, row_logits)
     _check("omni_product_topk", lib().omni_product_topk(
         L, Nr, Nc, kprime, K, _ptr(row_logits), _ptr(col_logits), _ptr(idx), _ptr(score),
         _ptr(gate), _ptr(rlp), _ptr(clp), _ptr(rsel), _ptr(csel), _ptr(ws),
@@ -276,10 +288,10 @@ def schedule_tasks(expert_idx, gate, N, B, sched=None, stream=None, grouping="ac
     elif sched.grouping != grouping:
         raise ValueError(f"schedule buffers were sized for grouping {sched.grouping!r}")
     st = sched.struct()
-    ws = sched.workspace
+    ws = _workspace(sched.workspace, 0, expert_idx)
     _check("omni_schedule_tasks", lib().omni_schedule_tasks(
         L, K, N, B, _grouping(grouping), _ptr(expert_idx), _ptr(gate), ctypes.byref(st), _ptr(ws),
-        ws.numel() if ws is not None else 0, _stream(stream)))
+        ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
     sched.flat_expert, sched.flat_gate = expert_idx, gate
     return sched
 
@@ -327,9 +339,7 @@ def atomic_forward(x, w, v, sched, y=None, accumulate=False, workspace=None, str
     _req(y, "y", torch.float32, (L, d))
     st = sched.struct()
     nws = lib().omni_atomic_forward_workspace(_dtype_code(x), L, d, N, sched.K, sched.B, code)
-    ws = workspace
-    if nws and (ws is None or ws.numel() < nws):
-        ws = torch.empty(nws, dtype=torch.uint8, device=x.device)
+    ws = _workspace(workspace, nws, x)
     _check("omni_atomic_forward", lib().omni_atomic_forward(
         _dtype_code(x), L, d, N, sched.K, sched.B, _ptr(x), _ptr(w), _ptr(v),
         ctypes.byref(st), _ptr(y), int(bool(accumulate)), code, _ptr(ws),
@@ -353,9 +363,7 @@ def atomic_forward_glu(x, w, u, v, sched, y=None, accumulate=False, workspace=No
     st = sched.struct()
     nws = lib().omni_atomic_forward_workspace(_dtype_code(x), L, d, N, sched.K, sched.B,
                                               EXEC_MODES["token"])
-    ws = workspace
-    if nws and (ws is None or ws.numel() < nws):
-        ws = torch.empty(nws, dtype=torch.uint8, device=x.device)
+    ws = _workspace(workspace, nws, x)
     _check("omni_atomic_forward_glu", lib().omni_atomic_forward_glu(
         _dtype_code(x), L, d, N, sched.K, sched.B, _ptr(x), _ptr(w), _ptr(u), _ptr(v),
         ctypes.byref(st), _ptr(y), int(bool(accumulate)), _ptr(ws),
@@ -384,9 +392,7 @@ def flat_router_topk(x, wf, K, bias=None, want_logp=False, out=None, workspace=N
     r["logp"] = torch.empty((L, N), dtype=torch.float32, device=dev) if want_logp else None
     code = _dtype_code(x)
     nws = lib().omni_flat_router_workspace(code, L, N)
-    ws = workspace
-    if ws is None or ws.numel() < nws:
-        ws = torch.empty(max(1, nws), dtype=torch.uint8, device=dev)
+    ws = _workspace(workspace, max(1, nws), x)
     _check("omni_flat_router_topk", lib().omni_flat_router_topk(
         code, L, d, N, K, _ptr(x), _ptr(wf), _ptr(bias), _ptr(r["expert_idx"]),
         _ptr(r["score"]), _ptr(r["gate"]), _ptr(r["logp"]), _ptr(ws), nws, _stream(stream)))
@@ -419,9 +425,7 @@ def shared_mlp(x, w_gate, w_up, w_down, y=None, accumulate=False, workspace=None
     _req(y, "y", torch.float32, (L, d))
     code = _dtype_code(x)
     nws = lib().omni_shared_mlp_workspace(code, L, d, d_ff)
-    ws = workspace
-    if ws is None or ws.numel() < nws:
-        ws = torch.empty(max(1, nws), dtype=torch.uint8, device=x.device)
+    ws = _workspace(workspace, max(1, nws), x)
     _check("omni_shared_mlp", lib().omni_shared_mlp(
         code, L, d, d_ff, _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(y),
         int(bool(accumulate)), _ptr(ws), nws, _stream(stream)))
@@ -481,9 +485,7 @@ def routed_backward(x, wr_t, wc_t, w, v, expert_idx, gate, dy, out=None, workspa
          "dgate": get("dgate", (L, K), torch.float32)}
     code = _dtype_code(x)
     nws = lib().omni_routed_backward_workspace(code, L, d, Nr, Nc, K)
-    ws = workspace
-    if ws is None or ws.numel() < nws:
-        ws = torch.empty(max(1, nws), dtype=torch.uint8, device=dev)
+    ws = _workspace(workspace, max(1, nws), x)
     _check("omni_routed_backward", lib().omni_routed_backward(
         code, L, d, Nr, Nc, K, _ptr(x), _ptr(wr_t), _ptr(wc_t), _ptr(w), _ptr(v),
         _ptr(expert_idx), _ptr(gate), _ptr(dy), _ptr(r["dx"]), _ptr(r["dwr"]), _ptr(r["dwc"]),
@@ -614,9 +616,7 @@ def expert_weight_grad(x, dy, offsets, x_row=None, dy_row=None, dw=None, workspa
              (offsets, "offsets", torch.int32, (E + 1,)), (dw, "dw", torch.float32, (E, n, k)))
     code = _dtype_code(x)
     nws = lib().omni_expert_weight_grad_workspace(code, M, E, n, k)
-    ws = workspace
-    if nws and (ws is None or ws.numel() < nws):
-        ws = _empty(nws, torch.uint8, x, stream)
+    ws = _workspace(workspace, nws, x, stream)
     _call("omni_expert_weight_grad", dev, stream, code, M, E, n, k, R, Ry, x.data_ptr(),
           _addr(x_row), dy.data_ptr(), _addr(dy_row), offsets.data_ptr(), dw.data_ptr(),
           _addr(ws) if nws else None, nws)
