@@ -181,7 +181,7 @@ def router_logits(x, wr_t, wc_t, row_bias=None, col_bias=None, row_logits=None,
     _req(row_logits, "row_logits", torch.float32, (L, Nr))
     _req(col_logits, "col_logits", torch.float32, (L, Nc))
     nws = lib().omni_router_logits_workspace(_dtype_code(x), L, d, Nr, Nc)
-    ws = _workspace(workspace, nws, x)
+    ws = _workspace(workspace, nws, x, stream)
     _check("omni_router_logits", lib().omni_router_logits(
         _dtype_code(x), L, d, Nr, Nc, _ptr(x), _ptr(wr_t), _ptr(wc_t), _ptr(row_bias),
         _ptr(col_bias), _ptr(row_logits), _ptr(col_logits), _ptr(ws) if nws else None, nws,
@@ -214,7 +214,7 @@ def product_topk(row_logits, col_logits, kprime, K, want_sel=True, want_logp=Tru
     rsel = get("row_sel", (L, kprime), torch.int32) if want_sel else None
     csel = get("col_sel", (L, kprime), torch.int32) if want_sel else None
     nws = lib().omni_product_topk_workspace(L, Nr, Nc, kprime, K)
-    ws = _workspace(o.get("workspace"), nws, row_logits)
+    ws = _workspace(o.get("workspace"), nws, row_logits, stream)
     _check("omni_product_topk", lib().omni_product_topk(
         L, Nr, Nc, kprime, K, _ptr(row_logits), _ptr(col_logits), _ptr(idx), _ptr(score),
         _ptr(gate), _ptr(rlp), _ptr(clp), _ptr(rsel), _ptr(csel), _ptr(ws),
@@ -339,7 +339,7 @@ def atomic_forward(x, w, v, sched, y=None, accumulate=False, workspace=None, str
     _req(y, "y", torch.float32, (L, d))
     st = sched.struct()
     nws = lib().omni_atomic_forward_workspace(_dtype_code(x), L, d, N, sched.K, sched.B, code)
-    ws = _workspace(workspace, nws, x)
+    ws = _workspace(workspace, nws, x, stream)
     _check("omni_atomic_forward", lib().omni_atomic_forward(
         _dtype_code(x), L, d, N, sched.K, sched.B, _ptr(x), _ptr(w), _ptr(v),
         ctypes.byref(st), _ptr(y), int(bool(accumulate)), code, _ptr(ws),
@@ -363,7 +363,7 @@ def atomic_forward_glu(x, w, u, v, sched, y=None, accumulate=False, workspace=No
     st = sched.struct()
     nws = lib().omni_atomic_forward_workspace(_dtype_code(x), L, d, N, sched.K, sched.B,
                                               EXEC_MODES["token"])
-    ws = _workspace(workspace, nws, x)
+    ws = _workspace(workspace, nws, x, stream)
     _check("omni_atomic_forward_glu", lib().omni_atomic_forward_glu(
         _dtype_code(x), L, d, N, sched.K, sched.B, _ptr(x), _ptr(w), _ptr(u), _ptr(v),
         ctypes.byref(st), _ptr(y), int(bool(accumulate)), _ptr(ws),
@@ -392,7 +392,7 @@ def flat_router_topk(x, wf, K, bias=None, want_logp=False, out=None, workspace=N
     r["logp"] = torch.empty((L, N), dtype=torch.float32, device=dev) if want_logp else None
     code = _dtype_code(x)
     nws = lib().omni_flat_router_workspace(code, L, N)
-    ws = _workspace(workspace, max(1, nws), x)
+    ws = _workspace(workspace, max(1, nws), x, stream)
     _check("omni_flat_router_topk", lib().omni_flat_router_topk(
         code, L, d, N, K, _ptr(x), _ptr(wf), _ptr(bias), _ptr(r["expert_idx"]),
         _ptr(r["score"]), _ptr(r["gate"]), _ptr(r["logp"]), _ptr(ws), nws, _stream(stream)))
@@ -425,7 +425,7 @@ def shared_mlp(x, w_gate, w_up, w_down, y=None, accumulate=False, workspace=None
     _req(y, "y", torch.float32, (L, d))
     code = _dtype_code(x)
     nws = lib().omni_shared_mlp_workspace(code, L, d, d_ff)
-    ws = _workspace(workspace, max(1, nws), x)
+    ws = _workspace(workspace, max(1, nws), x, stream)
     _check("omni_shared_mlp", lib().omni_shared_mlp(
         code, L, d, d_ff, _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(y),
         int(bool(accumulate)), _ptr(ws), nws, _stream(stream)))
@@ -485,7 +485,7 @@ def routed_backward(x, wr_t, wc_t, w, v, expert_idx, gate, dy, out=None, workspa
          "dgate": get("dgate", (L, K), torch.float32)}
     code = _dtype_code(x)
     nws = lib().omni_routed_backward_workspace(code, L, d, Nr, Nc, K)
-    ws = _workspace(workspace, max(1, nws), x)
+    ws = _workspace(workspace, max(1, nws), x, stream)
     _check("omni_routed_backward", lib().omni_routed_backward(
         code, L, d, Nr, Nc, K, _ptr(x), _ptr(wr_t), _ptr(wc_t), _ptr(w), _ptr(v),
         _ptr(expert_idx), _ptr(gate), _ptr(dy), _ptr(r["dx"]), _ptr(r["dwr"]), _ptr(r["dwc"]),

@@ -108,3 +108,40 @@ def test_workspace_of_another_device_or_with_strides_is_refused():
     ws = Elsewhere(torch.zeros(64))
     assert B._workspace(ws, 256, like) is ws
     assert B._workspace(None, 0, like) is None
+
+
+STREAM_CALLS = {
+    "router_logits": lambda s: B.router_logits(bf(256, 2048), bf(1024, 2048), bf(1024, 2048),
+                                               stream=s),
+    "product_topk": lambda s: B.product_topk(torch.zeros(8, 64), torch.zeros(8, 64), 8, 8,
+                                             stream=s),
+    "atomic_forward": lambda s: B.atomic_forward(bf(8, 128), bf(64, 128), bf(64, 128),
+                                                 sched(8, 4, 64), stream=s),
+    "atomic_forward_glu": lambda s: B.atomic_forward_glu(
+        bf(8, 128), bf(64, 128), bf(64, 128), bf(64, 128), sched(8, 4, 64), stream=s),
+    "flat_router_topk": lambda s: B.flat_router_topk(bf(8, 128), bf(64, 128), 4, stream=s),
+    "shared_mlp": lambda s: B.shared_mlp(bf(8, 128), bf(64, 128), bf(64, 128), bf(128, 64),
+                                         stream=s),
+    "routed_backward": lambda s: B.routed_backward(
+        bf(8, 128), bf(8, 128), bf(8, 128), bf(64, 128), bf(64, 128), i32(8, 4),
+        torch.zeros(8, 4), torch.zeros(8, 128), stream=s),
+    "expert_weight_grad": lambda s: B.expert_weight_grad(
+        bf(8192, 64), bf(8192, 64), i32(2), dw=torch.zeros(1, 64, 64), stream=s),
+}
+
+
+@pytest.mark.parametrize("name", list(STREAM_CALLS))
+def test_a_fresh_workspace_belongs_to_the_stream_of_the_call(host_calls, monkeypatch, name):
+    """Freed when the call returns, it may be reused at once by its own stream only."""
+    streams = []
+
+    def empty(shape, dtype, like, stream):
+        streams.append(stream)
+        return torch.empty(shape, dtype=dtype)
+    monkeypatch.setattr(B, "_empty", empty)
+    mine = object()
+    try:
+        STREAM_CALLS[name](mine)
+    except Reached:
+        pass
+    assert streams == [mine]
