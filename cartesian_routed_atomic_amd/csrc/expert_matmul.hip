@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "device.hpp"
+#include "expert_tiles.hpp"
 #include "launch.hpp"
 
 namespace omni {
@@ -60,115 +61,6 @@ struct F32Op {
 
 // 16 bytes of zeros: where a lane of a direct load has nothing to fetch
 __device__ __attribute__((aligned(16))) const uint32_t kZeroChunk[4] = {0, 0, 0, 0};
-
-// ------------------------------------------------------------------ row tiles of the experts
-
-// Found by every wave for itself: lane l counts the tiles of q consecutive
-// experts, a prefix sum over the lanes gives the total and the lane that owns
-// row tile `rt`, and that lane's experts are walked.  Offsets are clamped to
-// [0, M] and to ascending order, so no value of theirs can lead a read or
-// write outside the row lists.
-struct ExpertTile {
-  int e, m0, m1;  // expert, first task of the tile, end of the tile (m0 == m1: none)
-};
-__device__ __forceinline__ void expert_range(const int32_t* off, int e, int M, int& lo, int& hi) {
-  lo = min(max(off[e], 0), M);
-  hi = min(max(off[e + 1], lo), M);
-}
-struct ExpertScan {
-  int mine, upto, total;
-  int lo, hi;  // tasks of this lane's last expert (its only one up to 64 experts)
-};
-__device__ __forceinline__ ExpertScan scan_experts(const int32_t* off, int E, int M, int bm) {
-  const int l = lane(), q = (E + kWave - 1) / kWave;
-  ExpertScan s{0, 0, 0, 0, 0};
-  for (int i = 0; i < q; ++i) {
-    const int e = l * q + i;
-    if (e < E) {
-      expert_range(off, e, M, s.lo, s.hi);
-      s.mine += (s.hi - s.lo + bm - 1) / bm;
-    }
-  }
-  s.upto = wave_prefix_sum(s.mine);
-  s.total = __builtin_amdgcn_readlane(s.upto, 63);
-  return s;
-}
-// Tile `id` of the n_nt column tiles of every row tile.  An expert's tiles run
-// in bands of kBand column tiles, each down all its row tiles: the tiles that
-// an XCD works on at a time (32 of the largest) then form a block of about
-// kBand x kBand, whose rows and weights its L2 fetches once.
-constexpr int kBand = 6;
-struct TilePlace {
-  ExpertTile t;
-  int nt;
-};
-__device__ __forceinline__ TilePlace place_in_expert(int e, int lo, int hi, int bm, int n_nt,
-                                                     int id) {
-  const int mt = (hi - lo + bm - 1) / bm;
-  const int band = id / (mt * kBand), width = min(kBand, n_nt - band * kBand);
-  const int rest = id - band * mt * kBand, rt = rest / width;
-  return {{e, lo + rt * bm, min(hi, lo + (rt + 1) * bm)}, band * kBand + rest - rt * width};
-}
-__device__ __forceinline__ TilePlace find_tile(const ExpertScan& s, const int32_t* off, int E,
-                                               int M, int bm, int n_nt, int id) {
-  const int q = (E + kWave - 1) / kWave, row = id / n_nt;
-  const uint64_t past = __ballot(s.upto > row);
-  if (past == 0) return {{0, 0, 0}, 0};
-  const int owner = __ffsll(static_cast<long long>(past)) - 1;
-  int left = row - (__builtin_amdgcn_readlane(s.upto, owner) -
-                    __builtin_amdgcn_readlane(s.mine, owner));
-  if (q == 1)
-    return place_in_expert(owner, __builtin_amdgcn_readlane(s.lo, owner),
-                           __builtin_amdgcn_readlane(s.hi, owner), bm, n_nt,
-                           id - (row - left) * n_nt);
-  for (int i = 0; i < q; ++i) {
-    const int e = owner * q + i;
-    if (e >= E) break;
-    int lo, hi;
-    expert_range(off, e, M, lo, hi);
-    const int mt = (hi - lo + bm - 1) / bm;
-    if (left < mt) return place_in_expert(e, lo, hi, bm, n_nt, id - (row - left) * n_nt);
-    left -= mt;
-  }
-  return {{0, 0, 0}, 0};
-}
-// The expert at position pos when every run of 64 experts is put in order of
-// its task counts, most first (ties by id), and its tasks.
-__device__ __forceinline__ int expert_by_size(const int32_t* off, int E, int M, int pos, int& lo,
-                                              int& hi) {
-  const int first = pos & ~63, e = first + lane();
-  int l = 0, h = -1;  // past the last expert: behind those without tasks
-  if (e < E) expert_range(off, e, M, l, h);
-  const int count = h - l;
-  int rank = 0;
-#pragma unroll 8
-  for (int j = 0; j < 64; ++j) {
-    const int c = __builtin_amdgcn_readlane(count, j);
-    rank += c > count || (c == count && j < lane()) ? 1 : 0;
-  }
-  const int at = __ffsll(static_cast<long long>(__ballot(rank == pos - first))) - 1;
-  lo = __builtin_amdgcn_readlane(l, at);
-  hi = __builtin_amdgcn_readlane(h, at);
-  return first + at;
-}
-// Workgroup b runs on XCD b % 8: give every XCD a contiguous run of the tiles
-// there are, so that neighbours share rows and weights in that XCD's L2.
-__device__ __forceinline__ int xcd_tile(int b, int total) {
-  const int per = total >> 3, rem = total & 7, xcd = b & 7;
-  return xcd * per + min(xcd, rem) + (b >> 3);
-}
-__device__ __forceinline__ bool xcd_has(int b, int total) {
-  return (b >> 3) < (total >> 3) + ((b & 7) < (total & 7) ? 1 : 0);
-}
-// The workgroup's tile; an empty one (m0 == m1) where there is none for it.
-__device__ __forceinline__ TilePlace my_tile(const ExpertMatmulArgs& a, int bm, int n_nt) {
-  if (!a.offsets)
-    return place_in_expert(0, 0, a.M, bm, n_nt, xcd_tile(blockIdx.x, gridDim.x));
-  const ExpertScan s = scan_experts(a.offsets, a.E, a.M, bm);
-  const int total = s.total * n_nt;
-  if (!xcd_has(blockIdx.x, total)) return {{0, 0, 0}, 0};
-  return find_tile(s, a.offsets, a.E, a.M, bm, n_nt, xcd_tile(blockIdx.x, total));
-}
 
 // ------------------------------------------------------------------ stages in LDS
 
@@ -487,7 +379,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
   const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
   const int K = QT ? a.n : a.k, N = QT ? a.k : a.n;
   const int n_nt = (N + BNO - 1) / BNO;
-  const TilePlace at = my_tile(a, BM, n_nt);
+  const TilePlace at = my_tile(blockIdx.x, gridDim.x, a.offsets, a.E, a.M, BM, n_nt);
   const ExpertTile t = at.t;
   const int n0 = at.nt * BNO;
   if (t.m0 >= t.m1) return;
@@ -653,32 +545,6 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
 
 // ------------------------------------------------------------------ the weight gradient
 
-// Where a workgroup's sum goes: dW itself, or a partial sum of one part of the
-// expert's tasks (experts with more tasks than a part has are cut into parts).
-struct WgradPart {
-  int e, lo, hi;
-  int slot;  // partial sum, -1: dW
-};
-// Slots of the experts in several parts come one after the other, by id.
-__device__ __forceinline__ int parts_of(int count, int part) {
-  return (count + part - 1) / part;
-}
-// first partial slot of expert e
-__device__ __forceinline__ int first_slot(const int32_t* off, int E, int M, int part, int e) {
-  const int l = lane(), q = (E + kWave - 1) / kWave;
-  int before = 0;  // slots of this lane's experts below e
-  for (int i = 0; i < q; ++i) {
-    const int f = l * q + i;
-    if (f < e) {
-      int lo, hi;
-      expert_range(off, f, M, lo, hi);
-      const int n = parts_of(hi - lo, part);
-      before += n > 1 ? n : 0;
-    }
-  }
-  return __builtin_amdgcn_readlane(wave_prefix_sum(before), 63);
-}
-
 // Tile BM output features (columns of dy) x BN inputs (columns of x) of one
 // expert; the contraction runs over its tasks in order, whose rows of dy and x
 // are gathered by the same ring of direct loads: a stage holds, task by task,
@@ -712,21 +578,10 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_wgrad_kernel(ExpertWgr
   WgradPart w;
   int n0, c0;
   if (a.part > 0) {
-    const ExpertScan sc = scan_experts(a.offsets, a.E, a.M, a.part);
-    const int tiles = n_nt * n_kt, total = sc.total * tiles;
-    if (!xcd_has(blockIdx.x, total)) return;
-    const int id = xcd_tile(blockIdx.x, total), p = id / tiles, tile = id - p * tiles;
-    // a part is a row tile of `part` rows; with one column tile each
-    const TilePlace at = find_tile(sc, a.offsets, a.E, a.M, a.part, 1, p);
-    if (at.t.m0 >= at.t.m1) return;
-    w = {at.t.e, at.t.m0, at.t.m1, -1};
-    int lo, hi;
-    expert_range(a.offsets, w.e, a.M, lo, hi);
-    if (hi - lo > a.part)
-      w.slot = first_slot(a.offsets, a.E, a.M, a.part, w.e) + (w.lo - lo) / a.part;
-    if (w.slot >= a.slots) return;  // offsets that overlap
-    n0 = tile / n_kt * BM;
-    c0 = tile % n_kt * BN;
+    w = my_part(blockIdx.x, a.offsets, a.E, a.M, a.part, a.slots, n_nt * n_kt);
+    if (w.lo >= w.hi) return;
+    n0 = w.tile / n_kt * BM;
+    c0 = w.tile % n_kt * BN;
   } else {
     // The n_kt tiles of one expert and one dy column block are a group: they
     // share dy's columns and x's rows in an L2.  Groups are dealt to the XCDs
@@ -891,7 +746,7 @@ __global__ __launch_bounds__(KS * 64) void expert_rows_kernel(ExpertMatmulArgs a
   const int wv = threadIdx.x >> 6, l = threadIdx.x & 63, fr = l & 15, g = l >> 4;
   const int K = a.k, N = a.n;
   const int n_nt = (N + BNO - 1) / BNO;
-  const TilePlace at = my_tile(a, BM, n_nt);
+  const TilePlace at = my_tile(blockIdx.x, gridDim.x, a.offsets, a.E, a.M, BM, n_nt);
   const ExpertTile t = at.t;
   const int n0 = at.nt * BNO;
   if (t.m0 >= t.m1) return;
