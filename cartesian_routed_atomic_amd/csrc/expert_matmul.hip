@@ -919,8 +919,8 @@ static ProductForm pick_form(const ExpertMatmulArgs& a) {
   return f32 ? kTileF32 : pick_tile(a);
 }
 bool expert_matmul_fits(const ExpertMatmulArgs& a) {
-  // a tile's offsets within W are 32 bits
-  if (a.n > 1 << 22 || a.k > 1 << 22) return false;
+  // a tile's offsets within W are 32 bits, and so is an expert's number rounded up to 64
+  if (a.n > 1 << 22 || a.k > 1 << 22 || a.E > 1 << 30) return false;
   if (a.M == 0) return true;
   const ProductForm f = pick_form(a);
   return form_blocks(a, f) < (1ll << 32) / form_shape(f, a.swiglu).threads;
@@ -1019,7 +1019,8 @@ size_t expert_wgrad_ws_bytes(int bf16, int M, int E, int n, int k) {
   return static_cast<size_t>(plan_wgrad(bf16, M, E, n, k).slots) * n * k * 4;
 }
 bool expert_wgrad_fits(const ExpertWgradArgs& a) {
-  if (a.n > 1 << 22 || a.k > 1 << 22) return false;  // row lengths in bytes are 32 bits
+  // row lengths in bytes are 32 bits, and so is a task's number rounded up to a part or stage
+  if (a.n > 1 << 22 || a.k > 1 << 22 || a.M > 1 << 30) return false;
   ExpertWgradArgs b = a;
   const WgradPlan p = plan_wgrad(a.bf16, a.M, a.E, a.n, a.k);
   b.part = p.part;

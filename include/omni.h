@@ -491,7 +491,7 @@ typedef enum omni_activation {
  * [E + 1] int32; out [Ro, n] of dt (transpose: [Ro, k]); x_row, out_row [M]
  * int32 or NULL.  Sums are float32, rounded once to dt.
  * Requires M, R, Ro >= 0 (R >= 1 where M > 0), E, n, k >= 1; k (transpose: n and k) a multiple of
- * 8 (bf16) or 4 (float32), else UNSUPPORTED, as are n or k past 2^22 and a
+ * 8 (bf16) or 4 (float32), else UNSUPPORTED, as are n or k past 2^22, E past 2^30 and a
  * launch of 2^32 work-items or more; x, w, out 16-byte aligned.  transpose with SWIGLU is
  * INVALID_ARG.  M == 0 enqueues nothing.  Deterministic.
  */
@@ -513,7 +513,7 @@ omni_status omni_expert_matmul(omni_dtype dt, int M, int E, int n, int k, int R,
  * NULL with 0 when that is 0 (few tiles of dw: experts with many tasks are cut
  * into parts, whose partial sums it holds; one workspace serves one call at a
  * time).  Requires n and k multiples of 8 (bf16) or 4 (float32) up to 2^22, else
- * UNSUPPORTED, as is a launch of 2^32 work-items or more; x, dy, dw 16-byte
+ * UNSUPPORTED, as are M past 2^30 and a launch of 2^32 work-items or more; x, dy, dw 16-byte
  * aligned.  Deterministic: every sum runs in a fixed order, in float32.
  */
 size_t omni_expert_weight_grad_workspace(omni_dtype dt, int M, int E, int n, int k);

@@ -1,0 +1,37 @@
+"""The limits of the expert operators, on both sides: host checks that return
+before any HIP call, so they need no GPU.  Where a size is taken, a later check
+(no tasks, no workspace) ends the call."""
+import ctypes
+
+import pytest
+
+B = pytest.importorskip("cartesian_routed_atomic_amd.binding")
+
+FAKE = ctypes.c_void_p(1 << 20)  # aligned, never dereferenced
+INV, UNS, OK = B.OMNI_ERR_INVALID_ARG, B.OMNI_ERR_UNSUPPORTED, B.OMNI_OK
+
+
+def weight_grad(dt=1, M=4, E=2, n=8, k=16, ws=None, nws=0, dw=FAKE):
+    return B.lib().omni_expert_weight_grad(dt, M, E, n, k, M, M, FAKE, None, FAKE, None, FAKE, dw,
+                                           ws, nws, None)
+
+
+def test_tasks_of_a_weight_gradient():
+    # a task's number rounded up to a stage or a part fits 31 bits
+    for dt in (0, 1):
+        assert weight_grad(dt, M=1 << 30) == B.OMNI_ERR_WORKSPACE
+        assert weight_grad(dt, M=(1 << 30) + 1) == UNS
+        assert weight_grad(dt, M=(1 << 31) - 1) == UNS
+
+
+def test_experts_of_a_product():
+    f = B.lib().omni_expert_matmul
+    call = lambda E: f(1, 0, E, 8, 16, 0, 0, FAKE, None, FAKE, FAKE, 0, 0, FAKE, None, None)
+    assert call(1 << 30) == OK
+    assert call((1 << 30) + 1) == UNS
+    assert call((1 << 31) - 1) == UNS
+    g = B.lib().omni_quantized_expert_matmul
+    call = lambda E: g(1, 0, E, 8, 16, 0, 0, FAKE, FAKE, None, FAKE, FAKE, FAKE, 0, FAKE, None,
+                       None)
+    assert call(1 << 30) == OK
+    assert call((1 << 30) + 1) == UNS
