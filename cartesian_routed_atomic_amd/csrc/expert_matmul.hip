@@ -507,7 +507,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
     TO* dst = out + static_cast<size_t>(row) * N;
     auto value = [&](int j, int q) {
       const float v = static_cast<float>(acc[i][j][q]);
-      if constexpr (Op::kBytes == 1) return v * rs * wsc[j][q];
+      // a row out of range gives zeros, whatever the weights and their scales hold
+      if constexpr (Op::kBytes == 1) return in ? v * rs * wsc[j][q] : 0.f;
       else return in ? v : 0.f;
     };
     if constexpr (QT) {
@@ -821,8 +822,9 @@ __global__ __launch_bounds__(KS * 64) void expert_rows_kernel(ExpertMatmulArgs a
       for (int h = 0; h < H; ++h) {
         z[h] = in ? static_cast<float>(s[h][q]) : 0.f;
         if constexpr (Op::kBytes == 1)
-          z[h] = z[h] * (in ? a.x_scale[xr] : 0.f) *
-                 a.w_scale[(static_cast<size_t>(t.e) * H + h) * N + min(c0 + q, N - 1)];
+          if (in)
+            z[h] = z[h] * a.x_scale[xr] *
+                   a.w_scale[(static_cast<size_t>(t.e) * H + h) * N + min(c0 + q, N - 1)];
       }
       v[q] = SWIGLU ? silu_mul(z[0], z[H - 1]) : z[0];
     }

@@ -470,7 +470,8 @@ omni_status omni_shared_mlp(omni_dtype dt, int L, int d, int d_ff, const void* x
  * give unspecified results (nothing outside the arrays is touched).  Tasks
  * from offsets[E] on are not computed and their output rows keep what they
  * held.  Row lists may be NULL (task m is row m; the array then has at least
- * M rows); x rows outside [0, R) count as zeros, output rows outside [0, Ro)
+ * M rows); tasks whose x row is outside [0, R) have zeros as their result,
+ * whatever the weights and their scales hold; output rows outside [0, Ro)
  * are not stored; two tasks with one output row give either's result.  Outputs
  * may not overlap inputs (omni_expert_combine's accumulated y aside).
  */

@@ -1,0 +1,50 @@
+"""Values and rows at the edges of the expert operators' definitions."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import omni_experts as OE
+from synth import bf16_bits_to_f32
+from tests.gpu_helpers import dev, host, log
+
+B = pytest.importorskip("cartesian_routed_atomic_amd.binding")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("counts,n,k", [
+    ([3, 0, 2], 40, 48),            # few rows
+    ([33, 40], 512, 64),            # more rows than few, few tiles
+    ([700, 90, 300], 1032, 80)])    # tiles
+def test_8_bit_rows_out_of_range_are_zeros_beside_any_scale(counts, n, k, swiglu, dt):
+    """As in the float products, a row out of range gives zeros where a weight's scale
+    is a NaN or an infinity too."""
+    rng = np.random.default_rng(n)
+    E, M = len(counts), sum(counts)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    rows = n * (2 if swiglu else 1)
+    log(f"[quantized_expert_matmul] rows out of range {counts} n={n} k={k} swiglu={swiglu} {dt}")
+    xq = rng.integers(-128, 128, (M, k)).astype(np.int8)
+    wq = rng.integers(-128, 128, (E, rows, k)).astype(np.int8)
+    xs = (rng.random(M) * 2.0 ** -8).astype(np.float32)
+    ws = (rng.random((E, rows)) / k ** 0.5 * 2.0 ** -6).astype(np.float32)
+    xr = rng.permutation(M).astype(np.int32)
+    lost = rng.permutation(M)[:max(2, M // 4)]
+    xr[lost] = np.where(np.arange(lost.size) % 2, M, -1)
+    out = torch.full((M, n), 7.0, device="cuda",
+                     dtype=torch.bfloat16 if dt == "bf16" else torch.float32)
+    plain = B.quantized_expert_matmul(dev(xq), dev(xs), dev(wq), dev(ws), dev(off), x_row=dev(xr),
+                                      out=out.clone(), swiglu=swiglu)
+    ws[:, ::3], ws[:, 1::3] = np.nan, np.inf
+    B.quantized_expert_matmul(dev(xq), dev(xs), dev(wq), dev(ws), dev(off), x_row=dev(xr), out=out,
+                              swiglu=swiglu)
+    got = host(out.float())
+    assert (got[lost] == 0).all()
+    kept = np.setdiff1d(np.arange(M), lost)
+    # columns with finite scales: as without the others
+    cols = np.arange(n) % 3 == 2
+    if swiglu:
+        cols &= (np.arange(n) + n) % 3 == 2
+    np.testing.assert_array_equal(got[kept][:, cols], host(plain.float())[kept][:, cols])
+    assert not np.isfinite(got[kept][:, np.arange(n) % 3 == 0]).any()
