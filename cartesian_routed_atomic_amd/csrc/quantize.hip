@@ -47,20 +47,23 @@ __device__ __forceinline__ void load_unit(const uint16_t* p, float (&v)[kUnit]) 
 
 // The row's scale, and what its quotients are formed with: rows whose scale is
 // tiny are lifted by 2^64 (exact), so that 1 / s and the remainders stay
-// normal numbers.
+// normal numbers.  A scale of 0 and one that is not finite have no quotients.
 struct RowScale {
   float s, lift, lifted, inv;
+  bool any;  // positive and finite
 };
 __device__ __forceinline__ RowScale row_scale(float top) {
   RowScale r;
   r.s = top / 127.f;
+  r.any = r.s > 0.f && r.s < INFINITY;
   r.lift = r.s < 0x1p-90f ? 0x1p64f : 1.f;
   r.lifted = r.s * r.lift;
-  r.inv = r.s > 0.f ? 1.f / r.lifted : 0.f;
+  r.inv = r.any ? 1.f / r.lifted : 0.f;
   return r;
 }
 
-// q of one unit with every case decided: scale 0, tiny scales, halves
+// q of one unit with every case decided: scales without quotients (q is 0),
+// tiny scales, halves
 __device__ void exact_unit(const float (&x)[kUnit], const RowScale& s, uint32_t (&w)[kUnit / 4]) {
   const float half = 0.5f * s.lifted;
 #pragma unroll
@@ -70,7 +73,7 @@ __device__ void exact_unit(const float (&x)[kUnit], const RowScale& s, uint32_t 
     const float r = fmaf(-q, s.lifted, v), a = fabsf(r);
     const bool odd = (static_cast<int>(q) & 1) != 0;
     if (a > half || (a == half && odd)) q += copysignf(1.f, r);
-    const int n = s.s > 0.f ? static_cast<int>(fminf(fmaxf(q, -127.f), 127.f)) : 0;
+    const int n = s.any ? static_cast<int>(fminf(fmaxf(q, -127.f), 127.f)) : 0;
     const uint32_t b = static_cast<uint32_t>(n & 255) << (8 * (i & 3));
     w[i >> 2] = (i & 3) ? w[i >> 2] | b : b;
   }
@@ -89,7 +92,7 @@ __device__ __forceinline__ void store_unit(int8_t* p, const float (&x)[kUnit], c
     t[i] = __float_as_uint(m);
     worst = fmaxf(worst, fabsf(fmaf(kMagic - m, s.s, x[i])));
   }
-  if (__any(!(worst < 0.5f * s.s) || s.lift != 1.f)) {  // a NaN scale as well
+  if (__any(!(worst < 0.5f * s.s) || s.lift != 1.f || !s.any)) {
     exact_unit(x, s, w);
   } else {
 #pragma unroll

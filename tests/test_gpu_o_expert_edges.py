@@ -48,3 +48,24 @@ def test_8_bit_rows_out_of_range_are_zeros_beside_any_scale(counts, n, k, swiglu
         cols &= (np.arange(n) + n) % 3 == 2
     np.testing.assert_array_equal(got[kept][:, cols], host(plain.float())[kept][:, cols])
     assert not np.isfinite(got[kept][:, np.arange(n) % 3 == 0]).any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [16, 48, 2064, 16400])
+def test_quantized_rows_of_infinities_and_zeros(k, dt):
+    """Scales without quotients give q 0 for every value of the row: an infinity of
+    either sign, alone, beside zeros, beside the largest number, or all along."""
+    big = np.float32(3.3895314e38)   # the largest bf16
+    x = np.zeros((7, k), np.float32)
+    x[0, k // 2] = -np.inf
+    x[1] = np.inf
+    x[2, ::2], x[2, 1::2] = -np.inf, big
+    x[3, :], x[3, k - 1] = np.nan, np.inf
+    x[5] = -big
+    x[6] = np.where(np.arange(k) % 3, np.float32(1e-45), 0) if dt == "f32" else 0
+    xd = dev(x) if dt == "f32" else dev(x).bfloat16()
+    q, s = B.quantize_rows(xd, q=torch.full((7, k), 99, dtype=torch.int8, device="cuda"))
+    q, s = host(q), host(s)
+    assert (q[[0, 1, 2, 3, 4, 6]] == 0).all() and (q[5] == -127).all()
+    assert (s[:3] == np.inf).all() and np.isnan(s[3]) and s[4] == 0 and s[6] == 0
+    assert s[5] == np.float32(np.float64(big) / 127)
