@@ -484,11 +484,7 @@ static omni_status combine_args(omni_dtype dt, int L, int K, int n) {
   if (dt != OMNI_F32 && dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
   if (L < 0 || K < 1 || n < 1 || !fits_i32(static_cast<long long>(L) * K))
     return OMNI_ERR_INVALID_ARG;
-  if (n % (dt == OMNI_BF16 ? 8 : 4) != 0) return OMNI_ERR_UNSUPPORTED;
-  if (!grid_fits((static_cast<long long>(L) * (n / 4) + 255) / 256, 256) ||
-      !grid_fits((static_cast<long long>(L) * K + 3) / 4, 256))
-    return OMNI_ERR_UNSUPPORTED;
-  return OMNI_OK;
+  return n % (dt == OMNI_BF16 ? 8 : 4) == 0 ? OMNI_OK : OMNI_ERR_UNSUPPORTED;
 }
 
 omni_status omni_expert_combine(omni_dtype dt, int L, int K, int n, const void* o,
@@ -496,6 +492,9 @@ omni_status omni_expert_combine(omni_dtype dt, int L, int K, int n, const void* 
                                 hipStream_t stream) {
   const omni_status st = combine_args(dt, L, K, n);
   if (st != OMNI_OK) return st;
+  // four columns of a token per work-item
+  if (!grid_fits((static_cast<long long>(L) * (n / 4) + 255) / 256, 256))
+    return OMNI_ERR_UNSUPPORTED;
   if (L == 0) return OMNI_OK;
   if (!o || !y || !aligned16(o) || !aligned16(y)) return OMNI_ERR_INVALID_ARG;
   return hip_status(omni::launch_expert_combine(dt == OMNI_BF16, L, K, n, o, gate, y,
@@ -507,6 +506,8 @@ omni_status omni_expert_combine_backward(omni_dtype dt, int L, int K, int n, con
                                          float* dgate, hipStream_t stream) {
   const omni_status st = combine_args(dt, L, K, n);
   if (st != OMNI_OK) return st;
+  // a wave per task
+  if (!grid_fits((static_cast<long long>(L) * K + 3) / 4, 256)) return OMNI_ERR_UNSUPPORTED;
   if (L == 0) return OMNI_OK;
   if (!dy || !dout || (dgate && !o)) return OMNI_ERR_INVALID_ARG;
   if (!aligned16(dy) || !aligned16(dout) || (dgate && !aligned16(o))) return OMNI_ERR_INVALID_ARG;
@@ -518,7 +519,8 @@ omni_status omni_quantize_rows(omni_dtype dt, int R, int k, const void* x, int8_
                                float* scale, hipStream_t stream) {
   if (dt != OMNI_F32 && dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
   if (R < 0 || k < 1) return OMNI_ERR_INVALID_ARG;
-  if (k % 16 != 0 || !grid_fits(R, 256)) return OMNI_ERR_UNSUPPORTED;
+  if (k % 16 != 0 || !grid_fits(omni::quantize_rows_blocks(R, k), 256))
+    return OMNI_ERR_UNSUPPORTED;
   if (R == 0) return OMNI_OK;
   if (!x || !q || !scale || !aligned16(x) || !aligned16(q)) return OMNI_ERR_INVALID_ARG;
   return hip_status(omni::launch_quantize_rows(dt == OMNI_BF16, R, k, x, q, scale, stream));

@@ -163,6 +163,7 @@ hipError_t launch_expert_combine_backward(int bf16, int L, int K, int n, const v
                                           float* dgate, hipStream_t s);
 
 // quantize.hip
+long long quantize_rows_blocks(int R, int k);  // workgroups of 256 of the launch
 hipError_t launch_quantize_rows(int bf16, int R, int k, const void* x, int8_t* q, float* scale,
                                 hipStream_t s);
 

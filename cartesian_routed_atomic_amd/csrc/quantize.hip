@@ -167,15 +167,19 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* __restrict_
   }
 }
 
+// rows of up to 128 units: a wave each, longer ones a workgroup
+long long quantize_rows_blocks(int R, int k) { return k / kUnit <= 128 ? (R + 3ll) / 4 : R; }
+
 template <typename T>
 static void run_quantize(const T* x, int8_t* q, float* scale, int R, int k, hipStream_t s) {
-  const int units = k / kUnit, nw = (R + 3) / 4;
-  if (units <= 64) quantize_rows_kernel<T, 64, 1><<<nw, 256, 0, s>>>(x, q, scale, R, k);
-  else if (units <= 128) quantize_rows_kernel<T, 64, 2><<<nw, 256, 0, s>>>(x, q, scale, R, k);
-  else if (units <= 256) quantize_rows_kernel<T, 256, 1><<<R, 256, 0, s>>>(x, q, scale, R, k);
-  else if (units <= 512) quantize_rows_kernel<T, 256, 2><<<R, 256, 0, s>>>(x, q, scale, R, k);
-  else if (units <= 1024) quantize_rows_kernel<T, 256, 4><<<R, 256, 0, s>>>(x, q, scale, R, k);
-  else quantize_rows_kernel<T, 256, 0><<<R, 256, 0, s>>>(x, q, scale, R, k);
+  const int units = k / kUnit;
+  const unsigned nb = static_cast<unsigned>(quantize_rows_blocks(R, k));
+  if (units <= 64) quantize_rows_kernel<T, 64, 1><<<nb, 256, 0, s>>>(x, q, scale, R, k);
+  else if (units <= 128) quantize_rows_kernel<T, 64, 2><<<nb, 256, 0, s>>>(x, q, scale, R, k);
+  else if (units <= 256) quantize_rows_kernel<T, 256, 1><<<nb, 256, 0, s>>>(x, q, scale, R, k);
+  else if (units <= 512) quantize_rows_kernel<T, 256, 2><<<nb, 256, 0, s>>>(x, q, scale, R, k);
+  else if (units <= 1024) quantize_rows_kernel<T, 256, 4><<<nb, 256, 0, s>>>(x, q, scale, R, k);
+  else quantize_rows_kernel<T, 256, 0><<<nb, 256, 0, s>>>(x, q, scale, R, k);
 }
 
 hipError_t launch_quantize_rows(int bf16, int R, int k, const void* x, int8_t* q, float* scale,

@@ -534,7 +534,8 @@ omni_status omni_expert_weight_grad(omni_dtype dt, int M, int E, int n, int k, i
  * adds onto y as it stands, e.g. onto omni_shared_mlp's output.  Summed in
  * float32 in k order, without atomics.
  * Requires K, n >= 1, n a multiple of 8 (bf16) or 4 (float32), else
- * UNSUPPORTED; L*K < 2^31; o, y 16-byte aligned.
+ * UNSUPPORTED, as is a y of more than 2^34 - 1024 elements; L*K < 2^31; o, y
+ * 16-byte aligned.
  */
 omni_status omni_expert_combine(omni_dtype dt, int L, int K, int n, const void* o,
                                 const float* gate, float* y, int accumulate,
@@ -547,7 +548,8 @@ omni_status omni_expert_combine(omni_dtype dt, int L, int K, int n, const void* 
  *   dgate[t, k] = dy[t, :] . o[t K + k, :]      [L, K] float32
  *
  * gate NULL: gates of one; dgate NULL: not wanted (o may then be NULL).
- * Shapes and refusals as omni_expert_combine.  Deterministic.
+ * Shapes and refusals as omni_expert_combine, but instead of y's size L*K of
+ * 2^26 - 3 or more is UNSUPPORTED.  Deterministic.
  */
 omni_status omni_expert_combine_backward(omni_dtype dt, int L, int K, int n, const void* o,
                                          const float* gate, const float* dy, void* dout,
@@ -564,7 +566,8 @@ omni_status omni_expert_combine_backward(omni_dtype dt, int L, int K, int n, con
  *
  * x [R, k] of dt, q [R, k] int8, scale [R] float32.  Activations are rows of
  * tokens, weights rows of output channels.  Requires k a multiple of 16, else
- * UNSUPPORTED; x and q 16-byte aligned.
+ * UNSUPPORTED, as are 2^26 - 3 rows or more, from k = 2064 on 2^24 or more;
+ * x and q 16-byte aligned.
  */
 omni_status omni_quantize_rows(omni_dtype dt, int R, int k, const void* x, int8_t* q,
                                float* scale, hipStream_t stream);

@@ -35,3 +35,35 @@ def test_experts_of_a_product():
                        None)
     assert call(1 << 30) == OK
     assert call((1 << 30) + 1) == UNS
+
+
+def test_rows_of_a_combination():
+    f = B.lib().omni_expert_combine
+    # o missing ends a call whose size is taken
+    call = lambda dt, L, K, n: f(dt, L, K, n, None, None, FAKE, 0, None)
+    assert call(1, 1 << 23, 8, 8) == INV                  # 2^26 tasks
+    assert call(1, (1 << 31) - 1, 1, 8) == UNS            # y of nearly 2^34 elements
+    assert call(1, (1 << 31) - 128, 1, 8) == INV
+    assert call(1, (1 << 31) - 127, 1, 8) == UNS
+    assert call(0, 1, (1 << 31) - 1, 4) == INV
+    assert call(0, (1 << 24) - 1, 127, 1 << 10) == INV    # y of 2^34 - 1024
+    assert call(0, 1 << 24, 127, 1 << 10) == UNS
+
+
+def test_tasks_of_the_backward_combination():
+    f = B.lib().omni_expert_combine_backward
+    call = lambda L, K, n: f(1, L, K, n, FAKE, FAKE, None, FAKE, FAKE, None)
+    assert call((1 << 26) - 4, 1, 8) == INV               # dy missing
+    assert call((1 << 26) - 3, 1, 8) == UNS
+    assert call(1, (1 << 26) - 4, 8) == INV
+    assert call(1 << 23, 8, 8) == UNS
+    assert call(1 << 20, 8, 1 << 20) == INV               # the rows' length does not count
+
+
+def test_rows_to_quantise():
+    f = B.lib().omni_quantize_rows
+    call = lambda R, k: f(1, R, k, None, FAKE, FAKE, None)
+    assert call((1 << 26) - 4, 2048) == INV               # x missing
+    assert call((1 << 26) - 3, 16) == UNS
+    assert call((1 << 24) - 1, 2064) == INV
+    assert call(1 << 24, 2064) == UNS

@@ -60,3 +60,31 @@ def test_quantize_rows_of_2_to_the_31_columns(dt):
     assert scale.item() == want.item()
     for s in slices(k):
         assert torch.equal(q[0, s], torch.round(x[0, s].double() / want.double()).to(torch.int8))
+
+
+def test_combination_of_2_to_the_26_tasks():
+    L, K, n = (1 << 23) + 5, 8, 8
+    log(f"[combine] {L} tokens, {K} rows of {n}")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    o = torch.randint(-8, 9, (L * K, n), generator=g, device="cuda").bfloat16()
+    gate = torch.randint(0, 5, (L, K), generator=g, device="cuda").float()
+    y = B.expert_combine(o, K, gate=gate)              # whole numbers: every sum is exact
+    for s in range(0, L, 1 << 20):
+        e = min(L, s + (1 << 20))
+        want = (o[s * K:e * K].float().view(-1, K, n) * gate[s:e, :, None]).sum(1)
+        assert torch.equal(y[s:e], want)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_quantize_2_to_the_24_rows(dt):
+    R, k = (1 << 24) + 5, 16
+    log(f"[quantize_rows] {R} rows of {k}, {dt}")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((R, k), generator=g, device="cuda").to(dt)
+    q, scale = B.quantize_rows(x)
+    for s in range(0, R, 1 << 22):
+        a = x[s:s + (1 << 22)].double()
+        want = (a.abs().amax(1) / 127).float()
+        assert torch.equal(scale[s:s + (1 << 22)], want)
+        assert torch.equal(q[s:s + (1 << 22)],
+                           torch.round(a / want.double()[:, None]).clamp(-127, 127).to(torch.int8))
