@@ -1020,18 +1020,21 @@ static long long wgrad_blocks(const ExpertWgradArgs& a, int tile) {
 size_t expert_wgrad_ws_bytes(int bf16, int M, int E, int n, int k) {
   return static_cast<size_t>(plan_wgrad(bf16, M, E, n, k).slots) * n * k * 4;
 }
+static int wgrad_threads(int tile) { return tile == 256 ? 512 : 256; }
 bool expert_wgrad_fits(const ExpertWgradArgs& a) {
   // row lengths in bytes are 32 bits, and so is a task's number rounded up to a part or stage
   if (a.n > 1 << 22 || a.k > 1 << 22 || a.M > 1 << 30) return false;
   ExpertWgradArgs b = a;
   const WgradPlan p = plan_wgrad(a.bf16, a.M, a.E, a.n, a.k);
   b.part = p.part;
-  return wgrad_blocks(b, p.tile) < (1ll << 32) / 512 && a.E < (p.part ? 65536 : 1 << 30) &&
+  return wgrad_blocks(b, p.tile) < (1ll << 32) / wgrad_threads(p.tile) &&
+         a.E < (p.part ? 65536 : 1 << 30) &&
          static_cast<long long>(a.n) * a.k / 4 < (1ll << 32) - 1024;
 }
 
 template <class Op, int B, int WM, int WN>
 static hipError_t run_wgrad(const ExpertWgradArgs& a, hipStream_t s) {
+  static_assert(WM * WN <= (B == 256 ? 8 : 4), "wgrad_threads");
   const unsigned nb = static_cast<unsigned>(wgrad_blocks(a, B));
   if (a.x_row && a.dy_row)
     expert_wgrad_kernel<Op, B, B, WM, WN, 4, true><<<nb, WM * WN * 64, 0, s>>>(a);

@@ -67,3 +67,9 @@ def test_rows_to_quantise():
     assert call((1 << 26) - 3, 16) == UNS
     assert call((1 << 24) - 1, 2064) == INV
     assert call(1 << 24, 2064) == UNS
+
+
+def test_tiles_of_a_weight_gradient():
+    # launches of 2^32 work-items: tiles of up to 128 have 256, tiles of 256 have 512
+    assert weight_grad(M=4, E=1 << 24, n=8, k=8) == UNS
+    assert weight_grad(M=64 << 20, E=1 << 20, n=256, k=256 * 8) == UNS

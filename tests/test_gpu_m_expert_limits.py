@@ -88,3 +88,18 @@ def test_quantize_2_to_the_24_rows(dt):
         assert torch.equal(scale[s:s + (1 << 22)], want)
         assert torch.equal(q[s:s + (1 << 22)],
                            torch.round(a / want.double()[:, None]).clamp(-127, 127).to(torch.int8))
+
+
+def test_weight_gradient_of_2_to_the_23_experts():
+    E, M = (1 << 23) + 5, 40
+    log(f"[expert_weight_grad] {E} experts of 8 x 8")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randint(-4, 5, (M, 8), generator=g, device="cuda").bfloat16()
+    dy = torch.randint(-4, 5, (M, 8), generator=g, device="cuda").bfloat16()
+    expert = torch.tensor([0] * 3 + [70] * 20 + [1 << 22] * 7 + [E - 1] * 10, device="cuda")
+    off = torch.searchsorted(expert, torch.arange(E + 1, device="cuda")).int()
+    dw = torch.full((E, 8, 8), float("nan"), device="cuda")
+    B.expert_weight_grad(x, dy, off, dw=dw)
+    want = torch.zeros((E, 8, 8), device="cuda")
+    want.index_add_(0, expert, dy.float()[:, :, None] * x.float()[:, None, :])  # exact
+    assert torch.equal(dw, want)
