@@ -642,20 +642,33 @@ def expert_combine(o, K, gate=None, y=None, accumulate=False, stream=None):
     return y
 
 
-def expert_combine_backward(o, gate, dy, do=None, dgate=None, stream=None):
+def expert_combine_backward(o, gate, dy, do=None, dgate=None, want_dgate=True, stream=None):
     """omni_expert_combine_backward: returns (do [L*K, n] of o's type, dgate [L, K]
-    float32) for dy [L, n] float32."""
-    (L, K), n, dev = _matrix(gate, "gate"), _matrix(dy, "dy")[1], _device_of(o, "o")
-    if do is None:
-        do = _empty(o.shape, o.dtype, o, stream)
-    if dgate is None:
-        dgate = _empty((L, K), torch.float32, o, stream)
+    float32) for dy [L, n] float32.  gate None: gates of one, K from the rows of o;
+    want_dgate False: dgate is None and o's values are not read."""
+    (rows, width), (L, n), dev = _matrix(o, "o"), _matrix(dy, "dy"), _device_of(o, "o")
     f32 = torch.float32
-    _tensors(dev, (o, "o", o.dtype, (L * K, n)), (gate, "gate", f32, (L, K)),
-             (dy, "dy", f32, (L, n)), (do, "do", o.dtype, (L * K, n)),
-             (dgate, "dgate", f32, (L, K)))
+    if gate is not None:
+        K = _matrix(gate, "gate")[1]
+    else:
+        K = rows // L if L else 1
+        if K < 1 or rows != L * K:
+            raise ValueError(f"o has {rows} rows, not a multiple of dy's {L}")
+    if do is None:
+        do = _empty((rows, width), o.dtype, o, stream)
+    if not want_dgate:
+        if dgate is not None:
+            raise ValueError("dgate is not wanted but given")
+    elif dgate is None:
+        dgate = _empty((L, K), f32, o, stream)
+    _tensors(dev, (o, "o", o.dtype, (L * K, n)), (dy, "dy", f32, (L, n)),
+             (do, "do", o.dtype, (L * K, n)))
+    if gate is not None:
+        _tensors(dev, (gate, "gate", f32, (L, K)))
+    if dgate is not None:
+        _tensors(dev, (dgate, "dgate", f32, (L, K)))
     _call("omni_expert_combine_backward", dev, stream, _dtype_code(o), L, K, n, o.data_ptr(),
-          gate.data_ptr(), dy.data_ptr(), do.data_ptr(), dgate.data_ptr())
+          _addr(gate), dy.data_ptr(), do.data_ptr(), _addr(dgate))
     return do, dgate
 
 

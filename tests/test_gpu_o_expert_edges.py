@@ -69,3 +69,55 @@ def test_quantized_rows_of_infinities_and_zeros(k, dt):
     assert (q[[0, 1, 2, 3, 4, 6]] == 0).all() and (q[5] == -127).all()
     assert (s[:3] == np.inf).all() and np.isnan(s[3]) and s[4] == 0 and s[6] == 0
     assert s[5] == np.float32(np.float64(big) / 127)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("L,K,n", [(1, 1, 8), (5, 3, 72), (67, 6, 1000), (33, 64, 264)])
+def test_combine_backward_without_gates_or_their_gradient(L, K, n, dt):
+    """Gates of one (the backward of a sum without gates), and no gradient of the
+    gates; through the Python call and the library's own, o missing there."""
+    rng = np.random.default_rng(L * 10 + K)
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    o = dev(rng.standard_normal((L * K, n)).astype(np.float32)).to(dtype)
+    gate = rng.random((L, K)).astype(np.float32)
+    dy = rng.standard_normal((L, n)).astype(np.float32)
+    log(f"[combine_backward] L={L} K={K} n={n} {dt}")
+    ones = np.ones_like(gate)
+    want, want_dg, mass = OE.expert_combine_backward_f64(host(o), ones, dy)
+    half = 2.0 ** -8 if dt == "bf16" else 2.0 ** -24
+    value = lambda t: host(t.float()).astype(np.float64)
+    do, dgate = B.expert_combine_backward(o, None, dev(dy))
+    assert (np.abs(value(do) - want) <= half * 1.001 * np.abs(want)).all()
+    # a sum of n products in float32, as of any gates
+    assert (np.abs(host(dgate) - want_dg) <= (n + 2) * 2.0 ** -23 * mass).all()
+    # the same bits as gates that are ones
+    do1, dgate1 = B.expert_combine_backward(o, dev(ones), dev(dy))
+    assert torch.equal(do, do1) and torch.equal(dgate, dgate1)
+    # no gradient of the gates: do as before, o not read
+    with_dg, _ = B.expert_combine_backward(o, dev(gate), dev(dy))
+    nan = torch.full_like(o, float("nan"))
+    for g in (dev(gate), None):
+        got, none = B.expert_combine_backward(nan, g, dev(dy), want_dgate=False)
+        assert none is None and torch.equal(got, do if g is None else with_dg)
+    raw = torch.full_like(o, float("nan"))
+    d = dev(dy)
+    assert B.lib().omni_expert_combine_backward(
+        1 if dt == "bf16" else 0, L, K, n, None, None, d.data_ptr(), raw.data_ptr(), None,
+        torch.cuda.current_stream().cuda_stream) == B.OMNI_OK
+    torch.cuda.synchronize()
+    assert torch.equal(raw, do)
+
+
+def test_combine_backward_refuses_what_does_not_fit():
+    o = torch.zeros((7, 16), device="cuda")
+    dy = torch.zeros((2, 16), device="cuda")
+    with pytest.raises(ValueError, match="not a multiple"):
+        B.expert_combine_backward(o, None, dy)
+    with pytest.raises(ValueError, match="not wanted"):
+        B.expert_combine_backward(o[:6].contiguous(), None, dy, want_dgate=False,
+                                  dgate=torch.zeros((2, 3), device="cuda"))
+    with pytest.raises(ValueError, match="expected"):
+        B.expert_combine_backward(o, torch.zeros((2, 3), device="cuda"), dy)
+    empty = torch.zeros((0, 16), device="cuda")
+    do, dgate = B.expert_combine_backward(empty, None, empty)
+    assert do.shape == (0, 16) and dgate.shape[0] == 0
