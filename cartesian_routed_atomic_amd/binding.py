@@ -538,6 +538,12 @@ def _call(fn, dev, stream, *args):
         _check(fn, code)
 
 
+def _sizes_fit(bits):
+    """bits: the sizes or-ed together.  The library's are 32-bit; ctypes cuts longer ones off."""
+    if bits >> 31:
+        raise ValueError("sizes of 2^31 or more are not taken")
+
+
 def _empty(shape, dtype, like, stream):
     """A fresh tensor, of the memory pool of the stream that will write it."""
     if stream is None:
@@ -595,6 +601,7 @@ def expert_matmul(x, w, offsets, x_row=None, out=None, out_row=None, transpose=F
     Ro = out.shape[0]
     _tensors(dev, (x, "x", dt, (R, n if transpose else k)), (w, "w", dt, w.shape),
              (offsets, "offsets", torch.int32, (E + 1,)), (out, "out", dt, (Ro, width)))
+    _sizes_fit(M | E | n | k | R | Ro)
     _call("omni_expert_matmul", dev, stream, _dtype_code(x), M, E, n, k, R, Ro, x.data_ptr(),
           _addr(x_row), w.data_ptr(), offsets.data_ptr(), 1 if transpose else 0,
           1 if swiglu else 0, out.data_ptr(), _addr(out_row))
@@ -615,6 +622,7 @@ def expert_weight_grad(x, dy, offsets, x_row=None, dy_row=None, dw=None, workspa
     _tensors(dev, (x, "x", dt, (R, k)), (dy, "dy", dt, (Ry, n)),
              (offsets, "offsets", torch.int32, (E + 1,)), (dw, "dw", torch.float32, (E, n, k)))
     code = _dtype_code(x)
+    _sizes_fit(M | E | n | k | R | Ry)
     nws = lib().omni_expert_weight_grad_workspace(code, M, E, n, k)
     ws = _workspace(workspace, nws, x, stream)
     _call("omni_expert_weight_grad", dev, stream, code, M, E, n, k, R, Ry, x.data_ptr(),
@@ -637,6 +645,7 @@ def expert_combine(o, K, gate=None, y=None, accumulate=False, stream=None):
     _tensors(dev, (o, "o", o.dtype, (rows, n)), (y, "y", torch.float32, (L, n)))
     if gate is not None:
         _tensors(dev, (gate, "gate", torch.float32, (L, K)))
+    _sizes_fit(L | K | n)
     _call("omni_expert_combine", dev, stream, _dtype_code(o), L, K, n, o.data_ptr(), _addr(gate),
           y.data_ptr(), 1 if accumulate else 0)
     return y
@@ -667,6 +676,7 @@ def expert_combine_backward(o, gate, dy, do=None, dgate=None, want_dgate=True, s
         _tensors(dev, (gate, "gate", f32, (L, K)))
     if dgate is not None:
         _tensors(dev, (dgate, "dgate", f32, (L, K)))
+    _sizes_fit(L | K | n)
     _call("omni_expert_combine_backward", dev, stream, _dtype_code(o), L, K, n, o.data_ptr(),
           _addr(gate), dy.data_ptr(), do.data_ptr(), _addr(dgate))
     return do, dgate
@@ -683,6 +693,7 @@ def quantize_rows(x, q=None, scale=None, stream=None):
         scale = _empty(R, torch.float32, x, stream)
     _tensors(dev, (x, "x", x.dtype, (R, k)), (q, "q", torch.int8, (R, k)),
              (scale, "scale", torch.float32, (R,)))
+    _sizes_fit(R | k)
     _call("omni_quantize_rows", dev, stream, _dtype_code(x), R, k, x.data_ptr(), q.data_ptr(),
           scale.data_ptr())
     return q, scale
@@ -702,6 +713,7 @@ def quantized_matmul(xq, x_scale, wq, w_scale, out=None, out_dtype=torch.bfloat1
     _tensors(dev, (xq, "xq", i8, (M, k)), (wq, "wq", i8, (rows, k)),
              (x_scale, "x_scale", f32, (M,)), (w_scale, "w_scale", f32, (rows,)),
              (out, "out", out.dtype, (M, n)))
+    _sizes_fit(M | n | k)
     _call("omni_quantized_matmul", dev, stream, _dtype_code(out), M, n, k, xq.data_ptr(),
           x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), 1 if swiglu else 0,
           out.data_ptr())
@@ -721,6 +733,7 @@ def quantized_expert_matmul(xq, x_scale, wq, w_scale, offsets, x_row=None, out=N
     _tensors(dev, (xq, "xq", i8, (R, k)), (wq, "wq", i8, wq.shape),
              (x_scale, "x_scale", f32, (R,)), (w_scale, "w_scale", f32, wq.shape[:2]),
              (offsets, "offsets", torch.int32, (E + 1,)), (out, "out", out.dtype, (Ro, n)))
+    _sizes_fit(M | E | n | k | R | Ro)
     _call("omni_quantized_expert_matmul", dev, stream, _dtype_code(out), M, E, n, k, R, Ro,
           xq.data_ptr(), x_scale.data_ptr(), _addr(x_row), wq.data_ptr(), w_scale.data_ptr(),
           offsets.data_ptr(), 1 if swiglu else 0, out.data_ptr(), _addr(out_row))

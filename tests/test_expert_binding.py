@@ -145,3 +145,46 @@ def test_a_fresh_workspace_belongs_to_the_stream_of_the_call(host_calls, monkeyp
     except Reached:
         pass
     assert streams == [mine]
+
+
+def meta(shape, dtype):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+BF, F32, I8, I32 = torch.bfloat16, torch.float32, torch.int8, torch.int32
+FAR = (1 << 32) + 5     # 5 in the library's 32-bit sizes
+FAR_CALLS = {
+    "rows to quantise": lambda: B.quantize_rows(meta((FAR, 16), BF), q=1, scale=1),
+    "columns to quantise": lambda: B.quantize_rows(meta((1, FAR + 11), BF), q=1, scale=1),
+    "rows of x": lambda: B.expert_matmul(meta((FAR, 8), BF), meta((2, 8, 8), BF), meta((3,), I32),
+                                         x_row=meta((4,), I32)),
+    "tasks": lambda: B.expert_matmul(meta((4, 8), BF), meta((2, 8, 8), BF), meta((3,), I32),
+                                     x_row=meta((FAR,), I32), out=meta((4, 8), BF)),
+    "output rows": lambda: B.expert_matmul(meta((4, 8), BF), meta((2, 8, 8), BF), meta((3,), I32),
+                                           out=meta((FAR, 8), BF)),
+    "experts": lambda: B.expert_matmul(meta((4, 8), BF), meta((FAR, 8, 8), BF),
+                                       meta((FAR + 1,), I32)),
+    "outputs": lambda: B.expert_matmul(meta((4, 8), BF), meta((1, FAR, 8), BF), meta((2,), I32)),
+    "rows of dy": lambda: B.expert_weight_grad(meta((4, 8), BF), meta((FAR, 8), BF),
+                                               meta((3,), I32), dw=meta((2, 8, 8), F32)),
+    "experts of dw": lambda: B.expert_weight_grad(meta((4, 8), BF), meta((4, 8), BF),
+                                                  meta((FAR + 1,), I32),
+                                                  dw=meta((FAR, 8, 8), F32)),
+    "rows to combine": lambda: B.expert_combine(meta((FAR, 8), BF), 1, y=meta((FAR, 8), F32)),
+    "rows of dout": lambda: B.expert_combine_backward(meta((FAR, 8), BF), None,
+                                                      meta((FAR, 8), F32), do=1, dgate=1),
+    "8-bit rows": lambda: B.quantized_matmul(meta((FAR, 16), I8), None, meta((8, 16), I8), None,
+                                             out=meta((FAR, 8), BF)),
+    "8-bit weights": lambda: B.quantized_matmul(meta((4, 16), I8), None, meta((FAR, 16), I8), None,
+                                                out=meta((4, FAR), BF)),
+    "8-bit output rows": lambda: B.quantized_expert_matmul(
+        meta((4, 16), I8), None, meta((2, 8, 16), I8), None, meta((3,), I32),
+        out=meta((FAR, 8), BF)),
+}
+
+
+@pytest.mark.parametrize("name", list(FAR_CALLS))
+def test_sizes_past_32_bits_are_refused(host_calls, name):
+    """The library's sizes are 32-bit: one past them would reach it as another one."""
+    with pytest.raises(ValueError, match="2\\^31"):
+        FAR_CALLS[name]()
