@@ -121,3 +121,26 @@ def test_combine_backward_refuses_what_does_not_fit():
     empty = torch.zeros((0, 16), device="cuda")
     do, dgate = B.expert_combine_backward(empty, None, empty)
     assert do.shape == (0, 16) and dgate.shape[0] == 0
+
+
+@pytest.mark.parametrize("counts,n,k", [([9, 0, 12], 40, 72), ([700, 640], 2056, 328)])
+def test_tasks_that_share_an_output_row(counts, n, k):
+    """Every element of the row is one of its tasks' results."""
+    rng = np.random.default_rng(n)
+    E, M = len(counts), sum(counts)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    x = dev(rng.standard_normal((M, k)).astype(np.float32)).bfloat16()
+    w = dev((rng.standard_normal((E, n, k)) * k ** -0.5).astype(np.float32)).bfloat16()
+    alone = host(B.expert_matmul(x, w, dev(off)).float())
+    row = rng.integers(0, M // 2, M).astype(np.int32)
+    out0 = rng.standard_normal((M, n)).astype(np.float32)
+    out = dev(out0).bfloat16()
+    kept = host(out.float())
+    B.expert_matmul(x, w, dev(off), out=out, out_row=dev(row))
+    got = host(out.float())
+    for r in range(M):
+        tasks = np.flatnonzero(row == r)
+        if tasks.size == 0:
+            np.testing.assert_array_equal(got[r], kept[r])
+        else:
+            assert (alone[tasks] == got[r]).any(axis=0).all()
