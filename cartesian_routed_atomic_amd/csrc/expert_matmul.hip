@@ -360,9 +360,9 @@ __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + 
 // of fragments from LDS per 32 MFMAs, which the LDS just keeps up with (tiles
 // of 64 x 64 per wave read 16 KiB); the matrix cores are busy 56 % of the
 // kernel's cycles and the card lowers its clock under them.  65536 tasks of 61
-// experts, 1408 x 2048, bf16: 390 us, 0.96 PFLOP/s; 8192 x 8192 x 8192: 829 us,
-// 1.33 PFLOP/s (int8 439 us, 2.5 POP/s).  HBM-bound with few rows: 2048 tasks of
-// 64 experts, 2 x 704 x 2048, 64 x 128 tiles: 78 us, 4.8 TB/s.
+// experts, 1408 x 2048, bf16: 400 us, 0.94 PFLOP/s; 8192 x 8192 x 8192: 843 us,
+// 1.30 PFLOP/s (int8 446 us, 2.5 POP/s).  HBM-bound with few rows: 2048 tasks of
+// 64 experts, 2 x 704 x 2048, 64 x 128 tiles: 82 us, 4.5 TB/s.
 // QT: W is read as [contraction][columns] (the input gradient).
 // SWIGLU: every 64 columns of Q are 32 gate rows, then the same 32 up rows.
 template <class Op, typename TO, bool QT, bool SWIGLU, int BM, int BN, int WM, int WN, int S>
@@ -555,10 +555,15 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void expert_product_kernel(ExpertM
 // numbers are read one stage ahead as constants at uniform addresses (scalar
 // loads: the vector-memory counter stays with the ring), and the address work
 // is kept to a few instructions per load: at two waves per SIMD the
-// instructions between the MFMAs are what bounds this kernel: 65536 tasks, 64
-// experts of 1408 x 2048 take 512 us (0.74 PFLOP/s) with 54 scalar and 60
-// vector ones per stage and wave (the whole kernel's by its stages), took 543
-// with 74 vector ones and 630 with 105 scalar ones besides.
+// instructions between the MFMAs bound this kernel: 65536 tasks, 64 experts of
+// 1408 x 2048 take 511 us (0.74 PFLOP/s) with 54 scalar and 60 vector ones per
+// stage and wave (the whole kernel's by its stages), took 543 with 74 vector ones
+// and 630 with 105 scalar ones besides.  Memory is not far behind: 1.88e7 L2
+// misses, 2.4 GB (4.7 TB/s), 0.74 of it dW; the x rows of an expert are fetched by
+// every XCD that has one of its column blocks of dy.
+// bf16 sums stay in one accumulator (an MFMA adds 32 tasks, so it rounds 8 times
+// less often than float32's): relative error 2.9e-7 at 8192 tasks in parts, 1.6e-6
+// at 65536 tasks uncut, where a float32 library product has 9.6e-7 and 3.5e-6.
 // Where either row is out of range both are fetched as zeros, which removes the
 // task's term whatever the other row holds: the comparison's lane mask is folded
 // onto both halves of the task (a test of each task's two row numbers took 525 us).
@@ -737,7 +742,8 @@ __global__ __launch_bounds__(256) void expert_wgrad_reduce_kernel(ExpertWgradArg
 // and splitting the contraction gives one token's eight experts 2816 waves.
 // That token's gate and up halves (2 x 704 x 2048, bf16, 46 MB): 12 us, 3.8 TB/s,
 // of which about 4 us are the launch and finding the tile; 4 or 8 waves and 2 to
-// 16 stages ahead measure the same.
+// 16 stages ahead measure the same.  Each wave sums its share of the contraction
+// in one accumulator (float32: an eighth of the steps, not blocks of 128).
 template <class Op, typename TO, bool SWIGLU, int RT, int CT, int KS, int U>
 __global__ __launch_bounds__(KS * 64) void expert_rows_kernel(ExpertMatmulArgs a) {
   using Frag = typename Op::Frag;

@@ -10,9 +10,11 @@
 // The maximum keeps a NaN: a row with a NaN or an infinity has that as its scale
 // and q 0, so that its products are NaN instead of a finite number.
 //
-// HBM-bound: a row is read once, kept in registers and written once.  8192 x
-// 2048 takes 15.1 us from bf16 (3.3 TB/s; the VALU work per element is as long
-// as the loads) and 16.1 us from float32 (5.2 TB/s).
+// A row is read once, kept in registers and written once.  8192 x 2048 takes 15.0
+// us from float32 (5.6 TB/s), bound by HBM, and 14.3 us from bf16 (3.5 TB/s): 10
+// vector instructions per element are 4-5 us of the SIMDs, and since all 8192
+// waves are resident at once they read (6.4 us at a copy's rate), compute and
+// write (3.2 us) one after the other instead of side by side.
 #include "device.hpp"
 #include "launch.hpp"
 
@@ -79,9 +81,9 @@ __device__ void exact_unit(const float (&x)[kUnit], const RowScale& s, uint32_t 
   }
 }
 // Adding 1.5 * 2^23 leaves x / s as an integer in the low bits: its low byte is
-// q.  The VALU work per element bounds this kernel as much as HBM does, so the
-// common case is one fma, one subtraction, one fma for the remainder and the
-// packing (8192 x 2048 bf16: 15.1 us; 16.6 with every element decided on its own).
+// q.  The vector work per element counts beside HBM, so the common case is one
+// fma, one subtraction, one fma for the remainder and the packing (8192 x 2048
+// bf16: 15.1 us when measured; 16.6 with every element decided on its own).
 __device__ __forceinline__ void store_unit(int8_t* p, const float (&x)[kUnit], const RowScale& s) {
   constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
   uint32_t t[kUnit], w[kUnit / 4];

@@ -473,7 +473,8 @@ omni_status omni_shared_mlp(omni_dtype dt, int L, int d, int d_ff, const void* x
  * M rows); tasks whose x row is outside [0, R) have zeros as their result,
  * whatever the weights and their scales hold; output rows outside [0, Ro)
  * are not stored; of two tasks with one output row each element is either's
- * result, not all of them of the same task.  Outputs may not overlap inputs (omni_expert_combine's accumulated y aside).
+ * result, not all of them of the same task.  Outputs may not overlap inputs
+ * (omni_expert_combine's accumulated y aside).
  */
 typedef enum omni_activation {
   OMNI_ACT_NONE = 0,
