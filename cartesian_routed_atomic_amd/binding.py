@@ -19,6 +19,8 @@ OMNI_OK, OMNI_ERR_INVALID_ARG, OMNI_ERR_WORKSPACE, OMNI_ERR_UNSUPPORTED, OMNI_ER
 OMNI_F32, OMNI_BF16 = 0, 1
 EXEC_MODES = {"auto": 0, "expert": 1, "token": 2, "grouped": 3}  # omni_exec_mode
 GROUPINGS = {"active": 0, "window": 1}             # omni_grouping
+SCORES = {"softmax": 0, "sigmoid": 1}              # omni_score_fn
+GATE_NONE, GATE_COLUMN, GATE_TOKEN, GATE_FULL = range(4)  # omni_gate_kind
 ABI_VERSION = 14
 
 # Every symbol the header declares (checked by the CPU test suite).
@@ -35,6 +37,9 @@ EXPORTS = (
     "omni_expert_combine",
     "omni_expert_combine_backward", "omni_quantize_rows", "omni_quantized_matmul",
     "omni_quantized_expert_matmul",
+    "omni_microscale_rows", "omni_microscaled_matmul", "omni_microscaled_expert_matmul",
+    "omni_expert_route", "omni_expert_route_backward", "omni_residual_norm",
+    "omni_residual_norm_backward_workspace", "omni_residual_norm_backward",
 )
 
 
@@ -50,7 +55,7 @@ class ScheduleStruct(ctypes.Structure):
                  "task_gate", "task_index", "flat_expert", "flat_gate")]
 
 
-_vp, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 _SIGS = {
     "omni_abi_version": (_i, []),
     "omni_status_string": (ctypes.c_char_p, [_i]),
@@ -85,6 +90,15 @@ _SIGS = {
     "omni_quantize_rows": (_i, [_i] * 3 + [_vp] * 4),
     "omni_quantized_matmul": (_i, [_i] * 4 + [_vp] * 4 + [_i, _vp, _vp]),
     "omni_quantized_expert_matmul": (_i, [_i] * 7 + [_vp] * 6 + [_i] + [_vp] * 3),
+    "omni_microscale_rows": (_i, [_i] * 3 + [_vp] * 4),
+    "omni_microscaled_matmul": (_i, [_i] * 4 + [_vp] * 4 + [_i, _vp, _vp]),
+    "omni_microscaled_expert_matmul": (_i, [_i] * 7 + [_vp] * 6 + [_i] + [_vp] * 3),
+    "omni_expert_route": (_i, [_i] * 4 + [_vp] * 2 + [_i] * 5 + [_f] + [_vp] * 4),
+    "omni_expert_route_backward": (_i, [_i] * 4 + [_vp] * 3 + [_i] * 2 + [_f, _vp, _i] + [_vp] * 2),
+    "omni_residual_norm": (_i, [_i] * 4 + [_vp] * 2 + [_i] + [_vp] * 2 + [_i, _f, _f] + [_vp] * 4),
+    "omni_residual_norm_backward_workspace": (_sz, [_i] * 3),
+    "omni_residual_norm_backward": (_i, [_i] * 5 + [_vp] * 2 + [_i] + [_vp] * 2 + [_i, _f, _f]
+                                    + [_vp] * 9 + [_sz, _vp]),
     "omni_shared_mlp": (_i, [_i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
 }
 
@@ -738,3 +752,246 @@ def quantized_expert_matmul(xq, x_scale, wq, w_scale, offsets, x_row=None, out=N
           xq.data_ptr(), x_scale.data_ptr(), _addr(x_row), wq.data_ptr(), w_scale.data_ptr(),
           offsets.data_ptr(), 1 if swiglu else 0, out.data_ptr(), _addr(out_row))
     return out
+
+
+def _four_bit(t, name):
+    """Rows and elements per row of packed 4-bit rows [R, k / 2]."""
+    rows, half = _matrix(t, name)
+    return rows, 2 * half, (2 * half + 127) // 128 * 4
+
+
+def microscale_rows(x, q=None, scale=None, stream=None):
+    """omni_microscale_rows: rows in 4-bit floating point, (q [R, k / 2] uint8, scale
+    [R, 4 ceil(k / 128)] uint8): two e2m1 elements a byte, a power-of-two scale
+    2^(byte - 127) for each 32 elements.  Tokens' activations, or weights by output
+    channel (view [E, n, k] experts as [E*n, k])."""
+    (R, k), dev, u8 = _matrix(x, "x"), _device_of(x, "x"), torch.uint8
+    G = (k + 127) // 128 * 4
+    if q is None:
+        q = _empty((R, k // 2), u8, x, stream)
+    if scale is None:
+        scale = _empty((R, G), u8, x, stream)
+    _tensors(dev, (x, "x", x.dtype, (R, k)), (q, "q", u8, (R, k // 2)),
+             (scale, "scale", u8, (R, G)))
+    _sizes_fit(R | k)
+    _call("omni_microscale_rows", dev, stream, _dtype_code(x), R, k, x.data_ptr(), q.data_ptr(),
+          scale.data_ptr())
+    return q, scale
+
+
+def microscaled_matmul(xq, x_scale, wq, w_scale, out=None, out_dtype=torch.bfloat16,
+                       swiglu=False, stream=None):
+    """omni_microscaled_matmul: out [M, n] = x w^T for rows xq [M, k / 2] and weights
+    wq [n, k / 2] in microscale_rows' form (swiglu: [2n, k / 2], out = silu(gate
+    half) * up half)."""
+    (M, k, G), rows, dev = _four_bit(xq, "xq"), _matrix(wq, "wq")[0], _device_of(xq, "xq")
+    if swiglu and rows % 2:
+        raise ValueError("swiglu needs an even number of weight rows")
+    n = rows // 2 if swiglu else rows
+    if out is None:
+        out = _empty((M, n), out_dtype, xq, stream)
+    u8 = torch.uint8
+    _tensors(dev, (xq, "xq", u8, (M, k // 2)), (wq, "wq", u8, (rows, k // 2)),
+             (x_scale, "x_scale", u8, (M, G)), (w_scale, "w_scale", u8, (rows, G)),
+             (out, "out", out.dtype, (M, n)))
+    _sizes_fit(M | n | k)
+    _call("omni_microscaled_matmul", dev, stream, _dtype_code(out), M, n, k, xq.data_ptr(),
+          x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), 1 if swiglu else 0,
+          out.data_ptr())
+    return out
+
+
+def microscaled_expert_matmul(xq, x_scale, wq, w_scale, offsets, x_row=None, out=None,
+                              out_row=None, out_dtype=torch.bfloat16, swiglu=False, stream=None):
+    """omni_microscaled_expert_matmul: expert_matmul over 4-bit rows xq [., k / 2] with
+    x_scale and experts wq [E, n, k / 2] with w_scale [E, n, 4 ceil(k / 128)]."""
+    E, n, half = _experts(wq, swiglu, "wq")
+    (R, k, G), dev = _four_bit(xq, "xq"), _device_of(xq, "xq")
+    M = _tasks(dev, R, x_row, out_row, "out_row")
+    if out is None:
+        out = _empty((M, n), out_dtype, xq, stream)
+    u8, Ro = torch.uint8, out.shape[0]
+    _tensors(dev, (xq, "xq", u8, (R, half)), (wq, "wq", u8, wq.shape),
+             (x_scale, "x_scale", u8, (R, G)), (w_scale, "w_scale", u8, (*wq.shape[:2], G)),
+             (offsets, "offsets", torch.int32, (E + 1,)), (out, "out", out.dtype, (Ro, n)))
+    _sizes_fit(M | E | n | k | R | Ro)
+    _call("omni_microscaled_expert_matmul", dev, stream, _dtype_code(out), M, E, n, k, R, Ro,
+          xq.data_ptr(), x_scale.data_ptr(), _addr(x_row), wq.data_ptr(), w_scale.data_ptr(),
+          offsets.data_ptr(), 1 if swiglu else 0, out.data_ptr(), _addr(out_row))
+    return out
+
+
+def _scores(scores):
+    if scores not in SCORES:
+        raise ValueError(f"scores must be one of {sorted(SCORES)}, got {scores!r}")
+    return SCORES[scores]
+
+
+def expert_route(logits, K, bias=None, scores="softmax", groups=1, top_groups=None, group_best=2,
+                 renormalize=True, scale=1.0, expert_idx=None, gate=None, score=None,
+                 want_score=False, stream=None):
+    """omni_expert_route: (expert_idx [L, K] int32, gate [L, K] float32, score [L, E]
+    float32 or None) of logits [L, E].  The K best of score + bias (of the logits
+    without a bias) in rank order, of the top_groups best groups (None: all); a
+    group's value is the sum of its group_best best.  gate = scale * score, over the
+    sum of the K if renormalize.  score: where to leave the scores (want_score: a
+    fresh array)."""
+    (L, E), dev, f32 = _matrix(logits, "logits"), _device_of(logits, "logits"), torch.float32
+    fn = _scores(scores)
+    if expert_idx is None:
+        expert_idx = _empty((L, K), torch.int32, logits, stream)
+    if gate is None:
+        gate = _empty((L, K), f32, logits, stream)
+    if score is None and want_score:
+        score = _empty((L, E), f32, logits, stream)
+    _tensors(dev, (logits, "logits", logits.dtype, (L, E)),
+             (expert_idx, "expert_idx", torch.int32, (L, K)), (gate, "gate", f32, (L, K)))
+    if bias is not None:
+        _tensors(dev, (bias, "bias", f32, (E,)))
+    if score is not None:
+        _tensors(dev, (score, "score", f32, (L, E)))
+    top = groups if top_groups is None else top_groups
+    _sizes_fit(L | E | K | groups | top)
+    _call("omni_expert_route", dev, stream, _dtype_code(logits), L, E, K, logits.data_ptr(),
+          _addr(bias), fn, groups, top, group_best, 1 if renormalize else 0, scale,
+          expert_idx.data_ptr(), gate.data_ptr(), _addr(score))
+    return expert_idx, gate, score
+
+
+def expert_route_backward(logits, expert_idx, dgate, scores="softmax", renormalize=True,
+                          scale=1.0, dscore=None, dlogits=None, stream=None):
+    """omni_expert_route_backward: dlogits [L, E] of logits' type for dgate [L, K] float32
+    and dscore, the gradient of the scores: [L, E] float32, or [E], the same for
+    every token."""
+    (L, E), dev, f32 = _matrix(logits, "logits"), _device_of(logits, "logits"), torch.float32
+    K = _matrix(expert_idx, "expert_idx")[1]
+    fn = _scores(scores)
+    if dlogits is None:
+        dlogits = _empty((L, E), logits.dtype, logits, stream)
+    _tensors(dev, (logits, "logits", logits.dtype, (L, E)),
+             (expert_idx, "expert_idx", torch.int32, (L, K)), (dgate, "dgate", f32, (L, K)),
+             (dlogits, "dlogits", logits.dtype, (L, E)))
+    shared = dscore is not None and dscore.dim() == 1
+    if dscore is not None:
+        _tensors(dev, (dscore, "dscore", f32, (E,) if shared else (L, E)))
+    _sizes_fit(L | E | K)
+    _call("omni_expert_route_backward", dev, stream, _dtype_code(logits), L, E, K,
+          logits.data_ptr(), expert_idx.data_ptr(), dgate.data_ptr(), fn, 1 if renormalize else 0,
+          scale, _addr(dscore), 1 if shared else 0, dlogits.data_ptr())
+    return dlogits
+
+
+def _gate_kind(gate, L, d):
+    """omni_gate_kind of a gate [d], [L, 1] or [L, d]."""
+    if gate is None:
+        return GATE_NONE
+    if gate.shape == (d,):
+        return GATE_COLUMN
+    if gate.shape == (L, d):
+        return GATE_FULL
+    if gate.shape == (L, 1):
+        return GATE_TOKEN
+    raise ValueError(f"gate has shape {tuple(gate.shape)}, expected ({d},), ({L}, 1) or ({L}, {d})")
+
+
+def residual_norm(r, y=None, weight=None, post_weight=None, post=False, gate=None, alpha=1.0,
+                  eps=1e-6, r_out=None, x=None, want_x=True, stream=None):
+    """omni_residual_norm: (r_out, x) with r_out = r + alpha * gate * n and x = r_out /
+    sqrt(mean r_out^2 + eps) * weight, both [L, d] of r's type.  n is y [L, d] (r's
+    type or float32), normed likewise with post_weight, or with post=True and ones.
+    gate: [d], [L, 1] or [L, d].  Without y: r_out is r, x its norm.  want_x False:
+    the residual alone (x None).  r_out may be r itself."""
+    (L, d), dev, dt = _matrix(r, "r"), _device_of(r, "r"), r.dtype
+    kind, post = _gate_kind(gate, L, d), post or post_weight is not None
+    if y is None:
+        if post or gate is not None:
+            raise ValueError("post norm and gate need y")
+        if r_out is not None and r_out is not r:
+            raise ValueError("without y r_out is r")
+        r_out = r
+    elif r_out is None:
+        r_out = _empty((L, d), dt, r, stream)
+    if not want_x:
+        if x is not None or weight is not None:
+            raise ValueError("x is not wanted but it or its weight given")
+        if y is None:
+            raise ValueError("without y x has to be wanted")
+    elif x is None:
+        x = _empty((L, d), dt, r, stream)
+    _tensors(dev, (r, "r", dt, (L, d)), (r_out, "r_out", dt, (L, d)))
+    for t, name, shape in ((x, "x", (L, d)), (weight, "weight", (d,)),
+                           (post_weight, "post_weight", (d,)),
+                           (gate, "gate", None if gate is None else gate.shape)):
+        if t is not None:
+            _tensors(dev, (t, name, dt, shape))
+    y_code = code = _dtype_code(r)
+    if y is not None:
+        y_code = _dtype_code(y)
+        _tensors(dev, (y, "y", y.dtype, (L, d)))
+    _sizes_fit(L | d)
+    _call("omni_residual_norm", dev, stream, code, y_code, L, d, r.data_ptr(), _addr(y),
+          1 if post else 0, _addr(post_weight), _addr(gate), kind, alpha, eps,
+          r_out.data_ptr() if y is not None else None, _addr(weight), _addr(x))
+    return r_out, x
+
+
+def residual_norm_backward(r_out, dx=None, dr_out=None, y=None, weight=None, post_weight=None,
+                           post=False, gate=None, alpha=1.0, eps=1e-6, out=None, want_sums=True,
+                           workspace=None, stream=None):
+    """omni_residual_norm_backward: dict of dr [L, d] of r_out's type and, where the
+    forward had them, dweight [d] float32, dgate (float32 [d] or [L, 1], or [L, d] of
+    the gate's type), dpost_weight [d] float32, dy of y's type.  r_out: the forward's,
+    r without y.  dx [L, d] (float32 or r_out's type) and dr_out [L, d]: the gradients
+    of x and r_out, one of them may be None.  out: dict of arrays to use.  want_sums
+    False: no gradient of the weights and the gate."""
+    (L, d), dev, dt = _matrix(r_out, "r_out"), _device_of(r_out, "r_out"), r_out.dtype
+    kind, post = _gate_kind(gate, L, d), post or post_weight is not None
+    f32, code = torch.float32, _dtype_code(r_out)
+    if dx is None and dr_out is None:
+        raise ValueError("one of dx and dr_out is needed")
+    if dx is None and weight is not None:
+        raise ValueError("weight belongs to x: without dx it has no part")
+    if y is None and (post or gate is not None):
+        raise ValueError("post norm and gate need y")
+    given = out or {}
+    res = {}
+
+    def result(name, shape, dtype):
+        t = given.get(name)
+        if t is None:
+            t = _empty(shape, dtype, r_out, stream)
+        _tensors(dev, (t, name, dtype, shape))
+        res[name] = t
+    result("dr", (L, d), dt)
+    if want_sums:
+        if weight is not None:
+            result("dweight", (d,), f32)
+        if gate is not None:
+            result("dgate", gate.shape, dt if kind == GATE_FULL else f32)
+        if post_weight is not None:
+            result("dpost_weight", (d,), f32)
+    if y is not None:
+        result("dy", (L, d), y.dtype)
+    for name in given:
+        if name not in res and given[name] is not None:
+            raise ValueError(f"out has {name!r}, which this call does not give")
+    _tensors(dev, (r_out, "r_out", dt, (L, d)))
+    for t, name, dtype, shape in (
+            (y, "y", None if y is None else y.dtype, (L, d)), (weight, "weight", dt, (d,)),
+            (post_weight, "post_weight", dt, (d,)), (dr_out, "dr_out", dt, (L, d)),
+            (dx, "dx", None if dx is None else dx.dtype, (L, d)),
+            (gate, "gate", dt, None if gate is None else gate.shape)):
+        if t is not None:
+            _tensors(dev, (t, name, dtype, shape))
+    _sizes_fit(L | d)
+    nws = 0
+    if "dweight" in res or "dpost_weight" in res or ("dgate" in res and kind == GATE_COLUMN):
+        nws = lib().omni_residual_norm_backward_workspace(code, L, d)
+    ws = _workspace(workspace, nws, r_out, stream)
+    _call("omni_residual_norm_backward", dev, stream, code,
+          code if y is None else _dtype_code(y), code if dx is None else _dtype_code(dx), L, d,
+          r_out.data_ptr(), _addr(y), 1 if post else 0, _addr(post_weight), _addr(gate), kind,
+          alpha, eps, _addr(weight), _addr(dr_out), _addr(dx), res["dr"].data_ptr(),
+          _addr(res.get("dy")), _addr(res.get("dgate")), _addr(res.get("dweight")),
+          _addr(res.get("dpost_weight")), _addr(ws) if nws else None, nws)
+    return res

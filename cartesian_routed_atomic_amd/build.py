@@ -19,7 +19,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libomni.so")
 SOURCES = ["api.hip", "router.hip", "topk.hip", "schedule.hip", "execute.hip", "backward.hip",
            "flat_router.hip", "grouped.hip", "chunked.hip", "expert_matmul.hip",
-           "expert_combine.hip", "quantize.hip"]
+           "expert_combine.hip", "quantize.hip", "microscale.hip", "expert_route.hip",
+           "residual_norm.hip"]
 ARCH = os.environ.get("OMNI_OFFLOAD_ARCH", "gfx950")
 
 

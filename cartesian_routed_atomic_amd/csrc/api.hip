@@ -1,6 +1,7 @@
 // C ABI of the routed atomic-expert layer: argument validation, workspace
 // sizing and dispatch to the gfx950 kernels.  Every check runs on the host
 // before anything is enqueued; nothing here allocates or synchronises.
+#include <math.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -12,6 +13,7 @@ namespace {
 
 constexpr int kAbiVersion = 14;
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 bool fits_i32(long long v) { return v >= 0 && v < (1ll << 31); }
@@ -423,8 +425,11 @@ static omni_status expert_product(omni::ExpertMatmulArgs& a, int k_unit, int n_u
   if (act != OMNI_ACT_NONE && act != OMNI_ACT_SWIGLU) return OMNI_ERR_INVALID_ARG;
   if (act == OMNI_ACT_SWIGLU && a.transpose) return OMNI_ERR_INVALID_ARG;
   a.swiglu = act == OMNI_ACT_SWIGLU;
-  if (!a.w || (a.type == omni::kRowsI8 && !a.w_scale)) return OMNI_ERR_INVALID_ARG;
-  if (a.M > 0 && (!a.x || !a.out || (a.type == omni::kRowsI8 && !a.x_scale)))
+  const bool mx = a.type == omni::kRowsMx;
+  if (!a.w || (a.type == omni::kRowsI8 && !a.w_scale) || (mx && (!a.w_mx || !aligned4(a.w_mx))))
+    return OMNI_ERR_INVALID_ARG;
+  if (a.M > 0 && (!a.x || !a.out || (a.type == omni::kRowsI8 && !a.x_scale) ||
+                  (mx && (!a.x_mx || !aligned4(a.x_mx)))))
     return OMNI_ERR_INVALID_ARG;
   // rows out of range are read as row 0 or R - 1 and their results replaced
   if (a.M > 0 && a.R < 1) return OMNI_ERR_INVALID_ARG;
@@ -434,9 +439,11 @@ static omni_status expert_product(omni::ExpertMatmulArgs& a, int k_unit, int n_u
     return OMNI_ERR_INVALID_ARG;
   if (a.k % k_unit != 0 || (a.transpose && a.n % n_unit != 0)) return OMNI_ERR_UNSUPPORTED;
   if (a.type == omni::kRowsI8 && a.k > 131071) return OMNI_ERR_UNSUPPORTED;
-  if (!omni::expert_matmul_fits(a)) return OMNI_ERR_UNSUPPORTED;
+  if (!(mx ? omni::microscaled_matmul_fits(a) : omni::expert_matmul_fits(a)))
+    return OMNI_ERR_UNSUPPORTED;
   if (a.M == 0) return OMNI_OK;
-  return hip_status(omni::launch_expert_matmul(a, stream));
+  return hip_status(mx ? omni::launch_microscaled_matmul(a, stream)
+                       : omni::launch_expert_matmul(a, stream));
 }
 
 omni_status omni_expert_matmul(omni_dtype dt, int M, int E, int n, int k, int R, int Ro,
@@ -558,6 +565,170 @@ omni_status omni_quantized_expert_matmul(omni_dtype out_dt, int M, int E, int n,
   if (!offsets) return OMNI_ERR_INVALID_ARG;
   return quantized_product(out_dt, M, E, n, k, R, Ro, xq, x_scale, x_row, wq, w_scale, offsets,
                            act, out, out_row, stream);
+}
+
+omni_status omni_microscale_rows(omni_dtype dt, int R, int k, const void* x, uint8_t* q,
+                                 uint8_t* scale, hipStream_t stream) {
+  if (dt != OMNI_F32 && dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
+  if (R < 0 || k < 1) return OMNI_ERR_INVALID_ARG;
+  // sixteen work-items for four blocks of 32
+  if (k % 32 != 0 || static_cast<long long>(R) * ((k + 127ll) / 128) >= 1ll << 28)
+    return OMNI_ERR_UNSUPPORTED;
+  if (R == 0) return OMNI_OK;
+  if (!x || !q || !scale || !aligned16(x) || !aligned16(q) || !aligned4(scale))
+    return OMNI_ERR_INVALID_ARG;
+  return hip_status(omni::launch_microscale_rows(dt == OMNI_BF16, R, k, x, q, scale, stream));
+}
+
+static omni_status microscaled_product(omni_dtype out_dt, int M, int E, int n, int k, int R,
+                                       int Ro, const uint8_t* xq, const uint8_t* xs,
+                                       const int32_t* x_row, const uint8_t* wq, const uint8_t* ws,
+                                       const int32_t* offsets, omni_activation act, void* out,
+                                       const int32_t* out_row, hipStream_t stream) {
+  if (out_dt != OMNI_F32 && out_dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
+  omni::ExpertMatmulArgs a = {};
+  a.type = omni::kRowsMx;
+  a.out_bf16 = out_dt == OMNI_BF16;
+  a.M = M; a.E = E; a.n = n; a.k = k; a.R = R; a.Ro = Ro;
+  a.x = xq; a.x_mx = xs; a.x_row = x_row; a.w = wq; a.w_mx = ws;
+  a.offsets = offsets; a.out = out; a.out_row = out_row;
+  return expert_product(a, 32, 1, act, stream);
+}
+
+omni_status omni_microscaled_matmul(omni_dtype out_dt, int M, int n, int k, const uint8_t* xq,
+                                    const uint8_t* xs, const uint8_t* wq, const uint8_t* ws,
+                                    omni_activation act, void* out, hipStream_t stream) {
+  return microscaled_product(out_dt, M, 1, n, k, M, M, xq, xs, nullptr, wq, ws, nullptr, act, out,
+                             nullptr, stream);
+}
+
+omni_status omni_microscaled_expert_matmul(omni_dtype out_dt, int M, int E, int n, int k, int R,
+                                           int Ro, const uint8_t* xq, const uint8_t* xs,
+                                           const int32_t* x_row, const uint8_t* wq,
+                                           const uint8_t* ws, const int32_t* offsets,
+                                           omni_activation act, void* out,
+                                           const int32_t* out_row, hipStream_t stream) {
+  if (!offsets) return OMNI_ERR_INVALID_ARG;
+  return microscaled_product(out_dt, M, E, n, k, R, Ro, xq, xs, x_row, wq, ws, offsets, act, out,
+                             out_row, stream);
+}
+
+static omni_status route_args(omni_dtype dt, int L, int E, int K, omni_score_fn fn, float scale) {
+  if (dt != OMNI_F32 && dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
+  if (fn != OMNI_SCORE_SOFTMAX && fn != OMNI_SCORE_SIGMOID) return OMNI_ERR_INVALID_ARG;
+  if (L < 0 || E < 1 || K < 1 || !fits_i32(static_cast<long long>(L) * K) || !isfinite(scale))
+    return OMNI_ERR_INVALID_ARG;
+  // a wave holds a token's logits and one selected expert per lane
+  return K > 64 || E > 1024 || L >= 1 << 26 ? OMNI_ERR_UNSUPPORTED : OMNI_OK;
+}
+
+omni_status omni_expert_route(omni_dtype dt, int L, int E, int K, const void* logits,
+                              const float* bias, omni_score_fn fn, int groups, int top_groups,
+                              int group_best, int renormalize, float scale, int32_t* expert_idx,
+                              float* gate, float* score, hipStream_t stream) {
+  if (groups < 1 || top_groups < 1 || top_groups > groups || group_best < 1 || group_best > 2)
+    return OMNI_ERR_INVALID_ARG;
+  const omni_status st = route_args(dt, L, E, K, fn, scale);
+  if (st == OMNI_ERR_INVALID_ARG) return st;
+  if (E % groups != 0 || K > static_cast<long long>(top_groups) * (E / groups))
+    return OMNI_ERR_INVALID_ARG;
+  if (st != OMNI_OK) return st;
+  if (groups > 64) return OMNI_ERR_UNSUPPORTED;
+  if (L == 0) return OMNI_OK;
+  if (!logits || !expert_idx || !gate) return OMNI_ERR_INVALID_ARG;
+  const omni::ExpertRouteArgs a = {dt == OMNI_BF16, L, E, K, fn == OMNI_SCORE_SIGMOID, groups,
+                                   top_groups, group_best, renormalize != 0, scale, logits, bias,
+                                   expert_idx, gate, score};
+  return hip_status(omni::launch_expert_route(a, stream));
+}
+
+omni_status omni_expert_route_backward(omni_dtype dt, int L, int E, int K, const void* logits,
+                                       const int32_t* expert_idx, const float* dgate,
+                                       omni_score_fn fn, int renormalize, float scale,
+                                       const float* dscore, int dscore_shared, void* dlogits,
+                                       hipStream_t stream) {
+  const omni_status st = route_args(dt, L, E, K, fn, scale);
+  if (st != OMNI_OK) return st;
+  if (L == 0) return OMNI_OK;
+  if (!logits || !expert_idx || !dgate || !dlogits) return OMNI_ERR_INVALID_ARG;
+  const omni::ExpertRouteBackwardArgs a = {dt == OMNI_BF16, L, E, K, fn == OMNI_SCORE_SIGMOID,
+                                           renormalize != 0, dscore_shared != 0, scale, logits,
+                                           expert_idx, dgate, dscore, dlogits};
+  return hip_status(omni::launch_expert_route_backward(a, stream));
+}
+
+// has_y: there is a y (an empty batch comes without its arrays)
+static omni_status norm_args(omni_dtype dt, omni_dtype y_dt, int L, int d, bool has_y, int post,
+                             const void* post_w, const void* gate, omni_gate_kind gate_kind,
+                             float alpha, float eps) {
+  if (dt != OMNI_F32 && dt != OMNI_BF16) return OMNI_ERR_INVALID_ARG;
+  if (L < 0 || d < 1 || !isfinite(alpha) || !isfinite(eps) || eps < 0.f)
+    return OMNI_ERR_INVALID_ARG;
+  if (y_dt != OMNI_F32 && y_dt != dt) return OMNI_ERR_INVALID_ARG;
+  if (gate_kind < OMNI_GATE_NONE || gate_kind > OMNI_GATE_FULL) return OMNI_ERR_INVALID_ARG;
+  if ((post_w && !post) || !aligned16(post_w)) return OMNI_ERR_INVALID_ARG;
+  if (gate_kind == OMNI_GATE_NONE ? gate != nullptr : L > 0 && !gate) return OMNI_ERR_INVALID_ARG;
+  const uintptr_t unit = gate_kind != OMNI_GATE_TOKEN ? 16 : dt == OMNI_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(gate) % unit != 0) return OMNI_ERR_INVALID_ARG;
+  if (!has_y && (post || gate_kind != OMNI_GATE_NONE)) return OMNI_ERR_INVALID_ARG;
+  // a workgroup of up to 1024 holds a row
+  const bool fits = d <= omni::kNormMaxWidth && L < 1 << 22;
+  return fits && d % (dt == OMNI_BF16 ? 8 : 4) == 0 ? OMNI_OK : OMNI_ERR_UNSUPPORTED;
+}
+
+omni_status omni_residual_norm(omni_dtype dt, omni_dtype y_dt, int L, int d, const void* r,
+                               const void* y, int post, const void* post_w, const void* gate,
+                               omni_gate_kind gate_kind, float alpha, float eps, void* r_out,
+                               const void* w, void* x, hipStream_t stream) {
+  const omni_status st = norm_args(dt, y_dt, L, d, y || L == 0, post, post_w, gate, gate_kind, alpha, eps);
+  if (st != OMNI_OK) return st;
+  if (L == 0) return OMNI_OK;
+  if (!r || (y == nullptr) != (r_out == nullptr) || (!x && (w || !y)))
+    return OMNI_ERR_INVALID_ARG;
+  const void* rows[] = {r, y, r_out, w, x};
+  for (const void* p : rows)
+    if (!aligned16(p)) return OMNI_ERR_INVALID_ARG;
+  const omni::ResidualNormArgs a = {dt == OMNI_BF16, y_dt == OMNI_BF16, L, d, post != 0, gate_kind,
+                                    alpha, eps, r, y, post_w, gate, r_out, w, x};
+  return hip_status(omni::launch_residual_norm(a, stream));
+}
+
+size_t omni_residual_norm_backward_workspace(omni_dtype dt, int L, int d) {
+  if (dt != OMNI_F32 && dt != OMNI_BF16) return 0;
+  if (L < 0 || d < 1 || d > omni::kNormMaxWidth) return 0;
+  return omni::residual_norm_backward_ws_bytes(dt == OMNI_BF16, L, d);
+}
+
+omni_status omni_residual_norm_backward(omni_dtype dt, omni_dtype y_dt, omni_dtype dx_dt, int L,
+                                        int d, const void* r_out, const void* y, int post,
+                                        const void* post_w, const void* gate,
+                                        omni_gate_kind gate_kind, float alpha, float eps,
+                                        const void* w, const void* dr_out, const void* dx,
+                                        void* dr, void* dy, void* dgate, float* dw,
+                                        float* dpost_w, void* ws, size_t ws_bytes,
+                                        hipStream_t stream) {
+  const omni_status st =
+      norm_args(dt, y_dt, L, d, y || L == 0, post, post_w, gate, gate_kind, alpha, eps);
+  if (st != OMNI_OK) return st;
+  if (dx_dt != OMNI_F32 && dx_dt != dt) return OMNI_ERR_INVALID_ARG;
+  if ((L > 0 && dy && !y) || (dgate && gate_kind == OMNI_GATE_NONE) || (dpost_w && !post))
+    return OMNI_ERR_INVALID_ARG;
+  if (L > 0 && !dx && (w || dw)) return OMNI_ERR_INVALID_ARG;
+  if (L > 0 && (!dr || (!dx && !dr_out) || (dx && !r_out))) return OMNI_ERR_INVALID_ARG;
+  const void* rows[] = {r_out, y, w, dr_out, dx, dr, dy, dw, dpost_w};
+  for (const void* p : rows)
+    if (!aligned16(p)) return OMNI_ERR_INVALID_ARG;
+  const bool row_gate = gate_kind == OMNI_GATE_TOKEN;
+  if (row_gate ? !aligned4(dgate) : !aligned16(dgate)) return OMNI_ERR_INVALID_ARG;
+  const bool sums = dw || dpost_w || (dgate && gate_kind == OMNI_GATE_COLUMN);
+  const size_t need = sums ? omni_residual_norm_backward_workspace(dt, L, d) : 0;
+  if (need > 0 && (!ws || ws_bytes < need || !aligned256(ws))) return OMNI_ERR_WORKSPACE;
+  if (L == 0 && !sums) return OMNI_OK;
+  const omni::ResidualNormBackwardArgs a = {dt == OMNI_BF16, y_dt == OMNI_BF16, dx_dt == OMNI_BF16,
+                                            L, d, post != 0, gate_kind, alpha, eps, r_out, y,
+                                            post_w, gate, w, dr_out, dx, dr, dy, dgate, dw,
+                                            dpost_w};
+  return hip_status(omni::launch_residual_norm_backward(a, static_cast<float*>(ws), stream));
 }
 
 }  // extern "C"

@@ -121,9 +121,9 @@ hipError_t launch_routed_backward(int bf16, int L, int d, int Nr, int Nc, int K,
 
 // expert_matmul.hip: products with experts that are matrices, tasks sorted by
 // expert.  offsets NULL: one dense product (E = 1, every row of it).
-constexpr int kRowsF32 = 0, kRowsBf16 = 1, kRowsI8 = 2;
+constexpr int kRowsF32 = 0, kRowsBf16 = 1, kRowsI8 = 2, kRowsMx = 3;
 struct ExpertMatmulArgs {
-  int type;      // kRowsF32, kRowsBf16 or kRowsI8: x and w
+  int type;      // kRowsF32, kRowsBf16, kRowsI8 or kRowsMx: x and w
   int out_bf16;  // out's type (of the float types: theirs)
   int M, E, n, k, R, Ro;
   int transpose, swiglu;
@@ -135,6 +135,7 @@ struct ExpertMatmulArgs {
   const int32_t* offsets;
   void* out;
   const int32_t* out_row;
+  const uint8_t *x_mx, *w_mx;  // kRowsMx: the scales
 };
 struct ExpertWgradArgs {
   int bf16, M, E, n, k, R, Ry;
@@ -166,5 +167,58 @@ hipError_t launch_expert_combine_backward(int bf16, int L, int K, int n, const v
 long long quantize_rows_blocks(int R, int k);  // workgroups of 256 of the launch
 hipError_t launch_quantize_rows(int bf16, int R, int k, const void* x, int8_t* q, float* scale,
                                 hipStream_t s);
+
+// microscale.hip: 4-bit rows, and products of them.  The arguments are
+// ExpertMatmulArgs of type kRowsMx with k in elements; x and w in packed bytes.
+hipError_t launch_microscale_rows(int bf16, int R, int k, const void* x, uint8_t* q,
+                                  uint8_t* scale, hipStream_t s);
+bool microscaled_matmul_fits(const ExpertMatmulArgs& a);
+hipError_t launch_microscaled_matmul(const ExpertMatmulArgs& a, hipStream_t s);
+
+// expert_route.hip
+struct ExpertRouteArgs {
+  int bf16, L, E, K, sigmoid, groups, top_groups, group_best, renormalize;
+  float scale;
+  const void* logits;
+  const float* bias;
+  int32_t* expert_idx;
+  float* gate;
+  float* score;
+};
+hipError_t launch_expert_route(const ExpertRouteArgs& a, hipStream_t s);
+struct ExpertRouteBackwardArgs {
+  int bf16, L, E, K, sigmoid, renormalize, dscore_shared;
+  float scale;
+  const void* logits;
+  const int32_t* expert_idx;
+  const float* dgate;
+  const float* dscore;
+  void* dlogits;
+};
+hipError_t launch_expert_route_backward(const ExpertRouteBackwardArgs& a, hipStream_t s);
+
+// residual_norm.hip
+constexpr int kNormMaxWidth = 16384;
+constexpr int kGateNone = 0, kGateColumn = 1, kGateToken = 2, kGateFull = 3;
+struct ResidualNormArgs {
+  int bf16, y_bf16, L, d, post, gate_kind;
+  float alpha, eps;
+  const void *r, *y, *post_w, *gate;
+  void* r_out;
+  const void* w;
+  void* x;
+};
+hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s);
+struct ResidualNormBackwardArgs {
+  int bf16, y_bf16, dx_bf16, L, d, post, gate_kind;
+  float alpha, eps;
+  const void *r_out, *y, *post_w, *gate, *w, *dr_out, *dx;
+  void *dr, *dy, *dgate;
+  float *dw, *dpost_w;
+};
+size_t residual_norm_backward_ws_bytes(int bf16, int L, int d);
+// ws: the sums over parts of the rows, where there are any to form
+hipError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a, float* ws,
+                                         hipStream_t s);
 
 }  // namespace omni

@@ -27,7 +27,11 @@
  * matrices, with the same schedule: their ragged products and gradients
  * (omni_expert_matmul, omni_expert_weight_grad), the combination of a token's
  * experts (omni_expert_combine) and products in 8-bit integers
- * (omni_quantize_rows, omni_quantized_matmul, omni_quantized_expert_matmul).
+ * (omni_quantize_rows, omni_quantized_matmul, omni_quantized_expert_matmul) or
+ * 4-bit floating point (omni_microscale_rows, omni_microscaled_matmul,
+ * omni_microscaled_expert_matmul).  Around those experts: the routing of tokens
+ * to them (omni_expert_route) and the norms before and after the block with its
+ * gate and residual (omni_residual_norm), each with its backward.
  *
  * Conventions shared by every call
  *   - All pointers except the `omni_schedule` descriptor itself are DEVICE
@@ -598,6 +602,174 @@ omni_status omni_quantized_expert_matmul(omni_dtype out_dt, int M, int E, int n,
                                          const float* w_scale, const int32_t* offsets,
                                          omni_activation act, void* out, const int32_t* out_row,
                                          hipStream_t stream);
+
+/*
+ * omni_microscale_rows — rows made 4-bit floating point, one power-of-two scale
+ * for each 32 elements (the microscaled MXFP4 format):
+ *
+ *   b = max(exponent field of max |x| as float32 - 2, 0) of each block of 32
+ *       (that is floor(log2 max |x|) - 2 + 127; 0 for blocks of zeros),
+ *   element = x / 2^(b - 127) rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *             and their negatives, ties to the even code, beyond 6 to 6
+ *
+ * x [R, k] of dt; q [R, k / 2] bytes, elements 2j (low half) and 2j + 1 in byte
+ * j, each as sign << 3 | code, codes 0..7 in the order above; scale [R, G] bytes
+ * b, G = 4 * ceil(k / 128): the blocks of a row in fours, the last four's rest
+ * 127.  A block with a NaN or an infinity has b = 255 (NaN) and elements 0: its
+ * row's products are NaN.
+ * Requires k a multiple of 32, else UNSUPPORTED, as is R * G of 2^30 or more;
+ * x and q 16-byte aligned, scale 4-byte aligned.
+ */
+omni_status omni_microscale_rows(omni_dtype dt, int R, int k, const void* x, uint8_t* q,
+                                 uint8_t* scale, hipStream_t stream);
+
+/*
+ * omni_microscaled_matmul — product of rows and weights in that form:
+ *
+ *   out[m, j] = sum_c xq[m, c] 2^(xs[m, c / 32] - 127) wq[j, c] 2^(ws[j, c / 32] - 127)
+ *
+ * xq [M, k / 2], wq [n, k / 2], xs [M, G], ws [n, G] bytes as above (any values;
+ * the last four's rest is not read as a scale); out [M, n] of out_dt.
+ * OMNI_ACT_SWIGLU: wq [2n, k / 2], ws [2n, G], gate half first, out = silu(gate) *
+ * up.  Sums are float32, rounded once to out_dt; scales as small as 2^-127 on both
+ * sides may lose products below float32's normal numbers.
+ * Requires k a multiple of 32, n and k at most 2^22, else UNSUPPORTED; xq, wq, out
+ * 16-byte aligned, xs, ws 4-byte aligned.
+ *
+ * omni_microscaled_expert_matmul — the same over tasks sorted by expert, wq
+ * [E, n, k / 2] and ws [E, n, G] (SWIGLU: 2n), xs [R, G] beside xq [R, k / 2];
+ * rows, offsets and refusals as omni_expert_matmul.
+ */
+omni_status omni_microscaled_matmul(omni_dtype out_dt, int M, int n, int k, const uint8_t* xq,
+                                    const uint8_t* xs, const uint8_t* wq, const uint8_t* ws,
+                                    omni_activation act, void* out, hipStream_t stream);
+omni_status omni_microscaled_expert_matmul(omni_dtype out_dt, int M, int E, int n, int k, int R,
+                                           int Ro, const uint8_t* xq, const uint8_t* xs,
+                                           const int32_t* x_row, const uint8_t* wq,
+                                           const uint8_t* ws, const int32_t* offsets,
+                                           omni_activation act, void* out,
+                                           const int32_t* out_row, hipStream_t stream);
+
+/*
+ * omni_expert_route — a token's experts and gates from its logits z [E]:
+ *
+ *   s = softmax(z) over the E experts, or 1 / (1 + exp(-z)) each;
+ *   c = s + bias (a balance bias: it selects, the gates do not see it);
+ *   groups > 1: group g is the E / groups experts from g * E / groups on, its
+ *   value the sum of its group_best (1 or 2) largest c (a group of one: that c);
+ *   only the top_groups best groups' experts can be selected;
+ *   the K best by (c desc, e asc) in rank order; w_k = s of the k-th, with
+ *   renormalize != 0 divided by the sum of the K;  gate = scale * w
+ *
+ * logits [L, E] of dt; bias [E] float32 or NULL; expert_idx [L, K] int32 out; gate
+ * [L, K] float32 out; score [L, E] float32 out (s) or NULL.
+ * What selects is compared in 64 bits: s and c computed in float64 from the
+ * logits; without a bias s grows with z, so that experts (and groups of
+ * group_best 1) are compared by the logits themselves, exactly.  Ties go to the
+ * lower index, -0 == +0.
+ * Masked experts: a logit of -infinity has s = 0.  A row of nothing else has
+ * s = 0 and gates 0.  A bias of -infinity ranks an expert behind all others that
+ * can be selected.  A NaN logit, or with softmax a +infinity, makes its row's s
+ * NaN (sigmoid: that expert's), and gates of NaN s are NaN; a NaN in what is
+ * compared ranks as -infinity.  K scores of 0 give K gates of 0.  The K ids are distinct and in [0, E) whatever the logits hold.
+ * Renormalised gates are formed from ratios that cannot lose all K (logits of
+ * -200 under sigmoid share out as exp does).
+ * Requires 1 <= K <= top_groups * (E / groups), 1 <= top_groups <= groups, E a
+ * multiple of groups, group_best 1 or 2, scale finite; top_groups == groups
+ * leaves every expert.  K > 64, E > 1024 or groups > 64 is UNSUPPORTED, as is
+ * L >= 2^26; L * K < 2^31.  Deterministic.
+ */
+typedef enum omni_score_fn {
+  OMNI_SCORE_SOFTMAX = 0,
+  OMNI_SCORE_SIGMOID = 1
+} omni_score_fn;
+omni_status omni_expert_route(omni_dtype dt, int L, int E, int K, const void* logits,
+                              const float* bias, omni_score_fn fn, int groups, int top_groups,
+                              int group_best, int renormalize, float scale, int32_t* expert_idx,
+                              float* gate, float* score, hipStream_t stream);
+
+/*
+ * omni_expert_route_backward — the gradient of the logits for gradients of the
+ * gates (and of the scores, e.g. a balance loss's); the selection is piecewise
+ * constant and passes none.  With a_k = scale * dgate_k, e_k the k-th expert, s
+ * recomputed from the logits:
+ *
+ *   renormalised: w_k = s_k / sum_j s_j, m = sum_j w_j a_j, and
+ *     softmax dz[e_k] += w_k (a_k - m);  sigmoid dz[e_k] += w_k (1 - s_k) (a_k - m)
+ *   else u[e_k] += a_k; with dscore u[e] += dscore[e]; and
+ *     softmax dz[e] += s_e (u_e - sum_j s_j u_j);  sigmoid dz[e] += s_e (1 - s_e) u_e
+ *
+ * logits [L, E], dlogits [L, E] of dt (overwritten); expert_idx [L, K] int32,
+ * dgate [L, K] float32; dscore float32 or NULL, [L, E], or with dscore_shared != 0
+ * [E], the same for every token.  An id outside [0, E) adds nothing and has no part
+ * in the sums; the same id twice adds twice.  A logit of -infinity has gradient 0.
+ * Limits as omni_expert_route.  Deterministic.
+ */
+omni_status omni_expert_route_backward(omni_dtype dt, int L, int E, int K, const void* logits,
+                                       const int32_t* expert_idx, const float* dgate,
+                                       omni_score_fn fn, int renormalize, float scale,
+                                       const float* dscore, int dscore_shared, void* dlogits,
+                                       hipStream_t stream);
+
+/*
+ * omni_residual_norm — the end of one block and the beginning of the next:
+ *
+ *   n = y, or with post != 0  y / sqrt(mean y^2 + eps) * post_w
+ *   r_out = r + alpha * g * n                     (g = 1 without a gate)
+ *   x = r_out / sqrt(mean r_out^2 + eps) * w      (before r_out is rounded)
+ *
+ * row by row, means over the d columns, all in float32; each output rounded once.
+ * Without y (NULL; then post = 0, no gate, r_out NULL) it is the norm alone: x =
+ * r / sqrt(mean r^2 + eps) * w.  x may be NULL (then w too) where only the
+ * residual is wanted.
+ * r, r_out, x [L, d] of dt; y [L, d] of y_dt (dt or OMNI_F32, as
+ * omni_expert_combine leaves it); post_w, w [d] of dt or NULL for ones; gate of dt:
+ * [d], [L] or [L, d] by gate_kind.  r_out may be r itself; no other overlap.
+ * Requires d a multiple of 8 (bf16) or 4 (float32) up to 16384 and L < 2^22, else
+ * UNSUPPORTED; alpha finite, eps >= 0 and finite; arrays 16-byte aligned (a gate [L]: 2 / 4).
+ * A row's result depends on that row alone.
+ */
+typedef enum omni_gate_kind {
+  OMNI_GATE_NONE = 0,
+  OMNI_GATE_COLUMN = 1,       /* [d]: one for each column                    */
+  OMNI_GATE_TOKEN = 2,        /* [L]: one for each row                       */
+  OMNI_GATE_FULL = 3          /* [L, d]                                      */
+} omni_gate_kind;
+omni_status omni_residual_norm(omni_dtype dt, omni_dtype y_dt, int L, int d, const void* r,
+                               const void* y, int post, const void* post_w, const void* gate,
+                               omni_gate_kind gate_kind, float alpha, float eps, void* r_out,
+                               const void* w, void* x, hipStream_t stream);
+
+/*
+ * omni_residual_norm_backward — its gradients.  With a = 1 / sqrt(mean r1^2 + eps)
+ * of r1 = r_out as stored (without y: r), b likewise of y, and p = dx * w:
+ *
+ *   dr = dr_out + a p - r1 a^3 mean(p r1)            dw = sum over rows of dx r1 a
+ *   dn = alpha g dr;  dgate = alpha dr n, summed over what the gate is shared by
+ *   post: dpost_w = sum over rows of dn y b;  q = dn post_w,
+ *         dy = b q - y b^3 mean(q y);  else dy = dn
+ *
+ * r_out, dr_out, dr [L, d] of dt; dx [L, d] of dx_dt (dt or OMNI_F32); y, dy of y_dt;
+ * post_w, w, gate as in the forward; dw, dpost_w [d] float32; dgate float32 [d] or
+ * [L], for OMNI_GATE_FULL [L, d] of dt.  Everything overwritten.  dx NULL: x was not
+ * used (then w and dw NULL, r_out is not read and may be NULL); dr_out NULL: none;
+ * one of them is needed.  dy, dgate, dw, dpost_w may be NULL where not wanted; they
+ * and y must be NULL where the forward had none.  dr may be dr_out, dy may be y, and
+ * either may be dx if of its type; no other overlap.
+ * ws / ws_bytes: at least omni_residual_norm_backward_workspace(...) bytes, 256-byte
+ * aligned, or NULL with 0 where none of dw, dpost_w and a column gate's dgate is
+ * wanted (their sums over parts of the rows; one workspace serves one call at a
+ * time).  Sizes as in the forward.  Deterministic: every sum runs in a fixed order.
+ */
+size_t omni_residual_norm_backward_workspace(omni_dtype dt, int L, int d);
+omni_status omni_residual_norm_backward(omni_dtype dt, omni_dtype y_dt, omni_dtype dx_dt, int L,
+                                        int d, const void* r_out, const void* y, int post,
+                                        const void* post_w, const void* gate,
+                                        omni_gate_kind gate_kind, float alpha, float eps,
+                                        const void* w, const void* dr_out, const void* dx,
+                                        void* dr, void* dy, void* dgate, float* dw,
+                                        float* dpost_w, void* ws, size_t ws_bytes,
+                                        hipStream_t stream);
 
 #ifdef __cplusplus
 }
