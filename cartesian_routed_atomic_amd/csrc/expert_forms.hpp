@@ -138,4 +138,74 @@ inline long long wgrad_blocks(const ExpertWgradArgs& a, int tile) {
 }
 inline int wgrad_threads(int tile) { return tile == 256 ? 512 : 256; }
 
+// ------------------------------------------------------------------ 4-bit rows
+
+// The forms of the 4-bit product: rows kernels of 16 x 16 (with SWIGLU 16 x 32
+// weight rows) and 32 x 32, and tiles of tasks x weight rows.
+enum MxForm { kMxRows16, kMxRows32, kMxSmall, kMxMid, kMxWide, kMxBig };
+inline FormShape mx_form_shape(MxForm f, int swiglu) {
+  switch (f) {
+    case kMxRows16: return {16, swiglu ? 32 : 16, 512};
+    case kMxRows32: return {32, 32, 512};
+    case kMxSmall: return {64, 128, 256};
+    case kMxMid: return {128, 128, 256};
+    case kMxWide: return {128, 256, 512};
+    default: return {256, 256, 512};
+  }
+}
+inline long long mx_tiles(const ExpertMatmulArgs& a, MxForm f) {
+  const FormShape h = mx_form_shape(f, a.swiglu);
+  const int bno = a.swiglu ? h.bn / 2 : h.bn;
+  return expert_row_tiles(a.M, a.E, h.bm) * ((a.n + bno - 1) / bno);
+}
+// A workgroup runs its tiles in turn where a row has 16 bytes of scales to load at
+// once (then it also has the two stages that the next tile's loads are ahead).
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+inline bool mx_tiles_in_turn(int k) { return k > 384; }
+// the workgroups that fit on the chip at a time
+inline int mx_slots(MxForm f) { return f == kMxSmall || f == kMxMid ? 512 : 256; }
+inline long long mx_blocks(const ExpertMatmulArgs& a, MxForm f) {
+  const long long t = mx_tiles(a, f);
+  const bool rows = f == kMxRows16 || f == kMxRows32;
+  return rows || !mx_tiles_in_turn(a.k) || t < mx_slots(f) ? t : mx_slots(f);
+}
+// Which one: the tile of least expected time, in us: its rounds of the chip times
+// the stages of 256 elements of a tile, and its start.  Fitted to (us; 2048 inputs,
+// the last two lines 704 and 8192):
+//   tiles of 256 x 256    256 x 256   128 x 256   128 x 128   64 x 128
+//   16                    19.4        13.5        11.0        9.1
+//   64                    20.7        14.9        12.7        12.9
+//   256                   37.4        30.4        30.5        38.9
+//   704                   67.8        77.0        79.8        107
+//   192 (32 experts)      28.8        21.2        19.3        23.3
+//   1024                  311         367         387         498
+// The rows kernels where a few of the smallest tiles have few rows (us; rows of 16
+// and of 32 against 64 x 128 tiles; 2048 inputs):
+//   1 expert, 2048 outputs, 1 / 64 / 128 / 256     6.8 6.9 10 17 / 6.5 6.7 7.7 10 / 8.7 8.8 8.8 8.8
+//   1 expert, 5632 outputs, SWIGLU, 1 / 8 / 32     7.1 7.7 11 / 7.3 8.2 11 / 10 9.8 9.2
+//   64 experts, 1408 outputs, 1 / 8                30 44 / 31 39 / 20 20
+inline MxForm pick_mx_form(const ExpertMatmulArgs& a) {
+  const int h = a.swiglu ? 2 : 1, r = a.M / used_experts(a);
+  const double nk = (a.k + 255) / 256;
+  const double small = expected_tiles(a, 64, 128 / h);
+  if (small <= 96 && small * r <= 2048) return r <= 8 ? kMxRows16 : kMxRows32;
+  auto rounds = [](double tiles, int slots) {
+    const double t = tiles / slots;
+    return t <= 1 ? 1. : t <= 4 ? static_cast<double>(static_cast<int>(t + 0.999)) : t;
+  };
+  // half the chip's slots: alone on a CU, a workgroup is faster
+  auto half = [](double tiles) { return tiles <= 256 ? 0.55 : 1.; };
+  const double mid = expected_tiles(a, 128, 128 / h), wide = expected_tiles(a, 128, 256 / h),
+               big = expected_tiles(a, 256, 256 / h);
+  const double t_small = 4 + rounds(small, 512) * (0.97 * nk + 1.2) * half(small);
+  const double t_mid = 5 + rounds(mid, 512) * (1.5 * nk + 0.8) * half(mid);
+  const double t_wide = 6 + rounds(wide, 256) * (1.43 * nk + 0.7);
+  const double t_big = 14 + (big > 256 ? big / 256 : 1.) * (2.4 * nk + 1);
+  if (t_big <= t_wide && t_big <= t_mid && t_big <= t_small) return kMxBig;
+  if (t_wide <= t_mid && t_wide <= t_small) return kMxWide;
+  return t_mid <= t_small ? kMxMid : kMxSmall;
+}
+
 }  // namespace omni

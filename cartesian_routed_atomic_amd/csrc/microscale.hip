@@ -1,6 +1,7 @@
 // Rows in 4-bit floating point with a power-of-two scale for each 32 elements,
 // and products of them on the scaled matrix-core instruction.
 #include "device.hpp"
+#include "expert_forms.hpp"
 #include "expert_pipeline.hpp"
 #include "expert_tiles.hpp"
 #include "launch.hpp"
@@ -84,6 +85,7 @@ hipError_t launch_microscale_rows(int bf16, int R, int k, const void* x, uint8_t
 
 // 16 rows by 64 bytes of an operand: lane 16 g + r holds the 16 bytes of row r's
 // g-th block of 32 elements, and their scale.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 struct MxFrag {
   i32x4 q;
   int scale;
@@ -183,24 +185,362 @@ __global__ __launch_bounds__(KS * 64) void mx_rows_kernel(ExpertMatmulArgs a) {
   }
 }
 
-static long long mx_rows_blocks(const ExpertMatmulArgs& a) {
-  const long long used = a.E < a.M ? a.E : a.M;
-  return (a.M + used * 15) / 16 * ((a.n + 15) / 16);
+// ------------------------------------------------------------------ tiles
+
+__device__ __forceinline__ void mx_mma32(f32x16& c, i32x4 q, i32x4 p, int qs, int ps,
+                                         std::false_type) {
+  typedef int i32x8 __attribute__((ext_vector_type(8)));
+  const i32x8 a = __builtin_shufflevector(q, q, 0, 1, 2, 3, -1, -1, -1, -1);
+  const i32x8 b = __builtin_shufflevector(p, p, 0, 1, 2, 3, -1, -1, -1, -1);
+  c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 0, qs, 0, ps);
 }
+__device__ __forceinline__ void mx_mma32(f32x16& c, i32x4 q, i32x4 p, int qs, int ps,
+                                         std::true_type) {  // byte 2 of the scales
+  typedef int i32x8 __attribute__((ext_vector_type(8)));
+  const i32x8 a = __builtin_shufflevector(q, q, 0, 1, 2, 3, -1, -1, -1, -1);
+  const i32x8 b = __builtin_shufflevector(p, p, 0, 1, 2, 3, -1, -1, -1, -1);
+  c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 4, 2, qs, 2, ps);
+}
+// Row i of an MFMA's 32 weight rows is row mx_row(i) of the tile's 32: a lane's
+// results are then 16 consecutive columns.
+__device__ __forceinline__ int mx_row(int i) {
+  return 16 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3);
+}
+// A row of a stage is 128 bytes, eight chunks, chunk c of row r stored at c ^
+// mx_swz(r).  A 16-byte-per-lane read is served
+// sixteen lanes at a time (0-3, 12-15, 20-23, 24-27 and the other sixteen, then the
+// same of the upper half) from the 256 bytes of the banks; their rows, of tasks and
+// by mx_row of weights, then lie on sixteen distinct 16-byte slots.
+__device__ __forceinline__ int mx_swz(int r) { return (r >> 1) & 7; }
+
+// Direct global -> LDS load of 4 bytes per lane to dst + 4 lane (dst uniform).
+__device__ __forceinline__ void load_lds4(const void* src, uint32_t dst) {
+  __asm__ volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off"
+                   :
+                   : "v"(src), "s"(dst)
+                   : "memory");
+}
+
+__device__ __forceinline__ TilePlace same_in_wave(TilePlace p) {
+  p.t.e = __builtin_amdgcn_readfirstlane(p.t.e);
+  p.t.m0 = __builtin_amdgcn_readfirstlane(p.t.m0);
+  p.t.m1 = __builtin_amdgcn_readfirstlane(p.t.m1);
+  p.nt = __builtin_amdgcn_readfirstlane(p.nt);
+  return p;
+}
+
+// Tile BM tasks x BN columns, WM x WN waves, ring of S stages of 128 bytes (256
+// elements, a cache line) a row.  A workgroup runs its tiles one after the other as one stream
+// of stages: the next tile's first stages are under way while this one's last run
+// and its results are stored.
+template <typename TO, bool SWIGLU, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(ExpertMatmulArgs a) {
+  constexpr int NW = WM * WN, S = 2;
+  constexpr int TI = BM / WM / 32, TJ = BN / WN / 32;
+  constexpr int IP = BM / 8 / NW, IQ = BN / 8 / NW, I = IP + IQ;  // 1-KiB loads per wave, stage
+  constexpr int IS = (BM + BN + NW * 64 - 1) / (NW * 64);  // loads of 64 rows' scales
+  constexpr int STAGE = (BM + BN) * 128, SCALES = (BM + BN) * 16;
+  constexpr int BNO = SWIGLU ? BN / 2 : BN;            // output columns of a tile
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "loads split evenly");
+  static_assert((BM + BN) % 64 == 0 && BM <= NW * 64, "whole loads of scales and row numbers");
+  static_assert(TI >= 1 && TJ >= (SWIGLU ? 2 : 1) && TJ % (SWIGLU ? 2 : 1) == 0, "column pairs");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * STAGE + S * SCALES + BM * 4];
+
+  const int tid = threadIdx.x, wv = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+  const int N = a.n, n_nt = (N + BNO - 1) / BNO;
+  const ExpertScan scan = a.offsets ? scan_experts(a.offsets, a.E, a.M, BM) : ExpertScan{};
+  // offsets that overlap ask for more tiles than there can be: those are left out
+  const int most = static_cast<int>((a.M + static_cast<long long>(min(a.E, a.M)) * (BM - 1)) / BM);
+  const int total = min(a.offsets ? all_tiles(scan, n_nt) : most * n_nt, most * n_nt);
+  auto place = [&](int v) -> TilePlace {
+    if (!xcd_has(v, total)) return {{0, 0, 0}, 0};
+    const int id = xcd_tile(v, total);
+    TilePlace p = a.offsets ? find_tile(scan, a.offsets, a.E, a.M, BM, n_nt, id)
+                            : place_in_expert(0, 0, a.M, BM, n_nt, id);
+    return same_in_wave(p);
+  };
+  int v = blockIdx.x;
+  TilePlace at = place(v);
+  if (at.t.m0 >= at.t.m1) return;
+
+  const int row_bytes = a.k / 2, G = mx_scale_bytes(a.k), blocks = a.k / kMxBlock;
+  const int nk = (blocks + 7) / 8, left = blocks - (nk - 1) * 8;  // blocks of the last stage
+  const int cut = left < 8 ? nk - 1 : -1;                         // the stage that is not whole
+  const bool wide = G >= 16;
+  const bool in_turn = mx_tiles_in_turn(a.k);
+  const uint32_t ring = lds_address(smem), scales = ring + S * STAGE;
+  int32_t* rows = reinterpret_cast<int32_t*>(smem + S * STAGE + S * SCALES);
+
+  // Sources of this lane's direct loads.  Rows past the end and rows out of range
+  // re-read a valid one: their results are not stored (or stored as zeros).
+  // SWIGLU: every 64 rows of a tile's weights are 32 gate rows, then the same 32 up.
+  const uint8_t *psrc[IP], *ssrc[IS], *qbase;
+  uint32_t qoff[IQ];  // from the tile's first weight row
+  auto sources = [&](const TilePlace& p, auto task_row) {
+    // the lane, opaque: what follows from it alone would otherwise be kept in
+    // registers throughout
+    int l = tid & 63;
+    __asm__ volatile("" : "+v"(l));
+    const int n0 = p.nt * BNO;
+    const size_t first = static_cast<size_t>(p.t.e) * (SWIGLU ? 2 : 1) * N + n0;
+    auto x_row = [&](int r) -> size_t { return min(max(task_row(r), 0), a.R - 1); };
+    auto w_row = [&](int r) {
+      return min(SWIGLU ? (r >> 6) * 32 + (r & 31) : r, N - 1 - n0) + (SWIGLU ? (r >> 5) & 1 : 0) * N;
+    };
+#pragma unroll
+    for (int u = 0; u < IP; ++u) {
+      const int r = (wv * IP + u) * 8 + (l >> 3);
+      psrc[u] = static_cast<const uint8_t*>(a.x) + x_row(r) * row_bytes + ((l & 7) ^ mx_swz(r)) * 16;
+    }
+#pragma unroll
+    for (int u = 0; u < IQ; ++u) {
+      const int r = (wv * IQ + u) * 8 + (l >> 3);
+      qoff[u] = w_row(r) * static_cast<uint32_t>(row_bytes) + ((l & 7) ^ mx_swz(r)) * 16;
+    }
+    qbase = static_cast<const uint8_t*>(a.w) + first * row_bytes;
+#pragma unroll
+    for (int u = 0; u < IS; ++u) {
+      const int r = min((u * NW + wv) * 64 + l, BM + BN - 1);
+      ssrc[u] = r < BM ? a.x_mx + x_row(r) * G : a.w_mx + (first + w_row(r - BM)) * G;
+    }
+  };
+  auto listed_row = [&](const TilePlace& p, int r) {
+    const int m = min(p.t.m0 + r, p.t.m1 - 1);
+    return a.x_row ? a.x_row[m] : m;
+  };
+  // Scales come 16 bytes of a row at a time, those of two stages, with the first of
+  // the two.  A row's last 16 bytes start at G - 16.
+  auto first_scale = [&](int j) { return min(j * 16, max(G - 16, 0)); };
+  auto issue_scales = [&](int j, int slot) {
+#pragma unroll
+    for (int u = 0; u < IS; ++u)
+      if ((u * NW + wv) * 64 < BM + BN)
+        load_lds16(ssrc[u] + first_scale(j), scales + slot * SCALES + (u * NW + wv) * 1024);
+  };
+  // Load u of stage kt into the slot of the stream's q-th.  Past the end of a row the
+  // tasks' data are zeros; the weights', which are finite whatever their bits, are
+  // those of the row's start.
+  auto issue = [&](int kt, int q, int u) {
+    const uint32_t st = ring + (q % S) * STAGE;
+    if (u < IP) {
+      const int first = (wv * IP + u) * 8;
+      const void* src = psrc[u] + static_cast<size_t>(kt) * 128;
+      if (kt == cut && ((l & 7) ^ mx_swz(first + (l >> 3))) >= left) src = kZeroChunk;
+      load_lds16(src, st + first * 128);
+    } else {
+      u -= IP;
+      const int first = (wv * IQ + u) * 8, c = (l & 7) ^ mx_swz(first + (l >> 3));
+      uint32_t off = qoff[u] + kt * 128;
+      if (kt == cut && c >= left) off = qoff[u] - c * 16;
+      load_lds16(qbase, off, st + (BM + first) * 128);
+    }
+  };
+
+  const int i32 = l & 31, h = l >> 5;
+  int wm, wn;
+  wave_place<WM, WN>(wv, wm, wn);
+  const int prow = wm * (BM / WM) + i32, qrow = wn * (BN / WN) + mx_row(i32);
+  // chunk 2 s + h of the lane's row in step s of a stage's four, 64 elements each:
+  // the swizzle leaves the four apart by an exclusive or with 32 s
+  const uint32_t pread = kept(ring + prow * 128 + ((h ^ mx_swz(prow)) << 4));
+  const uint32_t qread = kept(ring + (BM + qrow) * 128 + ((h ^ mx_swz(qrow)) << 4));
+  const uint32_t pscale = kept(scales + prow * 16), qscale = kept(scales + (BM + qrow) * 16);
+  struct Frags {
+    i32x4 p[TI], q[TJ];
+  };
+  struct Scales {
+    int p[TI], q[TJ];  // bytes 0 and 2: of the lane's two chunks
+  };
+  Frags f0, f1;
+  Scales sc, next;
+  auto read_row = [&](Frags& f, int q, int s, int i, int of) {  // share i of `of`
+    const uint32_t st = (q % S) * STAGE, pat = (pread + st) ^ (32 * s), qat = (qread + st) ^ (32 * s);
+#pragma unroll
+    for (int j = i * TJ / of; j < (i + 1) * TJ / of; ++j)
+      f.q[j] = lds_read<i32x4>(qat + j * 32 * 128);
+#pragma unroll
+    for (int r = i * TI / of; r < (i + 1) * TI / of; ++r)
+      f.p[r] = lds_read<i32x4>(pat + r * 32 * 128);
+  };
+  // of steps 2 half and 2 half + 1 of stage kt
+  auto read_scales = [&](Scales& d, int kt, int half, int slot) {
+    const uint32_t base = slot * SCALES + (kt * 8 + half * 4 - first_scale(kt / 2));
+#pragma unroll
+    for (int i = 0; i < TI; ++i) d.p[i] = lds_read<int>(base + pscale + i * 32 * 16);
+#pragma unroll
+    for (int i = 0; i < TJ; ++i) d.q[i] = lds_read<int>(base + qscale + i * 32 * 16);
+  };
+  // past the end of a row the data are zeros, and so that they stay zeros whatever
+  // the last four scales' rest holds, their scale is one
+  auto use_scales = [&](int kt, int half) {
+    const int whole = min(max(left - half * 4, 0), 4);
+    const uint32_t keep = kt == cut && whole < 4 ? (1u << (8 * whole)) - 1u : ~0u;
+    const uint32_t one = 0x7f7f7f7fu & ~keep;
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+      sc.p[i] = static_cast<int>(((static_cast<uint32_t>(next.p[i]) & keep) | one) >> (8 * h));
+#pragma unroll
+    for (int i = 0; i < TJ; ++i)
+      sc.q[i] = static_cast<int>(((static_cast<uint32_t>(next.q[i]) & keep) | one) >> (8 * h));
+  };
+  f32x16 acc[TI][TJ];
+  auto mma_row = [&](const Frags& f, int i, auto step) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+      mx_mma32(acc[i][j], f.q[j], f.p[i], sc.q[j], sc.p[i], step);
+    // keeps the MFMAs here, between the reads ahead of and behind them
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) __asm__ volatile("" : "+v"(acc[i][j])::"memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto store = [&](const TilePlace& p) {
+    // lane (i32, h) holds row 32 i + i32, columns 32 j + 16 h + 0..15
+    TO* out = static_cast<TO*>(a.out);
+    const bool aligned = (N * sizeof(TO)) % 16 == 0;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const int m = p.t.m0 + wm * (BM / WM) + i * 32 + i32;
+      if (m >= p.t.m1) continue;
+      const int row = a.out_row ? a.out_row[m] : m, xr = a.x_row ? a.x_row[m] : m;
+      if (row < 0 || row >= a.Ro) continue;
+      const bool in = xr >= 0 && xr < a.R;  // a row out of range gives zeros
+      TO* dst = out + static_cast<size_t>(row) * N;
+#pragma unroll
+      for (int j = 0; j < TJ; j += SWIGLU ? 2 : 1)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float o[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int e = half * 8 + c;
+            if constexpr (SWIGLU) o[c] = in ? silu_mul(acc[i][j][e], acc[i][j + 1][e]) : 0.f;
+            else o[c] = in ? acc[i][j][e] : 0.f;
+          }
+          store_cols(dst, p.nt * BNO + wn * (BNO / WN) + (SWIGLU ? j / 2 : j) * 32 + h * 16 + half * 8,
+                     N, aligned, o);
+        }
+    }
+  };
+
+  sources(at, [&](int r) { return listed_row(at, r); });
+  if (wide) {
+    issue_scales(0, 0);
+  } else {  // rows of fewer than 16 scales: at most two stages, both in the first slot
+    for (int r = tid; r < BM + BN; r += NW * 64) {
+      uint32_t b[4] = {0, 0, 0, 0};
+      // of this lane's own sources where they are its rows: row (u NW + wv) 64 + l is tid's
+#pragma unroll
+      for (int u = 0; u < IS; ++u)
+        if (r == (u * NW + wv) * 64 + l) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c * 4 < G) b[c] = *reinterpret_cast<const uint32_t*>(ssrc[u] + c * 4);
+        }
+      *reinterpret_cast<uint4*>(smem + S * STAGE + r * 16) = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (s < nk) {
+#pragma unroll
+      for (int u = 0; u < I; ++u) issue(s, s, u);
+    }
+  wait_stages<I, S + 1>(min(S, nk) - 1);
+  lds_barrier();
+  read_row(f0, 0, 0, 0, 1);
+  read_scales(next, 0, 0, 0);
+  int q0 = 0, slot0 = 0;  // of the tile's first stage: its number in the stream, its scales' slot
+  for (;;) {
+    // the same for all lanes, which the compiler loses sight of behind the stores
+    at = same_in_wave(at);
+    q0 = __builtin_amdgcn_readfirstlane(q0);
+    slot0 = __builtin_amdgcn_readfirstlane(slot0);
+    v = __builtin_amdgcn_readfirstlane(v) + gridDim.x;
+    const TilePlace then = in_turn ? place(v) : TilePlace{{0, 0, 0}, 0};
+    const bool more = then.t.m0 < then.t.m1;
+    const int slot1 = (slot0 + (nk + 1) / 2) % S;
+    if (more && a.x_row && wv * 64 < BM)
+      load_lds4(a.x_row + min(then.t.m0 + wv * 64 + l, then.t.m1 - 1),
+                lds_address(rows) + wv * 256);
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) acc[i][j] = f32x16{};
+    // A step's MFMAs run while the fragments of the next one are read.  Before the
+    // last step the next stage has to have landed, after which nobody needs this
+    // one's slot: it is refilled with the stage S further on (of the next tile past
+    // this one's end).
+    for (int kt = 0; kt < nk; ++kt) {
+      const int q = q0 + kt;
+      const bool own = kt + S < nk, end = kt + 1 == nk;
+      const int in = own ? kt + S : kt + S - nk;
+      use_scales(kt, 0);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        read_row(f1, q, 1, i, TI);
+        mma_row(f0, i, std::false_type{});
+      }
+      read_scales(next, kt, 1, (slot0 + kt / 2) % S);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        read_row(f0, q, 2, i, TI);
+        mma_row(f1, i, std::true_type{});
+      }
+      use_scales(kt, 1);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        read_row(f1, q, 3, i, TI);
+        mma_row(f0, i, std::false_type{});
+      }
+      wait_vm_lds<0>();
+      lds_barrier();
+      if (kt + S == nk && more)
+        sources(then, [&](int r) {
+          return a.x_row ? rows[r] : min(then.t.m0 + r, then.t.m1 - 1);
+        });
+      if (in % 2 == 0 && (own || more)) issue_scales(in / 2, ((own ? slot0 : slot1) + in / 2) % S);
+      read_scales(next, end ? 0 : kt + 1, 0, end ? slot1 : (slot0 + (kt + 1) / 2) % S);
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        if (own || more) {
+#pragma unroll
+          for (int u = i * I / TI; u < (i + 1) * I / TI; ++u) issue(in, q + S, u);
+        }
+        read_row(f0, q + 1, 0, i, TI);
+        mma_row(f1, i, std::true_type{});
+      }
+    }
+    store(at);
+    if (!more) break;
+    at = then;
+    q0 += nk;
+    slot0 = slot1;
+  }
+}
+
+// ------------------------------------------------------------------ dispatch
+
 bool microscaled_matmul_fits(const ExpertMatmulArgs& a) {
+  // offsets within a tile's weights are 32 bits, and so is an expert's number rounded up to 64
   if (a.n > 1 << 22 || a.k > 1 << 22 || a.E > 1 << 30) return false;
-  return a.M == 0 || mx_rows_blocks(a) < (1ll << 32) / 512;
+  return a.M == 0 || mx_tiles(a, pick_mx_form(a)) < (1ll << 32) / 512;
 }
-template <typename TO>
-static void run_mx(const ExpertMatmulArgs& a, hipStream_t s) {
-  const unsigned nb = static_cast<unsigned>(mx_rows_blocks(a));
-  if (a.swiglu) mx_rows_kernel<TO, true, 1, 2, 8, 2><<<nb, 512, 0, s>>>(a);
-  else mx_rows_kernel<TO, false, 1, 1, 8, 2><<<nb, 512, 0, s>>>(a);
+template <typename TO, bool SW>
+static hipError_t run_mx(const ExpertMatmulArgs& a, hipStream_t s) {
+  const MxForm f = pick_mx_form(a);
+  const unsigned nb = static_cast<unsigned>(mx_blocks(a, f));
+  if (f == kMxRows16) mx_rows_kernel<TO, SW, 1, SW ? 2 : 1, 8, 2><<<nb, 512, 0, s>>>(a);
+  else if (f == kMxRows32) mx_rows_kernel<TO, SW, 2, 2, 8, 2><<<nb, 512, 0, s>>>(a);
+  else if (f == kMxSmall) mx_tile_kernel<TO, SW, 64, 128, 2, 2><<<nb, 256, 0, s>>>(a);
+  else if (f == kMxMid) mx_tile_kernel<TO, SW, 128, 128, 2, 2><<<nb, 256, 0, s>>>(a);
+  else if (f == kMxWide) mx_tile_kernel<TO, SW, 128, 256, 2, 4><<<nb, 512, 0, s>>>(a);
+  else mx_tile_kernel<TO, SW, 256, 256, 2, 4><<<nb, 512, 0, s>>>(a);
+  return hipGetLastError();
 }
 hipError_t launch_microscaled_matmul(const ExpertMatmulArgs& a, hipStream_t s) {
-  if (a.out_bf16) run_mx<uint16_t>(a, s);
-  else run_mx<float>(a, s);
-  return hipGetLastError();
+  if (a.out_bf16) return a.swiglu ? run_mx<uint16_t, true>(a, s) : run_mx<uint16_t, false>(a, s);
+  return a.swiglu ? run_mx<float, true>(a, s) : run_mx<float, false>(a, s);
 }
 
 }  // namespace omni
