@@ -1,261 +1,571 @@
 // A token's experts and gates from its logits, and the gradient of the logits.
 //
-// What selects is the score plus the balance bias, s + b.  Scores of different
-// experts can lie within float32's rounding of each other, so they are compared
-// in float64; without a bias the score grows with the logit, which is compared
-// as it stands.
+// What selects is the score plus the balance bias, c = s + b.  The c of different
+// experts can lie within float32's rounding of each other, so their order is that
+// of float64.  Nearly always float32 tells it: c is computed in float32, whose error
+// is below 2^-20 of the row's largest score and 2^-23 of c (below), and where any
+// two that had to be told apart are closer than four times that, the wave decides
+// them again in float64 (16384 tokens, 256 experts, 8 of them, sigmoid: about one
+// wave in 40; with float64 throughout 43.9 us).  Without a bias the score grows
+// with the logit, which is compared as it stands.
+//
+// Error of a score: v_exp_f32 and the reciprocal are good to one unit in the last
+// place, the product with log2 e rounds at 2^-24 of the exponent x, which is
+// x 2^-24 of e^-x: at most 0.54 x 2^-24 of the largest score; the sum of up to 1024
+// positive terms in at most 22 steps adds 22 x 2^-24 of the score.
 #include "device.hpp"
 #include "launch.hpp"
 
 namespace omni {
 
+// T lanes (a DPP row, or the wave) share a token; lane l of them holds experts
+// 4 T (v / 4) + 4 l + v % 4 in its slots v < V: four consecutive ones per load.
+constexpr int kRow = 16;
+template <int ctrl>
+__device__ __forceinline__ uint32_t dpp_row(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), ctrl, 0xf, 0xf, true));
+}
+// op over the token's lanes, the result in all of them; halves are added to halves,
+// so every lane forms the same sum
+template <int T, class Op>
+__device__ __forceinline__ uint32_t over_lanes(uint32_t v, Op op) {
+  v = op(v, dpp_row<0x128>(v));  // row_ror 8, 4, 2, 1
+  v = op(v, dpp_row<0x124>(v));
+  v = op(v, dpp_row<0x122>(v));
+  v = op(v, dpp_row<0x121>(v));
+  if constexpr (T == kWave) {
+    v = op(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 16)));
+    v = op(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 32)));
+  }
+  return v;
+}
+template <int T>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return __uint_as_float(over_lanes<T>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+template <int T>
+__device__ __forceinline__ float lanes_max(float v) {
+  return __uint_as_float(over_lanes<T>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+template <int T>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  return over_lanes<T>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int T>
+__device__ __forceinline__ uint64_t lanes_max(uint64_t v) {
+  const uint32_t hi = lanes_max<T>(static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = lanes_max<T>(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+template <int T>
+__device__ __forceinline__ int lanes_min(int v) {  // of numbers not negative
+  return static_cast<int>(over_lanes<T>(static_cast<uint32_t>(v), [](uint32_t a, uint32_t b) {
+    return min(a, b);
+  }));
+}
+// true in all of the token's lanes if in any
+template <int T>
+__device__ __forceinline__ bool lanes_any(bool v) {
+  const uint64_t m = __ballot(v);
+  if constexpr (T == kWave) return m != 0;
+  return (m >> (lane() & ~(kRow - 1)) & 0xffffu) != 0;
+}
+
 __device__ __forceinline__ float load_logit(const float* p, size_t i) { return p[i]; }
 __device__ __forceinline__ float load_logit(const uint16_t* p, size_t i) {
   return __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
 }
+// Values e .. e + 3 of a row of E, `past` behind its end; vec: rows start at 4 elements
+__device__ __forceinline__ void load4(const float* row, int e, int E, bool vec, float past,
+                                      float* v) {
+  if (vec && e < E) {
+    const float4 f = *reinterpret_cast<const float4*>(row + e);
+    v[0] = f.x;
+    v[1] = f.y;
+    v[2] = f.z;
+    v[3] = f.w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = e + i < E ? row[e + i] : past;
+}
+__device__ __forceinline__ void load4(const uint16_t* row, int e, int E, bool vec, float past,
+                                      float* v) {
+  if (vec && e < E) {
+    const uint2 u = *reinterpret_cast<const uint2*>(row + e);
+    v[0] = bf_lo(u.x);
+    v[1] = bf_hi(u.x);
+    v[2] = bf_lo(u.y);
+    v[3] = bf_hi(u.y);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = e + i < E ? load_logit(row, e + i) : past;
+}
+__device__ __forceinline__ void store4(float* row, int e, int E, bool vec, const float* v) {
+  if (vec && e < E) {
+    *reinterpret_cast<float4*>(row + e) = make_float4(v[0], v[1], v[2], v[3]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (e + i < E) row[e + i] = v[i];
+}
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+__device__ __forceinline__ void store4(uint16_t* row, int e, int E, bool vec, const float* v) {
+  if (vec && e < E) {
+    *reinterpret_cast<uint2*>(row + e) = make_uint2(bf16_bits(v[0]) | bf16_bits(v[1]) << 16,
+                                                    bf16_bits(v[2]) | bf16_bits(v[3]) << 16);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (e + i < E) row[e + i] = static_cast<uint16_t>(bf16_bits(v[i]));
+}
+template <typename P>
+__device__ __forceinline__ bool fours(const P* p, int E) {  // rows of E start at 4 elements
+  return E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(P) - 1)) == 0;
+}
 
-// Order-preserving map float64 -> uint64 (never 0), -0 onto +0, NaN as -infinity.
-__device__ __forceinline__ uint64_t dkey(double v) {
+// Order-preserving keys of what is compared: never 0, -0 onto +0, NaN as -infinity.
+__device__ __forceinline__ uint32_t order_key(float v) { return fkey(v == v ? v : -INFINITY); }
+__device__ __forceinline__ uint64_t order_key(double v) {
   if (!(v == v)) v = -INFINITY;
   const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
   return u >> 63 ? ~u : u | 1ull << 63;
 }
-__device__ __forceinline__ double sigmoid64(double z) { return 1.0 / (1.0 + exp(-z)); }
 
-// Gates' weights of a wave's K selected experts (lane k: the k-th's logit z, not
-// read from lane K on) over their sum.  Scores are formed relative to the largest,
-// so that scores too small for float32 still share out: softmax e^(z - m);
-// sigmoid, times e^-m for m = min(largest z, 0): e^(z - m) / (1 + e^z), or
-// 1 / (1 + e^-z) where z > 0 (then m = 0).
+// Gates' weights of a token's selected experts (a lane each: logit z where mine) over
+// their sum.  Scores are formed relative to the largest, so that scores too small
+// for float32 still share out: softmax e^(z - m); sigmoid, times e^-m for m =
+// min(largest z, 0): e^(z - m) / (1 + e^z), or 1 / (1 + e^-z) where z > 0 (then m = 0).
+template <int T>
 __device__ __forceinline__ float shared_weight(float z, bool mine, bool sigmoid) {
-  const float top = wave_max(mine ? z : -INFINITY);
+  const float top = lanes_max<T>(mine ? z : -INFINITY);
   float e;
   if (sigmoid) {
     const float m = fminf(top, 0.f);
-    e = z > 0.f ? 1.f / (1.f + expf(-z)) : expf(z - m) / (1.f + expf(z));
+    e = z > 0.f ? 1.f / (1.f + __expf(-z)) : __expf(z - m) / (1.f + __expf(z));
   } else {
-    e = expf(z - top);
+    e = __expf(z - top);
   }
   if (!mine) e = 0.f;
-  const float sum = wave_sum(e);
-  return top == -INFINITY && !(sum > 0.f) && !__any(mine && z != z) ? 0.f : e / sum;
+  const float sum = lanes_sum<T>(e);
+  // nothing but -infinity: weights of 0
+  return top == -INFINITY && !lanes_any<T>(mine && z != z) ? 0.f : e / sum;
 }
 
-// One wave per token; lane l holds experts l, l + 64, ..  The K best are taken one
-// at a time: every lane's best, the wave's best of those, which is then struck off.
-template <typename T, int V>
-__global__ __launch_bounds__(64) void expert_route_kernel(ExpertRouteArgs a) {
-  __shared__ double value[V * 64];
+// The K best of the token's slots by key, a round each: the slot of round k holds k + 1
+// afterwards, which is below every key.  Keys are taken to differ: equal ones share
+// their round, and where the keys then run out, earlier rounds' slots are struck
+// again.  seen(k, key): the key of round k, K or less if there was none.
+template <int T, int V, class Seen>
+__device__ __forceinline__ void strike_best(uint32_t (&key)[V], int K, Seen seen) {
+  for (int k = 0; k < K; ++k) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = max(best, key[v]);
+    best = lanes_max<T>(best);
+    seen(k, best);
+    const uint32_t taken = k + 1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = key[v] == best ? taken : key[v];
+  }
+}
+// The same over a wave by (key desc, expert asc): lane k gets the k-th expert.  Slot v of
+// lane l is expert 64 v + l.
+template <int V>
+__device__ __forceinline__ int take_best(uint64_t (&key)[V], int K) {
+  const int l = lane();
+  int mine = 0;
+  for (int k = 0; k < K; ++k) {
+    uint64_t best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = max(best, key[v]);
+    best = lanes_max<kWave>(best);
+    int at = 1 << 20;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v) at = key[v] == best ? v * 64 + l : at;
+    at = lanes_min<kWave>(at);
+    if (l == k) mine = at;
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = key[v] == best && at == v * 64 + l ? 0 : key[v];
+  }
+  return mine;
+}
+
+// Which groups stay, a bit each in the result: lane g sums group g's best.  c: the
+// token's E values in LDS.  far(a, b): the last that stays and the first that does
+// not are told apart.
+template <int T, typename F, class Far>
+__device__ __forceinline__ uint64_t best_groups(const F* c, const ExpertRouteArgs& a, int l,
+                                                Far far) {
+  const int size = a.E / a.groups;
+  F b1 = -INFINITY, b2 = -INFINITY;
+  if (l < a.groups) {
+    // started l further on: the lanes then read different banks
+    int i = l % size;
+    for (int n = 0; n < size; ++n) {
+      F m = c[l * size + i];
+      m = m == m ? m : -INFINITY;
+      b2 = b2 > m ? b2 : (b1 < m ? b1 : m);
+      b1 = b1 > m ? b1 : m;
+      i = i + 1 == size ? 0 : i + 1;
+    }
+  }
+  const F value = a.group_best == 2 && size > 1 ? b1 + b2 : b1;
+  using Key = decltype(order_key(value));
+  const Key key = l < a.groups ? order_key(value) : 0;
+  int ahead = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const Key other = __shfl(key, g, T);
+    ahead += other > key || (other == key && g < l) ? 1 : 0;
+  }
+  const F last = __shfl(value, __ffsll(static_cast<long long>(
+                                   __ballot(ahead == a.top_groups - 1 && l < a.groups) >>
+                                   (T == kWave ? 0 : lane() & ~(T - 1)))) - 1, T);
+  const F first = __shfl(value, __ffsll(static_cast<long long>(
+                                    __ballot(ahead == a.top_groups && l < a.groups) >>
+                                    (T == kWave ? 0 : lane() & ~(T - 1)))) - 1, T);
+  far(last, first);
+  const uint64_t stay = __ballot(l < a.groups && ahead < a.top_groups);
+  return T == kWave ? stay : stay >> (lane() & ~(T - 1)) & ((1ull << T) - 1);
+}
+
+// One token decided in float64 by its whole wave; lane k gets the k-th expert.  slots:
+// room for the token's values.
+template <typename L, int V, bool GROUPS>
+__device__ __forceinline__ int decide_exactly(const ExpertRouteArgs& a, size_t t, double* slots) {
   const int l = lane(), E = a.E;
-  const size_t t = blockIdx.x;
-  const T* row = static_cast<const T*>(a.logits) + t * E;
+  const L* row = static_cast<const L*>(a.logits) + t * E;
   float z[V];
-  double s[V], c[V];
-  float top = -INFINITY;
+  double d[V];
   bool bad = false;
+  float top = -INFINITY;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = l + v * 64;
-    z[v] = e < E ? load_logit(row, e) : -INFINITY;
+    z[v] = v * 64 + l < E ? load_logit(row, v * 64 + l) : -INFINITY;
     bad |= z[v] != z[v] || z[v] == INFINITY;
     top = fmaxf(top, z[v]);
   }
-  bad = __any(bad) && !a.sigmoid;
-  if (!a.sigmoid) {
-    top = wave_max(top);
-    double sum = 0.0;
+  const bool sums = GROUPS && (a.bias || a.group_best == 2);
+  if (a.bias || sums) {
+    const double from = wave_max(top);
+    double total = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      s[v] = z[v] == -INFINITY ? 0.0 : exp(static_cast<double>(z[v]) - top);
-      sum += s[v];
+      d[v] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(z[v])))
+                       : z[v] == -INFINITY ? 0.0 : exp(z[v] - from);
+      total += d[v];
     }
-    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    if (!a.sigmoid) {
+      bad = __any(bad);
+      for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = bad ? __builtin_nan("") : sum > 0.0 ? s[v] / sum : 0.0;
-  } else {
+      for (int v = 0; v < V; ++v)
+        d[v] = bad ? __builtin_nan("") : total > 0.0 ? d[v] / total : 0.0;
+    }
+    if (a.bias) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = sigmoid64(z[v]);
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = l + v * 64;
-    c[v] = a.bias && e < E ? s[v] + a.bias[e] : z[v];
-    if (a.score && e < E) a.score[t * E + e] = static_cast<float>(s[v]);
+      for (int v = 0; v < V; ++v)
+        if (v * 64 + l < E) d[v] += a.bias[v * 64 + l];
+    }
   }
   uint64_t stay = ~0ull;
-  const int size = E / a.groups;
-  if (a.top_groups < a.groups) {
+  if constexpr (GROUPS) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const double m = !a.bias && a.group_best == 2 ? s[v] : c[v];
-      value[l + v * 64] = m == m ? m : -INFINITY;
-    }
-    __syncthreads();
-    double b1 = -INFINITY, b2 = -INFINITY;
-    if (l < a.groups) {
-      for (int i = 0; i < size; ++i) {
-        const double m = value[l * size + i];
-        b2 = fmax(b2, fmin(b1, m));
-        b1 = fmax(b1, m);
-      }
-    }
-    const uint64_t key = l < a.groups ? dkey(a.group_best == 2 && size > 1 ? b1 + b2 : b1) : 0;
-    int ahead = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const uint64_t other = __shfl(key, g);
-      ahead += other > key || (other == key && g < l) ? 1 : 0;
-    }
-    stay = __ballot(l < a.groups && ahead < a.top_groups);
+    for (int v = 0; v < V; ++v)
+      if (v * 64 + l < E) slots[v * 64 + l] = sums ? d[v] : z[v];
+    wave_lds_fence();
+    stay = best_groups<kWave>(slots, a, l, [](double, double) {});
+    wave_lds_fence();
   }
+  const float per = GROUPS ? static_cast<float>(a.groups) / E : 0.f;
   uint64_t key[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = l + v * 64;
-    key[v] = e < E && (stay >> (e / size) & 1) ? dkey(c[v]) : 0;
+    const int e = v * 64 + l;
+    const bool in = e < E && (!GROUPS || (stay >> static_cast<int>((e + 0.5f) * per) & 1) != 0);
+    key[v] = in ? order_key(a.bias ? d[v] : static_cast<double>(z[v])) : 0ull;
   }
-  if (a.top_groups == a.groups) {
+  return take_best<V>(key, a.K);
+}
+
+// T lanes per token, V slots each.
+template <typename L, int T, int V, bool GROUPS>
+__global__ __launch_bounds__(256) void expert_route_kernel(ExpertRouteArgs a) {
+  constexpr int PER = kWave / T, ROOM = T * V + 8;  // tokens of a wave; 8: other banks each
+  // a token's values, in float32 for all of a wave's tokens, in float64 for one
+  constexpr int BYTES = !GROUPS ? 8 : PER * ROOM * 4 > ROOM * 8 ? PER * ROOM * 4 : ROOM * 8;
+  __shared__ __attribute__((aligned(16))) uint8_t room[4][BYTES];
+  __shared__ int list[4][kWave];
+  const int l = lane() & (T - 1), E = a.E, wv = threadIdx.x >> 6, sub = lane() / T;
+  const size_t first = (static_cast<size_t>(blockIdx.x) * 4 + wv) * PER, t0 = first + sub;
+  const bool live = t0 < static_cast<size_t>(a.L);
+  const size_t t = live ? t0 : a.L - 1;  // lanes without a token go along
+  const L* row = static_cast<const L*>(a.logits) + t * E;
+  const bool vec = fours(static_cast<const L*>(a.logits), E);
+  auto expert = [&](int v) { return 4 * T * (v / 4) + 4 * l + v % 4; };
+  float z[V], s[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = l + v * 64 < E ? dkey(c[v]) : 0;
-  }
-  int mine = 0;
-  for (int k = 0; k < a.K; ++k) {
-    uint64_t best = 0;
-    int at = 0;
+  for (int v = 0; v < V; v += 4) load4(row, expert(v), E, vec, -INFINITY, z + v);
+  float top = -INFINITY;
+  bool bad = false;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (key[v] > best) {
-        best = key[v];
-        at = l + v * 64;
-      }
-    for (int o = 32; o > 0; o >>= 1) {
-      const uint64_t k2 = __shfl_xor(best, o);
-      const int a2 = __shfl_xor(at, o);
-      if (k2 > best || (k2 == best && a2 < at)) {
-        best = k2;
-        at = a2;
-      }
+  for (int v = 0; v < V; ++v) top = fmaxf(top, z[v]);
+  top = lanes_max<T>(top);
+  const float from = top == -INFINITY ? 0.f : top;  // a row of -infinity alone has scores of 0
+  const bool biased = a.bias != nullptr;
+  const bool sums = GROUPS && (biased || a.group_best == 2);  // groups compared by scores
+  float largest = 1.f;  // score, or above it
+  if (!a.sigmoid) {
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      bad |= z[v] != z[v] || z[v] == INFINITY;
+      s[v] = __expf(z[v] - from);
+      sum += s[v];
     }
-    if (l == k) mine = at;
+    bad = lanes_any<T>(bad);
+    sum = lanes_sum<T>(sum);
+    largest = bad ? __builtin_nanf("") : sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] *= largest;
+  } else if (a.score || biased || sums) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = __builtin_amdgcn_rcpf(1.f + __expf(-z[v]));
+  }
+  if (a.score && live) {
+    float* out = a.score + t * E;
+    const bool whole = fours(a.score, E);
+#pragma unroll
+    for (int v = 0; v < V; v += 4) store4(out, expert(v), E, whole, s + v);
+  }
+  // what is compared, in float32
+  float c[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) c[v] = z[v];
+  if (biased) {
+    const bool whole = fours(a.bias, E);
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+      float b[4];
+      load4(a.bias, expert(v), E, whole, 0.f, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[v + i] = s[v + i] + b[i];
+    }
+  }
+  const float close = largest * 0x1p-18f;
+  bool unsure = false;
+  uint64_t stay = ~0ull;
+  if constexpr (GROUPS) {
+    float* mine = reinterpret_cast<float*>(room[wv]) + sub * ROOM;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (at == l + v * 64) key[v] = 0;
+      if (expert(v) < E) mine[expert(v)] = sums && !biased ? s[v] : c[v];
+    wave_lds_fence();
+    stay = best_groups<T>(mine, a, l, [&](float x, float y) {
+      if (sums) unsure |= !(x - y > 2 * close + 0x1p-19f * fabsf(x));
+    });
   }
-  const bool in = l < a.K;
+  // e / size of whole numbers up to 1024: the quotient of e + 1/2 is 1/1024 or more
+  // from a whole number, far beyond float32's rounding
+  const float per = GROUPS ? static_cast<float>(a.groups) / E : 0.f;
+  uint32_t key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = expert(v);
+    const bool in = e < E && (!GROUPS || (stay >> static_cast<int>((e + 0.5f) * per) & 1) != 0);
+    key[v] = in ? order_key(c[v]) : 0u;
+  }
+  uint32_t before = ~0u;
+  auto apart = [&](uint32_t best) {  // from the round before's; not where one is no number
+    const float x = fkey_inv(before), y = fkey_inv(best);
+    unsure |= !(x - y > close + 0x1p-20f * fabsf(x));
+  };
+  strike_best<T, V>(key, a.K, [&](int k, uint32_t best) {
+    unsure |= best <= static_cast<uint32_t>(a.K);  // equal keys left none for this round
+    if (biased && k > 0) apart(best);
+    before = best;
+  });
+  if (biased) {  // the first that is left has to be apart from the last taken
+    uint32_t best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = max(best, key[v]);
+    best = lanes_max<T>(best);
+    if (best > static_cast<uint32_t>(a.K)) apart(best);
+  }
+  int* ids = list[wv] + sub * T;
+  int count = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (key[v] - 1u < static_cast<uint32_t>(a.K)) {
+      ids[key[v] - 1u] = expert(v);
+      ++count;
+    }
+  }
+  // equal keys shared a round: more slots than rounds.  Otherwise each of K rounds
+  // struck one slot, and the list is whole.
+  unsure |= lanes_sum<T>(static_cast<float>(count)) != static_cast<float>(a.K);
+  uint64_t open = __ballot(unsure && live);
+  wave_lds_fence();
+  while (open != 0) {
+    const int at = __ffsll(static_cast<long long>(open)) - 1;  // a lane of the token
+    const int which = at / T;
+    const int id = decide_exactly<L, (T * V + 63) / 64, GROUPS>(
+        a, first + which, reinterpret_cast<double*>(room[wv]));
+    wave_lds_fence();
+    if (lane() < a.K) list[wv][which * T + lane()] = id;
+    wave_lds_fence();
+    open &= T == kWave ? 0ull : ~(((1ull << (T & 63)) - 1) << (which * T));
+  }
+  const bool in = l < a.K && live;  // the list of no token may not be whole
+  const int mine = in ? ids[l] : 0;
   const float zk = in ? load_logit(row, mine) : 0.f;
   float w;
-  if (a.renormalize) {
-    w = shared_weight(zk, in, a.sigmoid);
-  } else {
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v) value[l + v * 64] = s[v];
-    __syncthreads();
-    w = static_cast<float>(value[mine]);
-  }
+  if (a.renormalize) w = shared_weight<T>(zk, in, a.sigmoid);
+  else if (a.sigmoid) w = 1.f / (1.f + __expf(-zk));
+  else w = largest * __expf(zk - from);
   if (in) {
     a.expert_idx[t * a.K + l] = mine;
     a.gate[t * a.K + l] = bad ? __builtin_nanf("") : a.scale * w;
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store_logit(T* p, float v) {
-  if constexpr (sizeof(T) == 4) *p = v;
-  else *p = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-}
-
-// One wave per token, lane k the k-th selected expert.
-template <typename T, int V>
+// T lanes per token; lane k also the k-th selected expert.  The selected experts'
+// terms meet the token's row in LDS.
+template <typename L, int T, int V>
 __global__ __launch_bounds__(256) void expert_route_backward_kernel(ExpertRouteBackwardArgs a) {
-  const int l = lane(), E = a.E;
-  const size_t t = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (t >= static_cast<size_t>(a.L)) return;
-  const T* row = static_cast<const T*>(a.logits) + t * E;
-  int id = l < a.K ? a.expert_idx[t * a.K + l] : -1;
-  const bool in = l < a.K && id >= 0 && id < E;
-  if (!in) id = -1;
+  constexpr int PER = kWave / T, ROOM = T * V;
+  __shared__ __attribute__((aligned(16))) float room[4 * PER * ROOM];
+  const int l = lane() & (T - 1), E = a.E;
+  const size_t t0 = static_cast<size_t>(blockIdx.x) * 4 * PER + threadIdx.x / T;
+  const bool live = t0 < static_cast<size_t>(a.L);
+  const size_t t = live ? t0 : a.L - 1;
+  const L* row = static_cast<const L*>(a.logits) + t * E;
+  const bool vec = fours(static_cast<const L*>(a.logits), E);
+  auto expert = [&](int v) { return 4 * T * (v / 4) + 4 * l + v % 4; };
+  const bool dense = a.dscore || !a.renormalize;
+  float z[V], ds[V];
+  if (dense) {
+#pragma unroll
+    for (int v = 0; v < V; v += 4) load4(row, expert(v), E, vec, -INFINITY, z + v);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) ds[v] = 0.f;
+  if (a.dscore) {
+    const float* up = a.dscore + (a.dscore_shared ? 0 : t * E);
+    const bool whole = fours(a.dscore, E);
+#pragma unroll
+    for (int v = 0; v < V; v += 4) load4(up, expert(v), E, whole, 0.f, ds + v);
+  }
+  const int id = l < a.K ? a.expert_idx[t * a.K + l] : -1;
+  const bool in = id >= 0 && id < E;
   float up = in ? a.scale * a.dgate[t * a.K + l] : 0.f;
+  float* mine = room + (threadIdx.x / T) * ROOM;
+#pragma unroll
+  for (int v = 0; v < V; v += 4)
+    *reinterpret_cast<float4*>(mine + expert(v)) = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.renormalize) {
     const float zk = in ? load_logit(row, id) : 0.f;
-    const float w = shared_weight(zk, in, a.sigmoid);
-    const float m = wave_sum(in ? w * up : 0.f);
+    const float w = shared_weight<T>(zk, in, a.sigmoid);
+    const float m = lanes_sum<T>(in ? w * up : 0.f);
     up = in ? w * (up - m) : 0.f;
-    if (a.sigmoid && in) up *= 1.f / (1.f + expf(zk));
+    if (a.sigmoid && in) up *= 1.f / (1.f + __expf(zk));
   }
+  // the same expert more than once: each of its lanes forms the sum, in order
+  float sum = 0.f;
+  for (int k = 0; k < a.K; ++k) {
+    const int other = __shfl(id, k, T);
+    const float x = __shfl(up, k, T);
+    if (other == id) sum += x;
+  }
+  wave_lds_fence();
+  if (in) mine[id] = sum;
+  wave_lds_fence();
   float u[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) u[v] = 0.f;
-  for (int k = 0; k < a.K; ++k) {
-    const int e = __builtin_amdgcn_readlane(id, k);
-    const float x = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(up), k));
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (e == l + v * 64) u[v] += x;
+  for (int v = 0; v < V; v += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(mine + expert(v));
+    u[v] = f.x;
+    u[v + 1] = f.y;
+    u[v + 2] = f.z;
+    u[v + 3] = f.w;
   }
-  float s[V], ds[V], rest = 0.f;
-  const bool dense = a.dscore || !a.renormalize;
+  float dz[V];
   if (dense) {
-    float z[V], top = -INFINITY, sum = 0.f;
+    if (!a.renormalize) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = l + v * 64;
-      z[v] = e < E ? load_logit(row, e) : -INFINITY;
-      top = fmaxf(top, z[v]);
-      ds[v] = a.dscore && e < E ? a.dscore[(a.dscore_shared ? 0 : t * E) + e] : 0.f;
-      if (!a.renormalize) ds[v] += u[v];
+      for (int v = 0; v < V; ++v) ds[v] += u[v];
     }
     if (!a.sigmoid) {
-      top = wave_max(top);
-      float dot = 0.f;
+      float top = -INFINITY, total = 0.f, dot = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) top = fmaxf(top, z[v]);
+      top = lanes_max<T>(top);
+      if (top == -INFINITY) top = 0.f;  // scores of 0
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        s[v] = z[v] == -INFINITY ? 0.f : expf(z[v] - top);
-        sum += s[v];
+        z[v] = __expf(z[v] - top);
+        total += z[v];
+        dot = fmaf(z[v], ds[v], dot);
       }
-      sum = wave_sum(sum);
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      total = lanes_sum<T>(total);
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      const float rest = lanes_sum<T>(dot) * inv;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        s[v] *= inv;
-        dot = fmaf(s[v], ds[v], dot);
-      }
-      rest = wave_sum(dot);
+      for (int v = 0; v < V; ++v) dz[v] = z[v] * inv * (ds[v] - rest);
     } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) s[v] = 1.f / (1.f + expf(-z[v])) * (1.f / (1.f + expf(z[v])));
+      for (int v = 0; v < V; ++v)
+        dz[v] = __builtin_amdgcn_rcpf(1.f + __expf(-z[v])) *
+                __builtin_amdgcn_rcpf(1.f + __expf(z[v])) * ds[v];
     }
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = l + v * 64;
-    if (e >= E) continue;
-    const float dz = (dense ? s[v] * (ds[v] - rest) : 0.f) + (a.renormalize ? u[v] : 0.f);
-    store_logit(static_cast<T*>(a.dlogits) + t * E + e, dz);
+  for (int v = 0; v < V; ++v) dz[v] = (dense ? dz[v] : 0.f) + (a.renormalize ? u[v] : 0.f);
+  if (live) {
+    L* out = static_cast<L*>(a.dlogits) + t * E;
+    const bool whole = fours(static_cast<const L*>(a.dlogits), E);
+#pragma unroll
+    for (int v = 0; v < V; v += 4) store4(out, expert(v), E, whole, dz + v);
   }
 }
 
-template <typename T>
+// Sixteen lanes per token where they hold its experts, groups and selection.
+template <typename L, bool GROUPS>
 static void run_route(const ExpertRouteArgs& a, hipStream_t s) {
-  const unsigned nb = static_cast<unsigned>(a.L);
-  if (a.E <= 64) expert_route_kernel<T, 1><<<nb, 64, 0, s>>>(a);
-  else if (a.E <= 128) expert_route_kernel<T, 2><<<nb, 64, 0, s>>>(a);
-  else if (a.E <= 256) expert_route_kernel<T, 4><<<nb, 64, 0, s>>>(a);
-  else if (a.E <= 512) expert_route_kernel<T, 8><<<nb, 64, 0, s>>>(a);
-  else expert_route_kernel<T, 16><<<nb, 64, 0, s>>>(a);
+  const unsigned n = static_cast<unsigned>(a.L), few = (n + 15) / 16, many = (n + 3) / 4;
+  if (a.E <= 256 && a.K <= 16 && a.groups <= 16) {
+    if (a.E <= 64) expert_route_kernel<L, 16, 4, GROUPS><<<few, 256, 0, s>>>(a);
+    else if (a.E <= 128) expert_route_kernel<L, 16, 8, GROUPS><<<few, 256, 0, s>>>(a);
+    else expert_route_kernel<L, 16, 16, GROUPS><<<few, 256, 0, s>>>(a);
+  } else if (a.E <= 256) expert_route_kernel<L, 64, 4, GROUPS><<<many, 256, 0, s>>>(a);
+  else if (a.E <= 512) expert_route_kernel<L, 64, 8, GROUPS><<<many, 256, 0, s>>>(a);
+  else expert_route_kernel<L, 64, 16, GROUPS><<<many, 256, 0, s>>>(a);
 }
 hipError_t launch_expert_route(const ExpertRouteArgs& a, hipStream_t s) {
-  if (a.bf16) run_route<uint16_t>(a, s);
-  else run_route<float>(a, s);
+  const bool groups = a.top_groups < a.groups;
+  if (a.bf16) groups ? run_route<uint16_t, true>(a, s) : run_route<uint16_t, false>(a, s);
+  else groups ? run_route<float, true>(a, s) : run_route<float, false>(a, s);
   return hipGetLastError();
 }
-template <typename T>
+template <typename L>
 static void run_route_backward(const ExpertRouteBackwardArgs& a, hipStream_t s) {
-  const unsigned nb = (static_cast<unsigned>(a.L) + 3) / 4;
-  if (a.E <= 64) expert_route_backward_kernel<T, 1><<<nb, 256, 0, s>>>(a);
-  else if (a.E <= 128) expert_route_backward_kernel<T, 2><<<nb, 256, 0, s>>>(a);
-  else if (a.E <= 256) expert_route_backward_kernel<T, 4><<<nb, 256, 0, s>>>(a);
-  else if (a.E <= 512) expert_route_backward_kernel<T, 8><<<nb, 256, 0, s>>>(a);
-  else expert_route_backward_kernel<T, 16><<<nb, 256, 0, s>>>(a);
+  const unsigned n = static_cast<unsigned>(a.L), few = (n + 15) / 16, many = (n + 3) / 4;
+  if (a.E <= 256 && a.K <= 16) {
+    if (a.E <= 64) expert_route_backward_kernel<L, 16, 4><<<few, 256, 0, s>>>(a);
+    else if (a.E <= 128) expert_route_backward_kernel<L, 16, 8><<<few, 256, 0, s>>>(a);
+    else expert_route_backward_kernel<L, 16, 16><<<few, 256, 0, s>>>(a);
+  } else if (a.E <= 256) expert_route_backward_kernel<L, 64, 4><<<many, 256, 0, s>>>(a);
+  else if (a.E <= 512) expert_route_backward_kernel<L, 64, 8><<<many, 256, 0, s>>>(a);
+  else expert_route_backward_kernel<L, 64, 16><<<many, 256, 0, s>>>(a);
 }
 hipError_t launch_expert_route_backward(const ExpertRouteBackwardArgs& a, hipStream_t s) {
   if (a.bf16) run_route_backward<uint16_t>(a, s);
