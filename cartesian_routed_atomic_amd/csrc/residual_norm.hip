@@ -160,156 +160,246 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_kernel(Resi
 
 // Sums over rows: every workgroup adds up the rows it takes (its first, then every
 // G-th) in registers and leaves a partial sum of each column.
-constexpr int kNormParts = 512;
 constexpr int kSumW = 0, kSumPost = 1, kSumGate = 2;
-__host__ __device__ inline int norm_parts(int L, int rows) {
-  const int n = (L + rows - 1) / rows;
-  return n < kNormParts ? n : kNormParts;
-}
 
-template <typename T, typename TY, typename TX, int NT, int EPT>
+// 16 bytes of a row as loaded
+template <typename T, int U>
+struct Unit {
+  uint4 v[U * sizeof(T) / 16];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(U * sizeof(T) / 16); ++i)
+      v[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(U * sizeof(T) / 16); ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void floats(float (&f)[U]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < U; i += 4) {
+        f[i] = __uint_as_float(v[i / 4].x);
+        f[i + 1] = __uint_as_float(v[i / 4].y);
+        f[i + 2] = __uint_as_float(v[i / 4].z);
+        f[i + 3] = __uint_as_float(v[i / 4].w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; i += 8) {
+        const uint4 u = v[i / 8];
+        f[i] = bf_lo(u.x);
+        f[i + 1] = bf_hi(u.x);
+        f[i + 2] = bf_lo(u.y);
+        f[i + 3] = bf_hi(u.y);
+        f[i + 4] = bf_lo(u.z);
+        f[i + 5] = bf_hi(u.z);
+        f[i + 6] = bf_lo(u.w);
+        f[i + 7] = bf_hi(u.w);
+      }
+    }
+  }
+};
+
+// NT threads per row, as in the forward.  The row's sums are formed in one pass and
+// meet once: with t = g post_w y, the mean of q y is that of alpha t dr, and dr's
+// three terms give three sums.  The next row's loads are under way meanwhile
+// (AHEAD), and what belongs to a column stays in registers over the rows; rows too
+// long for that have neither.
+template <typename T, typename TY, typename TX, int NT, int EPT, bool AHEAD>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_kernel(
     ResidualNormBackwardArgs a, float* sums) {
   constexpr int U = 16 / sizeof(T), NV = EPT / U, ROWS = NT < 256 ? 256 / NT : 1;
-  __shared__ float part[2][2][3][16];
+  constexpr int NS = 6;
+  __shared__ float part[2][NS][16];
+  __shared__ __attribute__((aligned(16))) float joined[ROWS > 1 ? ROWS * NT * EPT : 4];
   const int t = threadIdx.x % NT, sub = threadIdx.x / NT, d = a.d;
   const T* gate = static_cast<const T*>(a.gate);
   const float over = 1.f / d;
   auto column = [&](int u) { return (u * NT + t) * U; };
-  float total[3][NV][U] = {};
-  int turn = 0;
-  for (size_t row = static_cast<size_t>(blockIdx.x) * ROWS + sub; row < static_cast<size_t>(a.L);
-       row += static_cast<size_t>(gridDim.x) * ROWS, turn ^= 1) {
+  struct Column {
+    Unit<T, U> w, pw, g;  // ones where there are none
+  };
+  Column kept[NV];
+  auto of_column = [&](Column& v, int u) {
+    constexpr uint32_t kOne = sizeof(T) == 4 ? 0x3f800000u : 0x3f803f80u;
+    v.w.v[0] = v.pw.v[0] = v.g.v[0] = make_uint4(kOne, kOne, kOne, kOne);
+    if (column(u) >= d) return;
+    if (a.w) v.w.load(static_cast<const T*>(a.w) + column(u));
+    if (a.post_w) v.pw.load(static_cast<const T*>(a.post_w) + column(u));
+    if (a.gate_kind == kGateColumn) v.g.load(gate + column(u));
+  };
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) of_column(kept[u], u);
+  }
+  struct Row {
+    Unit<T, U> dr[NV], r[NV], g[NV];
+    Unit<TX, U> dx[NV];
+    Unit<TY, U> y[NV];
+    float gate;
+  };
+  auto fetch = [&](Row& v, size_t row) {
+    const bool live = row < static_cast<size_t>(a.L);
     const size_t base = row * d;
-    float dr[NV][U], r[NV][U], dx[NV][U], y[NV][U];
+    v.gate = live && a.gate_kind == kGateToken ? load_one(gate + row) : 1.f;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-#pragma unroll
-      for (int i = 0; i < U; ++i) dr[u][i] = r[u][i] = dx[u][i] = y[u][i] = 0.f;
-      if (column(u) >= d) continue;
-      if (a.dr_out) load_unit(static_cast<const T*>(a.dr_out) + base + column(u), dr[u]);
+      v.dr[u].clear();
+      v.r[u].clear();
+      v.dx[u].clear();
+      v.y[u].clear();
+      v.g[u].clear();
+      if (!live || column(u) >= d) continue;
+      if (a.dr_out) v.dr[u].load(static_cast<const T*>(a.dr_out) + base + column(u));
       if (a.dx) {
-        load_unit(static_cast<const T*>(a.r_out) + base + column(u), r[u]);
-        load_unit(static_cast<const TX*>(a.dx) + base + column(u), dx[u]);
+        v.r[u].load(static_cast<const T*>(a.r_out) + base + column(u));
+        v.dx[u].load(static_cast<const TX*>(a.dx) + base + column(u));
       }
-      if (a.y) load_unit(static_cast<const TY*>(a.y) + base + column(u), y[u]);
+      if (a.y) v.y[u].load(static_cast<const TY*>(a.y) + base + column(u));
+      if (a.gate_kind == kGateFull) v.g[u].load(gate + base + column(u));
     }
-    float v[3] = {0.f, 0.f, 0.f};  // sums of r1^2, p r1, y^2
+  };
+  float total[3][NV][U] = {};
+  const size_t step = static_cast<size_t>(gridDim.x) * ROWS;
+  const bool full = a.gate_kind == kGateFull;
+  int turn = 0;
+  // the rows of a workgroup's turn: all its threads take part in the same turns
+  size_t row = static_cast<size_t>(blockIdx.x) * ROWS + sub;
+  size_t first = static_cast<size_t>(blockIdx.x) * ROWS;
+  Row now, then;
+  fetch(now, row);
+  for (; first < static_cast<size_t>(a.L); first += step, row += step, turn ^= 1) {
+    const bool live = row < static_cast<size_t>(a.L);
+    const size_t base = row * d;
+    if constexpr (AHEAD) fetch(then, row + step);
+    float v[NS] = {};  // sums of r1^2, p r1, y^2, t dr_out, t p, t r1
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      float w[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) w[i] = 1.f;
-      if (a.w && column(u) < d) load_unit(static_cast<const T*>(a.w) + column(u), w);
+      float r[U], dx[U], y[U], dr[U], wf[U], pf[U], g[U];
+      now.r[u].floats(r);
+      now.dx[u].floats(dx);
+      now.y[u].floats(y);
+      now.dr[u].floats(dr);
+      Column k;
+      if constexpr (AHEAD) k = kept[u];
+      else of_column(k, u);
+      k.w.floats(wf);
+      k.pw.floats(pf);
+      (full ? now.g[u] : k.g).floats(g);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        v[0] = fmaf(r[u][i], r[u][i], v[0]);
-        v[1] = fmaf(dx[u][i] * w[i], r[u][i], v[1]);
-        v[2] = fmaf(y[u][i], y[u][i], v[2]);
+        const float p = dx[i] * wf[i], q = g[i] * pf[i] * y[i];
+        v[0] = fmaf(r[i], r[i], v[0]);
+        v[1] = fmaf(p, r[i], v[1]);
+        v[2] = fmaf(y[i], y[i], v[2]);
+        v[3] = fmaf(q, dr[i], v[3]);
+        v[4] = fmaf(q, p, v[4]);
+        v[5] = fmaf(q, r[i], v[5]);
       }
     }
-    row_sums<NT>(v, part[turn][0]);
-    if (a.dx) {
-      const float s = rsqrtf(fmaf(v[0], over, a.eps)), c = s * s * s * (v[1] * over);
-#pragma unroll
-      for (int u = 0; u < NV; ++u) {
-        float w[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) w[i] = 1.f;
-        if (a.w && column(u) < d) load_unit(static_cast<const T*>(a.w) + column(u), w);
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          dr[u][i] += s * (dx[u][i] * w[i]) - c * r[u][i];
-          total[kSumW][u][i] = fmaf(dx[u][i], r[u][i] * s, total[kSumW][u][i]);
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < NV; ++u)
-      if (column(u) < d) store_unit(static_cast<T*>(a.dr) + base + column(u), dr[u]);
-    if (!a.y) continue;
+    row_sums<NT>(v, part[turn]);
+    const float s = a.dx ? rsqrtf(fmaf(v[0], over, a.eps)) : 0.f;
+    const float c = a.dx ? s * s * s * (v[1] * over) : 0.f;
     const float b = a.post ? rsqrtf(fmaf(v[2], over, a.eps)) : 1.f;
-    float row_gate = a.alpha;
-    if (a.gate_kind == kGateToken) row_gate *= load_one(gate + row);
-    float m[2] = {0.f, 0.f};  // sums of q y, dr n
-    float q[NV][U];
+    const float qy = v[3] + s * v[4] - c * v[5];  // sum of t dr
+    const float row_gate = a.alpha * now.gate;
+    const float back = a.post ? b * b * b * (row_gate * qy * over) : 0.f;
+    if (live && a.gate_kind == kGateToken && a.dgate && t == 0)
+      static_cast<float*>(a.dgate)[row] = a.alpha * b * qy;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      float w[U], g[U], dg[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) w[i] = g[i] = 1.f;
-      if (column(u) < d) {
-        if (a.post_w) load_unit(static_cast<const T*>(a.post_w) + column(u), w);
-        if (a.gate_kind == kGateColumn || a.gate_kind == kGateFull)
-          load_unit(gate + (a.gate_kind == kGateFull ? base : 0) + column(u), g);
-      }
+      float r[U], dx[U], y[U], dr[U], wf[U], pf[U], g[U], dg[U];
+      now.r[u].floats(r);
+      now.dx[u].floats(dx);
+      now.y[u].floats(y);
+      now.dr[u].floats(dr);
+      Column k;
+      if constexpr (AHEAD) k = kept[u];
+      else of_column(k, u);
+      k.w.floats(wf);
+      k.pw.floats(pf);
+      (full ? now.g[u] : k.g).floats(g);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const float dn = row_gate * g[i] * dr[u][i], yb = y[u][i] * b;
-        q[u][i] = dn * w[i];
-        dg[i] = a.alpha * dr[u][i] * (yb * w[i]);
-        m[0] = fmaf(q[u][i], y[u][i], m[0]);
-        m[1] += dg[i];
+        dr[i] += s * (dx[i] * wf[i]) - c * r[i];
+        total[kSumW][u][i] = fmaf(dx[i], r[i] * s, total[kSumW][u][i]);
+        const float dn = row_gate * g[i] * dr[i], yb = y[i] * b;
+        dg[i] = a.alpha * dr[i] * (yb * pf[i]);
         total[kSumPost][u][i] = fmaf(dn, yb, total[kSumPost][u][i]);
         total[kSumGate][u][i] += dg[i];
+        y[i] = b * (dn * pf[i]) - back * y[i];
       }
-      if (a.gate_kind == kGateFull && a.dgate && column(u) < d)
-        store_unit(static_cast<T*>(a.dgate) + base + column(u), dg);
+      if (!live || column(u) >= d) continue;
+      store_unit(static_cast<T*>(a.dr) + base + column(u), dr);
+      if (full && a.dgate) store_unit(static_cast<T*>(a.dgate) + base + column(u), dg);
+      if (a.dy) store_unit(static_cast<TY*>(a.dy) + base + column(u), y);
     }
-    const bool gate_sum = a.gate_kind == kGateToken && a.dgate;
-    if (a.post || gate_sum) row_sums<NT>(m, part[turn][1]);
-    if (gate_sum && t == 0) static_cast<float*>(a.dgate)[row] = m[1];
-    if (!a.dy) continue;
-    const float c = a.post ? b * b * b * (m[0] * over) : 0.f;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      if (column(u) >= d) continue;
-#pragma unroll
-      for (int i = 0; i < U; ++i) q[u][i] = b * q[u][i] - c * y[u][i];
-      store_unit(static_cast<TY*>(a.dy) + base + column(u), q[u]);
-    }
+    if constexpr (AHEAD) now = then;
+    else fetch(now, row + step);
   }
   if (!sums) return;
-  // the ROWS rows at a time of a workgroup are parts of their own
+  const float* wanted[3] = {a.dw, a.dpost_w,
+                            a.gate_kind == kGateColumn ? static_cast<const float*>(a.dgate)
+                                                       : nullptr};
 #pragma unroll
-  for (int k = 0; k < 3; ++k)
+  for (int k = 0; k < 3; ++k) {
+    if (!wanted[k]) continue;
+    float* out = sums + (static_cast<size_t>(blockIdx.x) * 3 + k) * d;
+    if constexpr (ROWS > 1) {  // the rows at a time of a workgroup, in order
+      __syncthreads();
 #pragma unroll
-    for (int u = 0; u < NV; ++u)
-      if (column(u) < d)
-        store_unit(sums + ((static_cast<size_t>(blockIdx.x) * ROWS + sub) * 3 + k) * d + column(u),
-                   total[k][u]);
-}
-
-// The partial sums in part order; 64 columns by 16 runs of the parts a workgroup.
-__global__ __launch_bounds__(256) void norm_sums_kernel(const float* sums, int parts, int d,
-                                                        float* dw, float* dpost, float* dgate) {
-  __shared__ float4 run[16][17];
-  float* out = blockIdx.y == kSumW ? dw : blockIdx.y == kSumPost ? dpost : dgate;
-  if (!out) return;
-  const int c = blockIdx.x * 64 + (threadIdx.x & 15) * 4, z = threadIdx.x >> 4;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (c < d) {
-    const int per = (parts + 15) / 16, end = min(parts, (z + 1) * per);
-    for (int p = z * per; p < end; ++p) {
-      const float4 v =
-          *reinterpret_cast<const float4*>(sums + (static_cast<size_t>(p) * 3 + blockIdx.y) * d + c);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
+      for (int u = 0; u < NV; ++u) store_unit(joined + sub * NT * EPT + column(u), total[k][u]);
+      __syncthreads();
+      for (int col = threadIdx.x; col < d; col += 256) {
+        float x = joined[col];
+#pragma unroll
+        for (int i = 1; i < ROWS; ++i) x += joined[i * NT * EPT + col];
+        out[col] = x;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < NV; ++u)
+        if (column(u) < d) store_unit(out + column(u), total[k][u]);
     }
   }
-  run[z][threadIdx.x & 15] = s;
-  __syncthreads();
-  if (z != 0 || c >= d) return;
-  for (int i = 1; i < 16; ++i) {
-    const float4 v = run[i][threadIdx.x];
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+}
+
+// The partial sums in part order: 16 columns by 64 runs of the parts a workgroup.
+__global__ __launch_bounds__(256) void norm_sums_kernel(const float* sums, int parts, int d,
+                                                        float* dw, float* dpost, float* dgate) {
+  __shared__ float4 run[64][4];
+  float* out = blockIdx.y == kSumW ? dw : blockIdx.y == kSumPost ? dpost : dgate;
+  if (!out) return;
+  const int l = threadIdx.x & 3, c = blockIdx.x * 16 + l * 4, z = threadIdx.x >> 2;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [](float4& x, const float4& y) {
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+  };
+  if (c < d) {
+    const int per = (parts + 63) / 64, end = min(parts, (z + 1) * per);
+#pragma unroll 8
+    for (int p = z * per; p < end; ++p)
+      add(s, *reinterpret_cast<const float4*>(sums + (static_cast<size_t>(p) * 3 + blockIdx.y) * d +
+                                              c));
   }
-  *reinterpret_cast<float4*>(out + c) = s;
+  run[z][l] = s;
+  __syncthreads();
+  if (z >= 8) return;
+  s = run[z * 8][l];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) add(s, run[z * 8 + i][l]);
+  // eight runs are left, in the first 32 lanes: 4 apart
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    const float4 y = make_float4(__shfl_down(s.x, o), __shfl_down(s.y, o), __shfl_down(s.z, o),
+                                 __shfl_down(s.w, o));
+    add(s, y);
+  }
+  if (z == 0 && c < d) *reinterpret_cast<float4*>(out + c) = s;
 }
 
 template <typename T, typename TY>
@@ -330,23 +420,31 @@ hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-static int norm_rows_at_a_time(int d) { return d <= 512 ? 4 : 1; }
+// Rows of up to 512 columns: a wave each, four to a workgroup.  Parts: as many
+// workgroups as the chip holds at a time (two of 256 threads a CU; 8192 x 2048: 67 us,
+// with twice the parts 75).
+constexpr int kNormParts = 512;
+static int norm_threads(int d) { return d <= 2048 ? 256 : d <= 8192 ? 512 : 1024; }
+static int norm_parts(int L, int d) {
+  const int rows = d <= 512 ? 4 : 1, n = (L + rows - 1) / rows, most = kNormParts * 256 / norm_threads(d);
+  return n < most ? n : most;
+}
 size_t residual_norm_backward_ws_bytes(int bf16, int L, int d) {
-  const int rows = norm_rows_at_a_time(d);
-  return static_cast<size_t>(norm_parts(L, rows)) * rows * 3 * d * 4;
+  return static_cast<size_t>(norm_parts(L, d)) * 3 * d * 4;
 }
 template <typename T, typename TY, typename TX>
 static void run_norm_backward(const ResidualNormBackwardArgs& a, float* sums, hipStream_t s) {
-  const unsigned nb = norm_parts(a.L, norm_rows_at_a_time(a.d));
-  if (a.d <= 512) residual_norm_backward_kernel<T, TY, TX, 64, 8><<<nb, 256, 0, s>>>(a, sums);
+  const unsigned nb = norm_parts(a.L, a.d);
+  if (a.d <= 512)
+    residual_norm_backward_kernel<T, TY, TX, 64, 8, true><<<nb, 256, 0, s>>>(a, sums);
   else if (a.d <= 2048)
-    residual_norm_backward_kernel<T, TY, TX, 256, 8><<<nb, 256, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 256, 8, true><<<nb, 256, 0, s>>>(a, sums);
   else if (a.d <= 4096)
-    residual_norm_backward_kernel<T, TY, TX, 256, 16><<<nb, 256, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 512, 8, true><<<nb, 512, 0, s>>>(a, sums);
   else if (a.d <= 8192)
-    residual_norm_backward_kernel<T, TY, TX, 1024, 8><<<nb, 1024, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 512, 16, false><<<nb, 512, 0, s>>>(a, sums);
   else
-    residual_norm_backward_kernel<T, TY, TX, 1024, 16><<<nb, 1024, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 1024, 16, false><<<nb, 1024, 0, s>>>(a, sums);
 }
 hipError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a, float* ws,
                                          hipStream_t s) {
@@ -361,11 +459,9 @@ hipError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a, floa
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.dw || a.dpost_w || dgate) {
-    const int rows = norm_rows_at_a_time(a.d), parts = norm_parts(a.L, rows) * rows;
-    norm_sums_kernel<<<dim3((a.d + 63) / 64, 3), 256, 0, s>>>(sums, parts, a.d, a.dw, a.dpost_w,
-                                                              dgate);
-  }
+  if (a.dw || a.dpost_w || dgate)
+    norm_sums_kernel<<<dim3((a.d + 15) / 16, 3), 256, 0, s>>>(sums, norm_parts(a.L, a.d), a.d, a.dw,
+                                                              a.dpost_w, dgate);
   return hipGetLastError();
 }
 
