@@ -7,6 +7,7 @@ library is missing the import fails; there is no other execution path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -754,10 +755,30 @@ def quantized_expert_matmul(xq, x_scale, wq, w_scale, offsets, x_row=None, out=N
     return out
 
 
-def _four_bit(t, name):
-    """Rows and elements per row of packed 4-bit rows [R, k / 2]."""
-    rows, half = _matrix(t, name)
-    return rows, 2 * half, (2 * half + 127) // 128 * 4
+# The calls below run at the pace of the host for a single token.  Their arguments are
+# checked in line, all in one condition; what is wrong is looked for only once
+# something is.
+
+_CODES = {torch.float32: OMNI_F32, torch.bfloat16: OMNI_BF16}
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+
+
+def _fits(t, dtype, shape, dev):
+    """An argument as it has to be: type, shape, device, contiguous."""
+    return (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous())
+
+
+def _type_code(dtype):
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _packed_width(k):
+    """Scale bytes of a row of k elements."""
+    return (k + 127) // 128 * 4
 
 
 def microscale_rows(x, q=None, scale=None, stream=None):
@@ -765,16 +786,16 @@ def microscale_rows(x, q=None, scale=None, stream=None):
     [R, 4 ceil(k / 128)] uint8): two e2m1 elements a byte, a power-of-two scale
     2^(byte - 127) for each 32 elements.  Tokens' activations, or weights by output
     channel (view [E, n, k] experts as [E*n, k])."""
-    (R, k), dev, u8 = _matrix(x, "x"), _device_of(x, "x"), torch.uint8
-    G = (k + 127) // 128 * 4
+    (R, k), dev, dt = _matrix(x, "x"), _device_of(x, "x"), x.dtype
+    packed, scales = (R, k // 2), (R, _packed_width(k))
     if q is None:
-        q = _empty((R, k // 2), u8, x, stream)
+        q = _empty(packed, _U8, x, stream)
     if scale is None:
-        scale = _empty((R, G), u8, x, stream)
-    _tensors(dev, (x, "x", x.dtype, (R, k)), (q, "q", u8, (R, k // 2)),
-             (scale, "scale", u8, (R, G)))
+        scale = _empty(scales, _U8, x, stream)
+    if not (x.is_contiguous() and _fits(q, _U8, packed, dev) and _fits(scale, _U8, scales, dev)):
+        _tensors(dev, (x, "x", dt, (R, k)), (q, "q", _U8, packed), (scale, "scale", _U8, scales))
     _sizes_fit(R | k)
-    _call("omni_microscale_rows", dev, stream, _dtype_code(x), R, k, x.data_ptr(), q.data_ptr(),
+    _call("omni_microscale_rows", dev, stream, _type_code(dt), R, k, x.data_ptr(), q.data_ptr(),
           scale.data_ptr())
     return q, scale
 
@@ -784,18 +805,21 @@ def microscaled_matmul(xq, x_scale, wq, w_scale, out=None, out_dtype=torch.bfloa
     """omni_microscaled_matmul: out [M, n] = x w^T for rows xq [M, k / 2] and weights
     wq [n, k / 2] in microscale_rows' form (swiglu: [2n, k / 2], out = silu(gate
     half) * up half)."""
-    (M, k, G), rows, dev = _four_bit(xq, "xq"), _matrix(wq, "wq")[0], _device_of(xq, "xq")
+    (M, half), rows, dev = _matrix(xq, "xq"), _matrix(wq, "wq")[0], _device_of(xq, "xq")
     if swiglu and rows % 2:
         raise ValueError("swiglu needs an even number of weight rows")
-    n = rows // 2 if swiglu else rows
+    n, k = rows // 2 if swiglu else rows, 2 * half
+    G = _packed_width(k)
     if out is None:
         out = _empty((M, n), out_dtype, xq, stream)
-    u8 = torch.uint8
-    _tensors(dev, (xq, "xq", u8, (M, k // 2)), (wq, "wq", u8, (rows, k // 2)),
-             (x_scale, "x_scale", u8, (M, G)), (w_scale, "w_scale", u8, (rows, G)),
-             (out, "out", out.dtype, (M, n)))
+    if not (xq.dtype is _U8 and xq.is_contiguous() and _fits(wq, _U8, (rows, half), dev)
+            and _fits(x_scale, _U8, (M, G), dev) and _fits(w_scale, _U8, (rows, G), dev)
+            and _fits(out, out.dtype, (M, n), dev)):
+        _tensors(dev, (xq, "xq", _U8, (M, half)), (wq, "wq", _U8, (rows, half)),
+                 (x_scale, "x_scale", _U8, (M, G)), (w_scale, "w_scale", _U8, (rows, G)),
+                 (out, "out", out.dtype, (M, n)))
     _sizes_fit(M | n | k)
-    _call("omni_microscaled_matmul", dev, stream, _dtype_code(out), M, n, k, xq.data_ptr(),
+    _call("omni_microscaled_matmul", dev, stream, _type_code(out.dtype), M, n, k, xq.data_ptr(),
           x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), 1 if swiglu else 0,
           out.data_ptr())
     return out
@@ -806,25 +830,26 @@ def microscaled_expert_matmul(xq, x_scale, wq, w_scale, offsets, x_row=None, out
     """omni_microscaled_expert_matmul: expert_matmul over 4-bit rows xq [., k / 2] with
     x_scale and experts wq [E, n, k / 2] with w_scale [E, n, 4 ceil(k / 128)]."""
     E, n, half = _experts(wq, swiglu, "wq")
-    (R, k, G), dev = _four_bit(xq, "xq"), _device_of(xq, "xq")
-    M = _tasks(dev, R, x_row, out_row, "out_row")
+    R, dev, k = _matrix(xq, "xq")[0], _device_of(xq, "xq"), 2 * half
+    G, M = _packed_width(k), _tasks(dev, R, x_row, out_row, "out_row")
     if out is None:
         out = _empty((M, n), out_dtype, xq, stream)
-    u8, Ro = torch.uint8, out.shape[0]
-    _tensors(dev, (xq, "xq", u8, (R, half)), (wq, "wq", u8, wq.shape),
-             (x_scale, "x_scale", u8, (R, G)), (w_scale, "w_scale", u8, (*wq.shape[:2], G)),
-             (offsets, "offsets", torch.int32, (E + 1,)), (out, "out", out.dtype, (Ro, n)))
+    Ro = out.shape[0]
+    _tensors(dev, (xq, "xq", _U8, (R, half)), (wq, "wq", _U8, wq.shape),
+             (x_scale, "x_scale", _U8, (R, G)), (w_scale, "w_scale", _U8, (*wq.shape[:2], G)),
+             (offsets, "offsets", _I32, (E + 1,)), (out, "out", out.dtype, (Ro, n)))
     _sizes_fit(M | E | n | k | R | Ro)
-    _call("omni_microscaled_expert_matmul", dev, stream, _dtype_code(out), M, E, n, k, R, Ro,
+    _call("omni_microscaled_expert_matmul", dev, stream, _type_code(out.dtype), M, E, n, k, R, Ro,
           xq.data_ptr(), x_scale.data_ptr(), _addr(x_row), wq.data_ptr(), w_scale.data_ptr(),
           offsets.data_ptr(), 1 if swiglu else 0, out.data_ptr(), _addr(out_row))
     return out
 
 
 def _scores(scores):
-    if scores not in SCORES:
+    fn = SCORES.get(scores)
+    if fn is None:
         raise ValueError(f"scores must be one of {sorted(SCORES)}, got {scores!r}")
-    return SCORES[scores]
+    return fn
 
 
 def expert_route(logits, K, bias=None, scores="softmax", groups=1, top_groups=None, group_best=2,
@@ -836,25 +861,27 @@ def expert_route(logits, K, bias=None, scores="softmax", groups=1, top_groups=No
     group's value is the sum of its group_best best.  gate = scale * score, over the
     sum of the K if renormalize.  score: where to leave the scores (want_score: a
     fresh array)."""
-    (L, E), dev, f32 = _matrix(logits, "logits"), _device_of(logits, "logits"), torch.float32
-    fn = _scores(scores)
-    if expert_idx is None:
-        expert_idx = _empty((L, K), torch.int32, logits, stream)
-    if gate is None:
-        gate = _empty((L, K), f32, logits, stream)
-    if score is None and want_score:
-        score = _empty((L, E), f32, logits, stream)
-    _tensors(dev, (logits, "logits", logits.dtype, (L, E)),
-             (expert_idx, "expert_idx", torch.int32, (L, K)), (gate, "gate", f32, (L, K)))
-    if bias is not None:
-        _tensors(dev, (bias, "bias", f32, (E,)))
-    if score is not None:
-        _tensors(dev, (score, "score", f32, (L, E)))
+    (L, E), dev, dt, fn = _matrix(logits, "logits"), _device_of(logits, "logits"), \
+        logits.dtype, _scores(scores)
     top = groups if top_groups is None else top_groups
     _sizes_fit(L | E | K | groups | top)
-    _call("omni_expert_route", dev, stream, _dtype_code(logits), L, E, K, logits.data_ptr(),
-          _addr(bias), fn, groups, top, group_best, 1 if renormalize else 0, scale,
-          expert_idx.data_ptr(), gate.data_ptr(), _addr(score))
+    if expert_idx is None:
+        expert_idx = _empty((L, K), _I32, logits, stream)
+    if gate is None:
+        gate = _empty((L, K), _F32, logits, stream)
+    if score is None and want_score:
+        score = _empty((L, E), _F32, logits, stream)
+    if not (logits.is_contiguous() and _fits(expert_idx, _I32, (L, K), dev)
+            and _fits(gate, _F32, (L, K), dev)
+            and (bias is None or _fits(bias, _F32, (E,), dev))
+            and (score is None or _fits(score, _F32, (L, E), dev))):
+        _tensors(dev, (logits, "logits", dt, (L, E)), (expert_idx, "expert_idx", _I32, (L, K)),
+                 (gate, "gate", _F32, (L, K)))
+        _given(dev, (bias, "bias", _F32, (E,)), (score, "score", _F32, (L, E)))
+    _call("omni_expert_route", dev, stream, _type_code(dt), L, E, K, logits.data_ptr(),
+          None if bias is None else bias.data_ptr(), fn, groups, top, group_best,
+          1 if renormalize else 0, scale, expert_idx.data_ptr(), gate.data_ptr(),
+          None if score is None else score.data_ptr())
     return expert_idx, gate, score
 
 
@@ -863,28 +890,33 @@ def expert_route_backward(logits, expert_idx, dgate, scores="softmax", renormali
     """omni_expert_route_backward: dlogits [L, E] of logits' type for dgate [L, K] float32
     and dscore, the gradient of the scores: [L, E] float32, or [E], the same for
     every token."""
-    (L, E), dev, f32 = _matrix(logits, "logits"), _device_of(logits, "logits"), torch.float32
+    (L, E), dev, dt, fn = _matrix(logits, "logits"), _device_of(logits, "logits"), \
+        logits.dtype, _scores(scores)
     K = _matrix(expert_idx, "expert_idx")[1]
-    fn = _scores(scores)
-    if dlogits is None:
-        dlogits = _empty((L, E), logits.dtype, logits, stream)
-    _tensors(dev, (logits, "logits", logits.dtype, (L, E)),
-             (expert_idx, "expert_idx", torch.int32, (L, K)), (dgate, "dgate", f32, (L, K)),
-             (dlogits, "dlogits", logits.dtype, (L, E)))
-    shared = dscore is not None and dscore.dim() == 1
-    if dscore is not None:
-        _tensors(dev, (dscore, "dscore", f32, (E,) if shared else (L, E)))
     _sizes_fit(L | E | K)
-    _call("omni_expert_route_backward", dev, stream, _dtype_code(logits), L, E, K,
-          logits.data_ptr(), expert_idx.data_ptr(), dgate.data_ptr(), fn, 1 if renormalize else 0,
-          scale, _addr(dscore), 1 if shared else 0, dlogits.data_ptr())
+    if dlogits is None:
+        dlogits = _empty((L, E), dt, logits, stream)
+    shared = dscore is not None and dscore.dim() == 1
+    up = (E,) if shared else (L, E)
+    if not (logits.is_contiguous() and _fits(expert_idx, _I32, (L, K), dev)
+            and _fits(dgate, _F32, (L, K), dev) and _fits(dlogits, dt, (L, E), dev)
+            and (dscore is None or _fits(dscore, _F32, up, dev))):
+        _tensors(dev, (logits, "logits", dt, (L, E)), (expert_idx, "expert_idx", _I32, (L, K)),
+                 (dgate, "dgate", _F32, (L, K)), (dlogits, "dlogits", dt, (L, E)))
+        _given(dev, (dscore, "dscore", _F32, up))
+    _call("omni_expert_route_backward", dev, stream, _type_code(dt), L, E, K, logits.data_ptr(),
+          expert_idx.data_ptr(), dgate.data_ptr(), fn, 1 if renormalize else 0, scale,
+          None if dscore is None else dscore.data_ptr(), 1 if shared else 0, dlogits.data_ptr())
     return dlogits
+
+
+def _given(dev, *specs):
+    """_tensors of the arguments that are there."""
+    _tensors(dev, *(s for s in specs if s[0] is not None))
 
 
 def _gate_kind(gate, L, d):
     """omni_gate_kind of a gate [d], [L, 1] or [L, d]."""
-    if gate is None:
-        return GATE_NONE
     if gate.shape == (d,):
         return GATE_COLUMN
     if gate.shape == (L, d):
@@ -901,38 +933,49 @@ def residual_norm(r, y=None, weight=None, post_weight=None, post=False, gate=Non
     type or float32), normed likewise with post_weight, or with post=True and ones.
     gate: [d], [L, 1] or [L, d].  Without y: r_out is r, x its norm.  want_x False:
     the residual alone (x None).  r_out may be r itself."""
-    (L, d), dev, dt = _matrix(r, "r"), _device_of(r, "r"), r.dtype
-    kind, post = _gate_kind(gate, L, d), post or post_weight is not None
+    shape, dev, dt = _matrix(r, "r"), _device_of(r, "r"), r.dtype
+    L, d = shape
+    _sizes_fit(L | d)
+    y_code = code = _type_code(dt)
+    kind = GATE_NONE if gate is None else _gate_kind(gate, L, d)
+    post = post or post_weight is not None
     if y is None:
         if post or gate is not None:
             raise ValueError("post norm and gate need y")
         if r_out is not None and r_out is not r:
             raise ValueError("without y r_out is r")
         r_out = r
-    elif r_out is None:
-        r_out = _empty((L, d), dt, r, stream)
+    else:
+        y_code = _type_code(y.dtype)
+        if r_out is None:
+            r_out = _empty(shape, dt, r, stream)
     if not want_x:
         if x is not None or weight is not None:
             raise ValueError("x is not wanted but it or its weight given")
         if y is None:
             raise ValueError("without y x has to be wanted")
     elif x is None:
-        x = _empty((L, d), dt, r, stream)
-    _tensors(dev, (r, "r", dt, (L, d)), (r_out, "r_out", dt, (L, d)))
-    for t, name, shape in ((x, "x", (L, d)), (weight, "weight", (d,)),
-                           (post_weight, "post_weight", (d,)),
-                           (gate, "gate", None if gate is None else gate.shape)):
-        if t is not None:
-            _tensors(dev, (t, name, dt, shape))
-    y_code = code = _dtype_code(r)
-    if y is not None:
-        y_code = _dtype_code(y)
-        _tensors(dev, (y, "y", y.dtype, (L, d)))
-    _sizes_fit(L | d)
-    _call("omni_residual_norm", dev, stream, code, y_code, L, d, r.data_ptr(), _addr(y),
-          1 if post else 0, _addr(post_weight), _addr(gate), kind, alpha, eps,
-          r_out.data_ptr() if y is not None else None, _addr(weight), _addr(x))
+        x = _empty(shape, dt, r, stream)
+    if not (r.is_contiguous() and _fits(r_out, dt, shape, dev)
+            and (y is None or _fits(y, y.dtype, shape, dev))
+            and (x is None or _fits(x, dt, shape, dev))
+            and (weight is None or _fits(weight, dt, (d,), dev))
+            and (post_weight is None or _fits(post_weight, dt, (d,), dev))
+            and (gate is None or _fits(gate, dt, gate.shape, dev))):
+        _given(dev, (r, "r", dt, shape), (r_out, "r_out", dt, shape),
+               (y, "y", None if y is None else y.dtype, shape), (x, "x", dt, shape),
+               (weight, "weight", dt, (d,)), (post_weight, "post_weight", dt, (d,)),
+               (gate, "gate", dt, None if gate is None else gate.shape))
+    _call("omni_residual_norm", dev, stream, code, y_code, L, d, r.data_ptr(),
+          None if y is None else y.data_ptr(), 1 if post else 0, _addr(post_weight), _addr(gate),
+          kind, alpha, eps, None if y is None else r_out.data_ptr(), _addr(weight), _addr(x))
     return r_out, x
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(code, L, d):
+    """The sizes' workspace in bytes: a number that only they decide."""
+    return lib().omni_residual_norm_backward_workspace(code, L, d)
 
 
 def residual_norm_backward(r_out, dx=None, dr_out=None, y=None, weight=None, post_weight=None,
@@ -944,54 +987,64 @@ def residual_norm_backward(r_out, dx=None, dr_out=None, y=None, weight=None, pos
     r without y.  dx [L, d] (float32 or r_out's type) and dr_out [L, d]: the gradients
     of x and r_out, one of them may be None.  out: dict of arrays to use.  want_sums
     False: no gradient of the weights and the gate."""
-    (L, d), dev, dt = _matrix(r_out, "r_out"), _device_of(r_out, "r_out"), r_out.dtype
-    kind, post = _gate_kind(gate, L, d), post or post_weight is not None
-    f32, code = torch.float32, _dtype_code(r_out)
-    if dx is None and dr_out is None:
-        raise ValueError("one of dx and dr_out is needed")
-    if dx is None and weight is not None:
-        raise ValueError("weight belongs to x: without dx it has no part")
-    if y is None and (post or gate is not None):
+    shape, dev, dt = _matrix(r_out, "r_out"), _device_of(r_out, "r_out"), r_out.dtype
+    L, d = shape
+    _sizes_fit(L | d)
+    y_code = dx_code = code = _type_code(dt)
+    kind = GATE_NONE if gate is None else _gate_kind(gate, L, d)
+    post = post or post_weight is not None
+    if dx is None:
+        if dr_out is None:
+            raise ValueError("one of dx and dr_out is needed")
+        if weight is not None:
+            raise ValueError("weight belongs to x: without dx it has no part")
+    else:
+        dx_code = _type_code(dx.dtype)
+    if y is not None:
+        y_code = _type_code(y.dtype)
+    elif post or gate is not None:
         raise ValueError("post norm and gate need y")
-    given = out or {}
-    res = {}
-
-    def result(name, shape, dtype):
-        t = given.get(name)
-        if t is None:
-            t = _empty(shape, dtype, r_out, stream)
-        _tensors(dev, (t, name, dtype, shape))
-        res[name] = t
-    result("dr", (L, d), dt)
+    # name: type and shape of each result
+    res = {"dr": (dt, shape)}
+    sums = False
     if want_sums:
         if weight is not None:
-            result("dweight", (d,), f32)
+            res["dweight"] = (_F32, (d,))
         if gate is not None:
-            result("dgate", gate.shape, dt if kind == GATE_FULL else f32)
+            res["dgate"] = (dt if kind == GATE_FULL else _F32, gate.shape)
         if post_weight is not None:
-            result("dpost_weight", (d,), f32)
+            res["dpost_weight"] = (_F32, (d,))
+        sums = weight is not None or post_weight is not None or kind == GATE_COLUMN
     if y is not None:
-        result("dy", (L, d), y.dtype)
-    for name in given:
-        if name not in res and given[name] is not None:
-            raise ValueError(f"out has {name!r}, which this call does not give")
-    _tensors(dev, (r_out, "r_out", dt, (L, d)))
-    for t, name, dtype, shape in (
-            (y, "y", None if y is None else y.dtype, (L, d)), (weight, "weight", dt, (d,)),
-            (post_weight, "post_weight", dt, (d,)), (dr_out, "dr_out", dt, (L, d)),
-            (dx, "dx", None if dx is None else dx.dtype, (L, d)),
-            (gate, "gate", dt, None if gate is None else gate.shape)):
-        if t is not None:
-            _tensors(dev, (t, name, dtype, shape))
-    _sizes_fit(L | d)
-    nws = 0
-    if "dweight" in res or "dpost_weight" in res or ("dgate" in res and kind == GATE_COLUMN):
-        nws = lib().omni_residual_norm_backward_workspace(code, L, d)
-    ws = _workspace(workspace, nws, r_out, stream)
-    _call("omni_residual_norm_backward", dev, stream, code,
-          code if y is None else _dtype_code(y), code if dx is None else _dtype_code(dx), L, d,
+        res["dy"] = (y.dtype, shape)
+    if out:
+        for name, t in out.items():
+            if t is not None and name not in res:
+                raise ValueError(f"out has {name!r}, which this call does not give")
+    for name, (dtype, size) in res.items():
+        t = out.get(name) if out else None
+        if t is None:
+            t = _empty(size, dtype, r_out, stream)
+        elif not _fits(t, dtype, size, dev):
+            _tensors(dev, (t, name, dtype, size))
+        res[name] = t
+    if not (r_out.is_contiguous() and (dx is None or _fits(dx, dx.dtype, shape, dev))
+            and (dr_out is None or _fits(dr_out, dt, shape, dev))
+            and (y is None or _fits(y, y.dtype, shape, dev))
+            and (weight is None or _fits(weight, dt, (d,), dev))
+            and (post_weight is None or _fits(post_weight, dt, (d,), dev))
+            and (gate is None or _fits(gate, dt, gate.shape, dev))):
+        _given(dev, (r_out, "r_out", dt, shape),
+               (y, "y", None if y is None else y.dtype, shape), (weight, "weight", dt, (d,)),
+               (post_weight, "post_weight", dt, (d,)), (dr_out, "dr_out", dt, shape),
+               (dx, "dx", None if dx is None else dx.dtype, shape),
+               (gate, "gate", dt, None if gate is None else gate.shape))
+    nws = _norm_workspace(code, L, d) if sums else 0
+    ws = _workspace(workspace, nws, r_out, stream) if nws else None
+    get = res.get
+    _call("omni_residual_norm_backward", dev, stream, code, y_code, dx_code, L, d,
           r_out.data_ptr(), _addr(y), 1 if post else 0, _addr(post_weight), _addr(gate), kind,
           alpha, eps, _addr(weight), _addr(dr_out), _addr(dx), res["dr"].data_ptr(),
-          _addr(res.get("dy")), _addr(res.get("dgate")), _addr(res.get("dweight")),
-          _addr(res.get("dpost_weight")), _addr(ws) if nws else None, nws)
+          _addr(get("dy")), _addr(get("dgate")), _addr(get("dweight")),
+          _addr(get("dpost_weight")), _addr(ws), nws)
     return res
