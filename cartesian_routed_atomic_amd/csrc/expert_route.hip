@@ -2,17 +2,20 @@
 //
 // What selects is the score plus the balance bias, c = s + b.  The c of different
 // experts can lie within float32's rounding of each other, so their order is that
-// of float64.  Nearly always float32 tells it: c is computed in float32, whose error
-// is below 2^-20 of the row's largest score and 2^-23 of c (below), and where any
-// two that had to be told apart are closer than four times that, the wave decides
-// them again in float64 (16384 tokens, 256 experts, 8 of them, sigmoid: about one
-// wave in 40; with float64 throughout 43.9 us).  Without a bias the score grows
-// with the logit, which is compared as it stands.
+// of float64.  Nearly always float32 tells it; where any two that had to be told
+// apart are closer than twice its error, those are decided in float64 (16384 tokens,
+// 256 experts, 8 of them, sigmoid, groups: 15.9 us, with float64 throughout 43.9).
+// Without a bias the score grows with the logit, which is compared as it stands.
 //
-// Error of a score: v_exp_f32 and the reciprocal are good to one unit in the last
-// place, the product with log2 e rounds at 2^-24 of the exponent x, which is
-// x 2^-24 of e^-x: at most 0.54 x 2^-24 of the largest score; the sum of up to 1024
-// positive terms in at most 22 steps adds 22 x 2^-24 of the score.
+// The error of c, in units of 2^-24.  e^x: the exponent's product with log2 e is off
+// by 1.5 |x|, the exponential and a reciprocal by 2 each, relative; times e^-|x|, at
+// most 2.1 of the largest term.  Sigmoid: s (1 - s) (1.5 |z| + 2) + 3 s < 3.7.
+// Softmax: 2.1 and the sum's, which all of a row's scores share, 22 (at most 16 + 6
+// additions) and 2, of the largest score.  c's own rounding adds 1 of c.  Twice that
+// is below 2^-20 and below 2^-18 of the largest score, plus 2^-22 of c.
+//
+// Bound by instructions: a token's 256 logits and scores are 2 KiB, 6.6 us of HBM for
+// 16384 tokens; the rounds of the selection are about 55 instructions each.
 #include "device.hpp"
 #include "launch.hpp"
 
@@ -200,42 +203,57 @@ __device__ __forceinline__ int take_best(uint64_t (&key)[V], int K) {
   return mine;
 }
 
-// Which groups stay, a bit each in the result: lane g sums group g's best.  c: the
-// token's E values in LDS.  far(a, b): the last that stays and the first that does
-// not are told apart.
-template <int T, typename F, class Far>
+// Lanes that share a group (a power of two): as many as the token's lanes hold.
+template <int T>
+__device__ __forceinline__ int group_shift(int groups) {
+  return 31 - __builtin_clz(static_cast<unsigned>(T / groups));
+}
+// Which groups stay, bit g << shift in the result for group g.  c: the token's E values
+// in LDS, none of them NaN.  apart(a, b, size): values of the last that stays and the
+// first that does not, and the sum of the absolute terms of both.
+template <int T, typename F, class Apart>
 __device__ __forceinline__ uint64_t best_groups(const F* c, const ExpertRouteArgs& a, int l,
-                                                Far far) {
-  const int size = a.E / a.groups;
+                                                int shift, Apart apart) {
+  const int size = a.E / a.groups, g = l >> shift, share = 1 << shift, part = l & (share - 1);
   F b1 = -INFINITY, b2 = -INFINITY;
-  if (l < a.groups) {
-    // started l further on: the lanes then read different banks
-    int i = l % size;
-    for (int n = 0; n < size; ++n) {
-      F m = c[l * size + i];
-      m = m == m ? m : -INFINITY;
-      b2 = b2 > m ? b2 : (b1 < m ? b1 : m);
-      b1 = b1 > m ? b1 : m;
-      i = i + 1 == size ? 0 : i + 1;
+  const int steps = (size + share - 1) >> shift;
+  // started g steps further on: the groups' lanes then read different banks
+  int n = g < steps ? g : g % steps;
+  if (g < a.groups) {
+#pragma unroll 4
+    for (int i = 0; i < steps; ++i) {
+      const int at = part + (n << shift);
+      const F m = at < size ? c[g * size + at] : -INFINITY;
+      b2 = max(b2, min(b1, m));
+      b1 = max(b1, m);
+      n = n + 1 == steps ? 0 : n + 1;
     }
   }
-  const F value = a.group_best == 2 && size > 1 ? b1 + b2 : b1;
-  using Key = decltype(order_key(value));
-  const Key key = l < a.groups ? order_key(value) : 0;
-  int ahead = 0;
-  for (int g = 0; g < a.groups; ++g) {
-    const Key other = __shfl(key, g, T);
-    ahead += other > key || (other == key && g < l) ? 1 : 0;
+  for (int o = 1; o < share; o <<= 1) {
+    const F m = __shfl_xor(b1, o, T), n2 = __shfl_xor(b2, o, T);
+    b2 = max(min(b1, m), max(b2, n2));
+    b1 = max(b1, m);
   }
-  const F last = __shfl(value, __ffsll(static_cast<long long>(
-                                   __ballot(ahead == a.top_groups - 1 && l < a.groups) >>
-                                   (T == kWave ? 0 : lane() & ~(T - 1)))) - 1, T);
-  const F first = __shfl(value, __ffsll(static_cast<long long>(
-                                    __ballot(ahead == a.top_groups && l < a.groups) >>
-                                    (T == kWave ? 0 : lane() & ~(T - 1)))) - 1, T);
-  far(last, first);
-  const uint64_t stay = __ballot(l < a.groups && ahead < a.top_groups);
-  return T == kWave ? stay : stay >> (lane() & ~(T - 1)) & ((1ull << T) - 1);
+  F value = a.group_best == 2 && size > 1 ? b1 + b2 : b1;
+  if (!(value == value)) value = -INFINITY;  // infinities of both signs
+  using Key = decltype(order_key(value));
+  const bool mine = g < a.groups && part == 0;
+  const Key key = order_key(value);
+  int ahead = 0;
+  for (int j = 0; j < a.groups; ++j) {
+    const Key other = __shfl(key, j << shift, T);
+    ahead += other > key || (other == key && j < g) ? 1 : 0;
+  }
+  const int low = T == kWave ? 0 : lane() & ~(T - 1);  // the token's first lane
+  auto lane_of = [&](int rank) {
+    return __ffsll(static_cast<long long>(__ballot(mine && ahead == rank) >> low)) - 1;
+  };
+  const int last = lane_of(a.top_groups - 1), first = lane_of(a.top_groups);
+  const F terms = a.group_best == 2 && size > 1 ? fabs(b1) + fabs(b2) : fabs(b1);
+  apart(__shfl(value, last, T), __shfl(value, first, T),
+        __shfl(terms, last, T) + __shfl(terms, first, T));
+  const uint64_t stay = __ballot(mine && ahead < a.top_groups);
+  return T == kWave ? stay : stay >> low & ((1ull << (T & 63)) - 1);
 }
 
 // One token decided in float64 by its whole wave; lane k gets the k-th expert.  slots:
@@ -278,12 +296,16 @@ __device__ __forceinline__ int decide_exactly(const ExpertRouteArgs& a, size_t t
     }
   }
   uint64_t stay = ~0ull;
+  int shift = 0;
   if constexpr (GROUPS) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * 64 + l < E) slots[v * 64 + l] = sums ? d[v] : z[v];
+    for (int v = 0; v < V; ++v) {
+      const double m = sums ? d[v] : z[v];
+      if (v * 64 + l < E) slots[v * 64 + l] = m == m ? m : -INFINITY;
+    }
     wave_lds_fence();
-    stay = best_groups<kWave>(slots, a, l, [](double, double) {});
+    shift = group_shift<kWave>(a.groups);
+    stay = best_groups<kWave>(slots, a, l, shift, [](double, double, double) {});
     wave_lds_fence();
   }
   const float per = GROUPS ? static_cast<float>(a.groups) / E : 0.f;
@@ -291,10 +313,72 @@ __device__ __forceinline__ int decide_exactly(const ExpertRouteArgs& a, size_t t
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = v * 64 + l;
-    const bool in = e < E && (!GROUPS || (stay >> static_cast<int>((e + 0.5f) * per) & 1) != 0);
+    const bool in = e < E && (!GROUPS || (stay >> (static_cast<int>((e + 0.5f) * per) << shift) & 1) != 0);
     key[v] = in ? order_key(a.bias ? d[v] : static_cast<double>(z[v])) : 0ull;
   }
   return take_best<V>(key, a.K);
+}
+
+// Sigmoid scores with a bias whose order float32 leaves open: the slots that may be
+// among the K best, those within what c is off of the K-th distinct c, go to a lane
+// each, which forms c in float64 and counts those ahead of it.  open: of this token
+// (the wave's others go along).  False where there are more than T of them.
+template <typename L, int T, int V>
+__device__ __forceinline__ bool rank_near(const ExpertRouteArgs& a, const L* row,
+                                          const float (&c)[V], const uint32_t (&key)[V],
+                                          float last, float close, bool open, int* ids, int l) {
+  const float floor = last - (close + 0x1p-22f * fabsf(last));
+  int count = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) count += key[v] != 0 && c[v] >= floor ? 1 : 0;
+  // exclusive prefix over the token's lanes
+  uint32_t upto = count;
+  upto += dpp_u<0x111, 0xf>(0u, upto);  // row_shr 1, 2, 4, 8
+  upto += dpp_u<0x112, 0xf>(0u, upto);
+  upto += dpp_u<0x114, 0xf>(0u, upto);
+  upto += dpp_u<0x118, 0xf>(0u, upto);
+  if constexpr (T == kWave) {
+    upto += dpp_u<0x142, 0xa>(0u, upto);
+    upto += dpp_u<0x143, 0xc>(0u, upto);
+  }
+  const int n = __shfl(static_cast<int>(upto), T - 1, T);
+  const bool fits = n >= a.K && n <= T;
+  int at = static_cast<int>(upto) - count;
+  wave_lds_fence();
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (key[v] != 0 && c[v] >= floor) {
+      if (open && fits) ids[at] = 4 * T * (v / 4) + 4 * l + v % 4;
+      ++at;
+    }
+  wave_lds_fence();
+  const bool in = open && fits && l < n;
+  const int e = in ? ids[l] : 1 << 20;
+  double exact = 0.0;
+  if (in)
+    exact = 1.0 / (1.0 + exp(-static_cast<double>(load_logit(row, e)))) + a.bias[e];
+  const uint64_t mine = in ? order_key(exact) : 0ull;
+  int ahead = 0;
+  if constexpr (T == kRow) {
+    uint32_t hi = static_cast<uint32_t>(mine >> 32), lo = static_cast<uint32_t>(mine), id = e;
+#pragma unroll
+    for (int r = 1; r < T; ++r) {
+      hi = dpp_row<0x121>(hi);
+      lo = dpp_row<0x121>(lo);
+      id = dpp_row<0x121>(id);
+      const uint64_t other = static_cast<uint64_t>(hi) << 32 | lo;
+      ahead += other > mine || (other == mine && static_cast<int>(id) < e) ? 1 : 0;
+    }
+  } else {
+    for (int j = 0; j < T; ++j) {
+      const uint64_t other = __shfl(mine, j);
+      const int id = __shfl(e, j);
+      ahead += other > mine || (other == mine && id < e) ? 1 : 0;
+    }
+  }
+  if (in && ahead < a.K) ids[ahead] = e;
+  wave_lds_fence();
+  return fits;
 }
 
 // T lanes per token, V slots each.
@@ -361,17 +445,21 @@ __global__ __launch_bounds__(256) void expert_route_kernel(ExpertRouteArgs a) {
       for (int i = 0; i < 4; ++i) c[v + i] = s[v + i] + b[i];
     }
   }
-  const float close = largest * 0x1p-18f;
+  const float close = largest * (a.sigmoid ? 0x1p-20f : 0x1p-18f);
   bool unsure = false;
   uint64_t stay = ~0ull;
+  int shift = 0;
   if constexpr (GROUPS) {
+    shift = group_shift<T>(a.groups);
     float* mine = reinterpret_cast<float*>(room[wv]) + sub * ROOM;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (expert(v) < E) mine[expert(v)] = sums && !biased ? s[v] : c[v];
+    for (int v = 0; v < V; ++v) {
+      const float m = sums && !biased ? s[v] : c[v];
+      if (expert(v) < E) mine[expert(v)] = m == m ? m : -INFINITY;
+    }
     wave_lds_fence();
-    stay = best_groups<T>(mine, a, l, [&](float x, float y) {
-      if (sums) unsure |= !(x - y > 2 * close + 0x1p-19f * fabsf(x));
+    stay = best_groups<T>(mine, a, l, shift, [&](float x, float y, float terms) {
+      if (sums) unsure |= !(x - y > 2 * close + 0x1p-22f * terms);
     });
   }
   // e / size of whole numbers up to 1024: the quotient of e + 1/2 is 1/1024 or more
@@ -381,13 +469,14 @@ __global__ __launch_bounds__(256) void expert_route_kernel(ExpertRouteArgs a) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = expert(v);
-    const bool in = e < E && (!GROUPS || (stay >> static_cast<int>((e + 0.5f) * per) & 1) != 0);
+    const bool in = e < E && (!GROUPS || (stay >> (static_cast<int>((e + 0.5f) * per) << shift) & 1) != 0);
     key[v] = in ? order_key(c[v]) : 0u;
   }
   uint32_t before = ~0u;
+  bool near = false;  // the best are the best, but their order or the last is in doubt
   auto apart = [&](uint32_t best) {  // from the round before's; not where one is no number
     const float x = fkey_inv(before), y = fkey_inv(best);
-    unsure |= !(x - y > close + 0x1p-20f * fabsf(x));
+    near |= !(x - y > close + 0x1p-22f * fabsf(x));
   };
   strike_best<T, V>(key, a.K, [&](int k, uint32_t best) {
     unsure |= best <= static_cast<uint32_t>(a.K);  // equal keys left none for this round
@@ -412,7 +501,16 @@ __global__ __launch_bounds__(256) void expert_route_kernel(ExpertRouteArgs a) {
   }
   // equal keys shared a round: more slots than rounds.  Otherwise each of K rounds
   // struck one slot, and the list is whole.
-  unsure |= lanes_sum<T>(static_cast<float>(count)) != static_cast<float>(a.K);
+  const bool shared = lanes_sum<T>(static_cast<float>(count)) != static_cast<float>(a.K);
+  const bool doubt = shared || near;
+  if (!biased || !a.sigmoid) {
+    unsure |= doubt;
+  } else {
+    const float last = fkey_inv(before);
+    unsure |= !(last > -INFINITY);  // what is not a number ranks there too
+    if (__any(doubt && !unsure))
+      unsure |= doubt && !rank_near<L, T, V>(a, row, c, key, last, close, doubt && !unsure, ids, l);
+  }
   uint64_t open = __ballot(unsure && live);
   wave_lds_fence();
   while (open != 0) {

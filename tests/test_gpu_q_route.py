@@ -109,6 +109,33 @@ def test_route_scores_next_to_each_other(E):
         check(z, 8, bias=bias, fn=fn, groups=4, top_groups=2, group_best=2)
 
 
+@pytest.mark.parametrize("E,K,groups,pairs", [
+    (40, 4, 1, 3), (64, 8, 4, 6), (128, 16, 1, 10), (256, 8, 8, 8), (256, 8, 1, 120),
+    (250, 33, 1, 20), (512, 16, 8, 12), (1000, 60, 4, 40)])
+@pytest.mark.parametrize("fn", ["softmax", "sigmoid"])
+def test_route_pairs_next_to_each_other(E, K, groups, pairs, fn):
+    """A few pairs of experts whose biased scores differ by less than float32 tells,
+    among the best and about the K-th, in rows that are otherwise well apart."""
+    rng = np.random.default_rng(E + K)
+    row = logits(rng, 1, E, "f32")[0]
+    s = OB.scores(row[None], fn)[0]
+    bias = (0.3 * rng.standard_normal(E)).astype(np.float32)
+    order = np.argsort(-(s + bias))
+    for i in range(pairs):
+        a, b = order[2 * i], order[2 * i + 1]
+        # the neighbour's bias, a few of its last places to either side
+        bias[b] = np.float32(s[a] + np.float64(bias[a]) - s[b])
+        for _ in range(rng.integers(0, 3)):
+            bias[b] = np.nextafter(bias[b], np.float32(rng.choice([-9, 9])))
+    z = np.repeat(row[None], 21, 0)
+    z[7:] += np.float32(2.0 ** -9) * rng.standard_normal((14, E)).astype(np.float32)
+    z[14:] = logits(rng, 7, E, "f32")
+    top = max(1, groups // 2)
+    for best in (1, 2):
+        check(z, K, bias=bias, fn=fn, groups=groups, top_groups=top, group_best=best)
+    check(z, K, bias=bias + np.float32(100.0), fn=fn, groups=groups, top_groups=top)
+
+
 @pytest.mark.parametrize("fn", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 @pytest.mark.parametrize("E,groups", [(24, 1), (64, 4), (256, 8), (520, 8)])
