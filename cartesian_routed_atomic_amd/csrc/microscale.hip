@@ -13,71 +13,124 @@ __host__ __device__ inline int mx_scale_bytes(int k) { return (k + 127) / 128 * 
 
 // ------------------------------------------------------------------ rows made 4-bit
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x;
-  v[1] = a.y;
-  v[2] = a.z;
-  v[3] = a.w;
-  v[4] = b.x;
-  v[5] = b.y;
-  v[6] = b.z;
-  v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  v[0] = bf_lo(u.x);
-  v[1] = bf_hi(u.x);
-  v[2] = bf_lo(u.y);
-  v[3] = bf_hi(u.y);
-  v[4] = bf_lo(u.z);
-  v[5] = bf_hi(u.z);
-  v[6] = bf_lo(u.w);
-  v[7] = bf_hi(u.w);
-}
+// Sixteen consecutive elements of a lane.
+struct F32Sixteen {
+  float v[16];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p + i);
+      v[i] = f.x;
+      v[i + 1] = f.y;
+      v[i + 2] = f.z;
+      v[i + 3] = f.w;
+    }
+  }
+  // the largest magnitude, as bits: NaN above infinity above numbers
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t = max(t, __float_as_uint(v[i]) & 0x7fffffffu);
+    return t;
+  }
+  template <int I>
+  __device__ __forceinline__ uint32_t four(float unit) const {  // elements 8 I .. 8 I + 7
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[8 * I], v[8 * I + 1], unit, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[8 * I + 2], v[8 * I + 3], unit, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[8 * I + 4], v[8 * I + 5], unit, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[8 * I + 6], v[8 * I + 7], unit, 3);
+  }
+  __device__ __forceinline__ void lift() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= 0x1p64f;
+  }
+};
+// In pairs as they lie in memory: the maximum and the conversion take them so.
+struct Bf16Sixteen {
+  typedef unsigned short Pair __attribute__((ext_vector_type(2)));
+  typedef __bf16 Bf16Pair __attribute__((ext_vector_type(2)));
+  uint32_t v[8];
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 8);
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = a.z;
+    v[3] = a.w;
+    v[4] = b.x;
+    v[5] = b.y;
+    v[6] = b.z;
+    v[7] = b.w;
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    Pair t = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      t = __builtin_elementwise_max(t, __builtin_bit_cast(Pair, v[i] & 0x7fff7fffu));
+    return static_cast<uint32_t>(max(t[0], t[1])) << 16;
+  }
+  template <int I>
+  __device__ __forceinline__ uint32_t four(float unit) const {
+    auto pair = [&](int i) { return __builtin_bit_cast(Bf16Pair, v[4 * I + i]); };
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(0), unit, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(1), unit, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(2), unit, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(3), unit, 3);
+  }
+  __device__ __forceinline__ void lift() {  // bfloat16 has float32's exponents: exact
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float lo = bf_lo(v[i]) * 0x1p64f, hi = bf_hi(v[i]) * 0x1p64f;
+      v[i] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
+    }
+  }
+};
 
-// Sixteen lanes take 128 elements of a row, eight each; four lanes share a block.
-template <typename T>
+// Eight lanes take 128 elements of a row, sixteen each; two lanes share a block.  The
+// conversion instruction rounds to nearest even and saturates, with a float32 scale
+// that has to be a normal number: blocks whose scale is 2^-127 are lifted by 2^64
+// (exact).  HBM-bound: 65536 x 2048 from bfloat16 in 58 us, 5.8 TB/s, 8192 x 2048 in
+// 7.9; eight elements a lane, converted from float32, took 13.3.
+template <typename T, typename Sixteen>
 __global__ __launch_bounds__(256) void microscale_kernel(const T* x, uint8_t* q, uint8_t* scale,
                                                          int R, int k) {
-  const int groups = (k + 127) / 128, l = threadIdx.x & 15;
-  const size_t item = static_cast<size_t>(blockIdx.x) * 16 + threadIdx.x / 16;
-  if (item >= static_cast<size_t>(R) * groups) return;
-  const size_t row = item / groups;
-  const int c = static_cast<int>(item - row * groups) * 128 + l * 8;
-  const bool in = c < k;
-  float v[8] = {};
-  if (in) load8(x + row * k + c, v);
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-  top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 1)));
-  top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 2)));
+  const uint32_t groups = (k + 127) / 128, l = threadIdx.x & 7;
+  const uint32_t item = blockIdx.x * 32 + threadIdx.x / 8;  // below 2^28
+  if (item >= static_cast<uint32_t>(R) * groups) return;
+  const uint32_t row = item / groups, c = (item - row * groups) * 128 + l * 16;
+  const bool in = c < static_cast<uint32_t>(k);
+  Sixteen v = {};
+  if (in) v.load(x + static_cast<size_t>(row) * k + c);
+  uint32_t top = v.top();
+  top = max(top, dpp_u<0xb1, 0xf>(0u, top));  // the neighbour: quad_perm 1 0 3 2
   const uint32_t ex = top >> 23;
   const uint32_t b = !in ? 127u : ex == 255u ? 255u : ex > 2u ? ex - 2u : 0u;
-  // 2^-127 is no normal number: such blocks are lifted by 2^64 (exact)
-  const float lift = b == 0u ? 0x1p64f : 1.f;
-  const float unit = __uint_as_float((b == 0u ? 64u : b) << 23);
-  uint32_t w = 0;
-  if (b != 255u) {
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0] * lift, v[1] * lift, unit, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2] * lift, v[3] * lift, unit, 1);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4] * lift, v[5] * lift, unit, 2);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6] * lift, v[7] * lift, unit, 3);
+  const bool tiny = b == 0u;
+  if (__any(tiny)) {
+    if (tiny) v.lift();
   }
-  uint32_t all = b << (l / 4 * 8);
-  all |= static_cast<uint32_t>(__shfl_xor(static_cast<int>(all), 4));
-  all |= static_cast<uint32_t>(__shfl_xor(static_cast<int>(all), 8));
-  if (in) *reinterpret_cast<uint32_t*>(q + row * (k / 2) + c / 2) = w;
-  if (l == 0) *reinterpret_cast<uint32_t*>(scale + item * 4) = all;
+  const float unit = __uint_as_float((tiny ? 64u : b) << 23);
+  uint2 w = make_uint2(v.template four<0>(unit), v.template four<1>(unit));
+  if (b == 255u) w = make_uint2(0u, 0u);
+  // the four blocks' bytes, from lanes 0, 2, 4, 6
+  uint32_t all = b << (l / 2 * 8);
+  all |= dpp_u<0x4e, 0xf>(0u, all);   // quad_perm 2 3 0 1
+  all |= dpp_u<0x141, 0xf>(0u, all);  // row_half_mirror
+  if (in) *reinterpret_cast<uint2*>(q + static_cast<size_t>(row) * (k / 2) + c / 2) = w;
+  if (l == 0) *reinterpret_cast<uint32_t*>(scale + static_cast<size_t>(item) * 4) = all;
 }
 
 hipError_t launch_microscale_rows(int bf16, int R, int k, const void* x, uint8_t* q,
                                   uint8_t* scale, hipStream_t s) {
   const size_t items = static_cast<size_t>(R) * ((k + 127) / 128);
-  const unsigned nb = static_cast<unsigned>((items + 15) / 16);
-  if (bf16) microscale_kernel<<<nb, 256, 0, s>>>(static_cast<const uint16_t*>(x), q, scale, R, k);
-  else microscale_kernel<<<nb, 256, 0, s>>>(static_cast<const float*>(x), q, scale, R, k);
+  const unsigned nb = static_cast<unsigned>((items + 31) / 32);
+  if (bf16)
+    microscale_kernel<uint16_t, Bf16Sixteen>
+        <<<nb, 256, 0, s>>>(static_cast<const uint16_t*>(x), q, scale, R, k);
+  else
+    microscale_kernel<float, F32Sixteen>
+        <<<nb, 256, 0, s>>>(static_cast<const float*>(x), q, scale, R, k);
   return hipGetLastError();
 }
 
@@ -317,22 +370,29 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(ExpertMatmulAr
       if ((u * NW + wv) * 64 < BM + BN)
         load_lds16(ssrc[u] + first_scale(j), scales + slot * SCALES + (u * NW + wv) * 1024);
   };
-  // Load u of stage kt into the slot of the stream's q-th.  Past the end of a row the
-  // tasks' data are zeros; the weights', which are finite whatever their bits, are
-  // those of the row's start.
+  // load u of stage kt into the slot of the stream's q-th
   auto issue = [&](int kt, int q, int u) {
-    const uint32_t st = ring + (q % S) * STAGE;
+    const uint32_t st = ring + (q % S) * STAGE, at = static_cast<uint32_t>(kt) * 128;
     if (u < IP) {
-      const int first = (wv * IP + u) * 8;
-      const void* src = psrc[u] + static_cast<size_t>(kt) * 128;
-      if (kt == cut && ((l & 7) ^ mx_swz(first + (l >> 3))) >= left) src = kZeroChunk;
-      load_lds16(src, st + first * 128);
+      load_lds16(psrc[u] + at, st + (wv * IP + u) * 1024);
     } else {
       u -= IP;
-      const int first = (wv * IQ + u) * 8, c = (l & 7) ^ mx_swz(first + (l >> 3));
-      uint32_t off = qoff[u] + kt * 128;
-      if (kt == cut && c >= left) off = qoff[u] - c * 16;
-      load_lds16(qbase, off, st + (BM + first) * 128);
+      load_lds16(qbase, qoff[u] + at, st + BM * 128 + (wv * IQ + u) * 1024);
+    }
+  };
+  // Before the stage that is not whole: past the end of a row the tasks' data are
+  // zeros; the weights', which are finite whatever their bits, are the row's start.
+  auto end_rows = [&] {
+    int ll = l;
+    __asm__ volatile("" : "+v"(ll));  // opaque, as above
+#pragma unroll
+    for (int u = 0; u < IP; ++u)
+      if (((ll & 7) ^ mx_swz((wv * IP + u) * 8 + (ll >> 3))) >= left)
+        psrc[u] = reinterpret_cast<const uint8_t*>(kZeroChunk) - static_cast<size_t>(cut) * 128;
+#pragma unroll
+    for (int u = 0; u < IQ; ++u) {
+      const int c = (ll & 7) ^ mx_swz((wv * IQ + u) * 8 + (ll >> 3));
+      if (c >= left) qoff[u] -= static_cast<uint32_t>(cut) * 128 + c * 16;
     }
   };
 
@@ -394,32 +454,71 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(ExpertMatmulAr
     for (int j = 0; j < TJ; ++j) __asm__ volatile("" : "+v"(acc[i][j])::"memory");
     __builtin_amdgcn_sched_barrier(0);
   };
+  // Lane (i32, h) holds row 32 i + i32, columns 32 j + 16 h + 0..15.  Two rows sixteen
+  // apart change halves, so that four lanes store a row's 32 columns side by side: with
+  // 16 bytes of every row at a time 8192 x 5632 x 2048 took 70.4 us for 67.8, and in
+  // tiles of 128 x 128 8192 x 8192 x 8192 416 for 370.
   auto store = [&](const TilePlace& p) {
-    // lane (i32, h) holds row 32 i + i32, columns 32 j + 16 h + 0..15
     TO* out = static_cast<TO*>(a.out);
     const bool aligned = (N * sizeof(TO)) % 16 == 0;
+    constexpr int W = 16 * sizeof(TO) / 4;  // 32-bit words of a lane's columns
+    const int lo = l & 15, quarter = l >> 4;
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
-      const int m = p.t.m0 + wm * (BM / WM) + i * 32 + i32;
-      if (m >= p.t.m1) continue;
-      const int row = a.out_row ? a.out_row[m] : m, xr = a.x_row ? a.x_row[m] : m;
-      if (row < 0 || row >= a.Ro) continue;
-      const bool in = xr >= 0 && xr < a.R;  // a row out of range gives zeros
-      TO* dst = out + static_cast<size_t>(row) * N;
+      const int m = p.t.m0 + wm * (BM / WM) + i * 32;
+      int row[2];  // where the lane stores: rows lo and 16 + lo
 #pragma unroll
-      for (int j = 0; j < TJ; j += SWIGLU ? 2 : 1)
+      for (int e = 0; e < 2; ++e) {
+        const int at = m + 16 * e + lo;
+        row[e] = at >= p.t.m1 ? -1 : a.out_row ? a.out_row[at] : at;
+        if (row[e] >= a.Ro) row[e] = -1;
+      }
+      bool in = true;  // a row out of range gives zeros
+      if (a.x_row) {
+        const int xr = a.x_row[min(m + i32, p.t.m1 - 1)];
+        in = xr >= 0 && xr < a.R;
+      }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float o[8];
+      for (int j = 0; j < TJ; j += SWIGLU ? 2 : 1) {
+        uint32_t w[W];
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int e = half * 8 + c;
-            if constexpr (SWIGLU) o[c] = in ? silu_mul(acc[i][j][e], acc[i][j + 1][e]) : 0.f;
-            else o[c] = in ? acc[i][j][e] : 0.f;
-          }
-          store_cols(dst, p.nt * BNO + wn * (BNO / WN) + (SWIGLU ? j / 2 : j) * 32 + h * 16 + half * 8,
-                     N, aligned, o);
+        for (int c = 0; c < 16; c += 4 / static_cast<int>(sizeof(TO))) {
+          auto value = [&](int e) {
+            if constexpr (SWIGLU) return in ? silu_mul(acc[i][j][e], acc[i][j + 1][e]) : 0.f;
+            else return in ? acc[i][j][e] : 0.f;
+          };
+          if constexpr (sizeof(TO) == 2) w[c / 2] = bf16_pair(value(c), value(c + 1));
+          else w[c] = __float_as_uint(value(c));
         }
+        // pieces of 16 bytes: 0, 1, .. of a lane's own row; odd ones change places
+#pragma unroll
+        for (int b = 0; b < W; b += 8)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const auto both = __builtin_amdgcn_permlane16_swap(w[b + c], w[b + 4 + c], false, false);
+            w[b + c] = both[0];
+            w[b + 4 + c] = both[1];
+          }
+        const int c0 = p.nt * BNO + wn * (BNO / WN) + (SWIGLU ? j / 2 : j) * 32 +
+                       (quarter >> 1) * 16 + (quarter & 1) * (16 / static_cast<int>(sizeof(TO)));
+#pragma unroll
+        for (int b = 0; b < W; b += 4) {
+          const int to = row[(b >> 2) & 1], c = c0 + (b >> 3) * 8;
+          if (to < 0) continue;
+          TO* dst = out + static_cast<size_t>(to) * N;
+          constexpr int N4 = 16 / sizeof(TO);
+          if (aligned && c + N4 <= N) {
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[b], w[b + 1], w[b + 2], w[b + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < N4; ++e) {
+              if (c + e >= N) continue;
+              if constexpr (sizeof(TO) == 2) dst[c + e] = static_cast<TO>(w[b + e / 2] >> (16 * (e & 1)));
+              else dst[c + e] = __uint_as_float(w[b + e]);
+            }
+          }
+        }
+      }
     }
   };
 
@@ -443,6 +542,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(ExpertMatmulAr
 #pragma unroll
   for (int s = 0; s < S; ++s)
     if (s < nk) {
+      if (s == cut) end_rows();
 #pragma unroll
       for (int u = 0; u < I; ++u) issue(s, s, u);
     }
@@ -499,6 +599,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(ExpertMatmulAr
         sources(then, [&](int r) {
           return a.x_row ? rows[r] : min(then.t.m0 + r, then.t.m1 - 1);
         });
+      if (in == cut && (own || more)) end_rows();
       if (in % 2 == 0 && (own || more)) issue_scales(in / 2, ((own ? slot0 : slot1) + in / 2) % S);
       read_scales(next, end ? 0 : kt + 1, 0, end ? slot1 : (slot0 + (kt + 1) / 2) % S);
 #pragma unroll
