@@ -62,7 +62,14 @@ __device__ __forceinline__ float load_one(const uint16_t* p) {
 template <int NT, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[16]) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  for (int i = 0; i < N; ++i) {
+    if constexpr (NT >= kWave) {
+      v[i] = wave_sum(v[i]);
+    } else {
+#pragma unroll
+      for (int o = NT / 2; o > 0; o >>= 1) v[i] += __shfl_xor(v[i], o);
+    }
+  }
   if constexpr (NT > kWave) {
     if (lane() == 0) {
 #pragma unroll
@@ -73,7 +80,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[16]) {
     for (int i = 0; i < N; ++i) {
       v[i] = 0.f;
 #pragma unroll
-      for (int w = 0; w < NT / kWave; ++w) v[i] += part[i][w];
+      for (int w = 0; w < NT / kWave; ++w) v[i] += part[i][threadIdx.x / NT * (NT / kWave) + w];
     }
   }
 }
@@ -203,17 +210,24 @@ struct Unit {
 
 // NT threads per row, as in the forward.  The row's sums are formed in one pass and
 // meet once: with t = g post_w y, the mean of q y is that of alpha t dr, and dr's
-// three terms give three sums.  The next row's loads are under way meanwhile
-// (AHEAD), and what belongs to a column stays in registers over the rows; rows too
-// long for that have neither.
-template <typename T, typename TY, typename TX, int NT, int EPT, bool AHEAD>
+// three terms give three sums.  What a row's registers hold:
+// kAhead: the row and what belongs to its columns, and the next row's loads are under
+//   way meanwhile;
+// kHeld: the row (longer ones);
+// kTwice: nothing, it is read again for the results, from the L2 or the chip's last
+//   cache (longer still, where holding spills: 1024 x 16384 from bfloat16 with float32
+//   dx and y 211 us for 363, 2048 x 8192 float32 102 for 114, but from bfloat16, which
+//   does not spill, 89 for 81).
+enum RowIn { kAhead, kHeld, kTwice };
+template <typename T, typename TY, typename TX, int NT, int EPT, RowIn IN>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_kernel(
     ResidualNormBackwardArgs a, float* sums) {
   constexpr int U = 16 / sizeof(T), NV = EPT / U, ROWS = NT < 256 ? 256 / NT : 1;
   constexpr int NS = 6;
   __shared__ float part[2][NS][16];
   __shared__ __attribute__((aligned(16))) float joined[ROWS > 1 ? ROWS * NT * EPT : 4];
-  const int t = threadIdx.x % NT, sub = threadIdx.x / NT, d = a.d;
+  int t = threadIdx.x % NT;
+  const int sub = threadIdx.x / NT, d = a.d;
   const T* gate = static_cast<const T*>(a.gate);
   const float over = 1.f / d;
   auto column = [&](int u) { return (u * NT + t) * U; };
@@ -229,36 +243,42 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
     if (a.post_w) v.pw.load(static_cast<const T*>(a.post_w) + column(u));
     if (a.gate_kind == kGateColumn) v.g.load(gate + column(u));
   };
-  if constexpr (AHEAD) {
+  if constexpr (IN == kAhead) {
 #pragma unroll
     for (int u = 0; u < NV; ++u) of_column(kept[u], u);
   }
+  struct RowUnit {
+    Unit<T, U> dr, r, g;
+    Unit<TX, U> dx;
+    Unit<TY, U> y;
+  };
   struct Row {
-    Unit<T, U> dr[NV], r[NV], g[NV];
-    Unit<TX, U> dx[NV];
-    Unit<TY, U> y[NV];
+    RowUnit u[NV];
     float gate;
   };
-  auto fetch = [&](Row& v, size_t row) {
-    const bool live = row < static_cast<size_t>(a.L);
+  auto fetch_unit = [&](RowUnit& v, size_t row, int u) {
     const size_t base = row * d;
-    v.gate = live && a.gate_kind == kGateToken ? load_one(gate + row) : 1.f;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      v.dr[u].clear();
-      v.r[u].clear();
-      v.dx[u].clear();
-      v.y[u].clear();
-      v.g[u].clear();
-      if (!live || column(u) >= d) continue;
-      if (a.dr_out) v.dr[u].load(static_cast<const T*>(a.dr_out) + base + column(u));
-      if (a.dx) {
-        v.r[u].load(static_cast<const T*>(a.r_out) + base + column(u));
-        v.dx[u].load(static_cast<const TX*>(a.dx) + base + column(u));
-      }
-      if (a.y) v.y[u].load(static_cast<const TY*>(a.y) + base + column(u));
-      if (a.gate_kind == kGateFull) v.g[u].load(gate + base + column(u));
+    v.dr.clear();
+    v.r.clear();
+    v.dx.clear();
+    v.y.clear();
+    v.g.clear();
+    if (row >= static_cast<size_t>(a.L) || column(u) >= d) return;
+    if (a.dr_out) v.dr.load(static_cast<const T*>(a.dr_out) + base + column(u));
+    if (a.dx) {
+      v.r.load(static_cast<const T*>(a.r_out) + base + column(u));
+      v.dx.load(static_cast<const TX*>(a.dx) + base + column(u));
     }
+    if (a.y) v.y.load(static_cast<const TY*>(a.y) + base + column(u));
+    if (a.gate_kind == kGateFull) v.g.load(gate + base + column(u));
+  };
+  auto fetch_gate = [&](size_t row) {
+    return row < static_cast<size_t>(a.L) && a.gate_kind == kGateToken ? load_one(gate + row) : 1.f;
+  };
+  auto fetch = [&](Row& v, size_t row) {
+    v.gate = fetch_gate(row);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) fetch_unit(v.u[u], row, u);
   };
   float total[3][NV][U] = {};
   const size_t step = static_cast<size_t>(gridDim.x) * ROWS;
@@ -268,25 +288,39 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
   size_t row = static_cast<size_t>(blockIdx.x) * ROWS + sub;
   size_t first = static_cast<size_t>(blockIdx.x) * ROWS;
   Row now, then;
-  fetch(now, row);
+  if constexpr (IN != kTwice) fetch(now, row);
   for (; first < static_cast<size_t>(a.L); first += step, row += step, turn ^= 1) {
     const bool live = row < static_cast<size_t>(a.L);
     const size_t base = row * d;
-    if constexpr (AHEAD) fetch(then, row + step);
+    if constexpr (IN == kAhead) fetch(then, row + step);
+    if constexpr (IN == kTwice) now.gate = fetch_gate(row);
+    // a unit of the row and its columns' values
+    auto unit = [&](int u, RowUnit& x, Column& k) {
+      if constexpr (IN == kTwice) {
+        // one unit after the other, its addresses formed anew
+        __builtin_amdgcn_sched_barrier(0);
+        __asm__ volatile("" : "+v"(t)::"memory");
+        fetch_unit(x, row, u);
+      } else {
+        x = now.u[u];
+      }
+      if constexpr (IN == kAhead) k = kept[u];
+      else of_column(k, u);
+    };
     float v[NS] = {};  // sums of r1^2, p r1, y^2, t dr_out, t p, t r1
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       float r[U], dx[U], y[U], dr[U], wf[U], pf[U], g[U];
-      now.r[u].floats(r);
-      now.dx[u].floats(dx);
-      now.y[u].floats(y);
-      now.dr[u].floats(dr);
+      RowUnit x;
       Column k;
-      if constexpr (AHEAD) k = kept[u];
-      else of_column(k, u);
+      unit(u, x, k);
+      x.r.floats(r);
+      x.dx.floats(dx);
+      x.y.floats(y);
+      x.dr.floats(dr);
       k.w.floats(wf);
       k.pw.floats(pf);
-      (full ? now.g[u] : k.g).floats(g);
+      (full ? x.g : k.g).floats(g);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const float p = dx[i] * wf[i], q = g[i] * pf[i] * y[i];
@@ -310,16 +344,16 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       float r[U], dx[U], y[U], dr[U], wf[U], pf[U], g[U], dg[U];
-      now.r[u].floats(r);
-      now.dx[u].floats(dx);
-      now.y[u].floats(y);
-      now.dr[u].floats(dr);
+      RowUnit x;
       Column k;
-      if constexpr (AHEAD) k = kept[u];
-      else of_column(k, u);
+      unit(u, x, k);
+      x.r.floats(r);
+      x.dx.floats(dx);
+      x.y.floats(y);
+      x.dr.floats(dr);
       k.w.floats(wf);
       k.pw.floats(pf);
-      (full ? now.g[u] : k.g).floats(g);
+      (full ? x.g : k.g).floats(g);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         dr[i] += s * (dx[i] * wf[i]) - c * r[i];
@@ -335,8 +369,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
       if (full && a.dgate) store_unit(static_cast<T*>(a.dgate) + base + column(u), dg);
       if (a.dy) store_unit(static_cast<TY*>(a.dy) + base + column(u), y);
     }
-    if constexpr (AHEAD) now = then;
-    else fetch(now, row + step);
+    if constexpr (IN == kAhead) now = then;
+    if constexpr (IN == kHeld) fetch(now, row + step);
   }
   if (!sums) return;
   const float* wanted[3] = {a.dw, a.dpost_w,
@@ -420,13 +454,16 @@ hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows of up to 512 columns: a wave each, four to a workgroup.  Parts: as many
-// workgroups as the chip holds at a time (two of 256 threads a CU; 8192 x 2048: 67 us,
-// with twice the parts 75).
+// As few threads to a row as hold it: 8192 x 1024 from bfloat16 takes 25 us with 128
+// and 38 with 256.  Parts: as many workgroups as the chip holds at a time (two of 256 threads a CU; 8192 x
+// 2048: 67 us, with twice the parts 75).
 constexpr int kNormParts = 512;
-static int norm_threads(int d) { return d <= 2048 ? 256 : d <= 8192 ? 512 : 1024; }
+static int norm_threads(int d) {  // of a row
+  return d <= 256 ? 32 : d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 8192 ? 512 : 1024;
+}
 static int norm_parts(int L, int d) {
-  const int rows = d <= 512 ? 4 : 1, n = (L + rows - 1) / rows, most = kNormParts * 256 / norm_threads(d);
+  const int nt = norm_threads(d), rows = nt < 256 ? 256 / nt : 1, n = (L + rows - 1) / rows;
+  const int most = nt <= 256 ? kNormParts : kNormParts * 256 / nt;
   return n < most ? n : most;
 }
 size_t residual_norm_backward_ws_bytes(int bf16, int L, int d) {
@@ -435,16 +472,21 @@ size_t residual_norm_backward_ws_bytes(int bf16, int L, int d) {
 template <typename T, typename TY, typename TX>
 static void run_norm_backward(const ResidualNormBackwardArgs& a, float* sums, hipStream_t s) {
   const unsigned nb = norm_parts(a.L, a.d);
-  if (a.d <= 512)
-    residual_norm_backward_kernel<T, TY, TX, 64, 8, true><<<nb, 256, 0, s>>>(a, sums);
+  if (a.d <= 256)
+    residual_norm_backward_kernel<T, TY, TX, 32, 8, kAhead><<<nb, 256, 0, s>>>(a, sums);
+  else if (a.d <= 512)
+    residual_norm_backward_kernel<T, TY, TX, 64, 8, kAhead><<<nb, 256, 0, s>>>(a, sums);
+  else if (a.d <= 1024)
+    residual_norm_backward_kernel<T, TY, TX, 128, 8, kAhead><<<nb, 256, 0, s>>>(a, sums);
   else if (a.d <= 2048)
-    residual_norm_backward_kernel<T, TY, TX, 256, 8, true><<<nb, 256, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 256, 8, kAhead><<<nb, 256, 0, s>>>(a, sums);
   else if (a.d <= 4096)
-    residual_norm_backward_kernel<T, TY, TX, 512, 8, true><<<nb, 512, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 512, 8, kAhead><<<nb, 512, 0, s>>>(a, sums);
   else if (a.d <= 8192)
-    residual_norm_backward_kernel<T, TY, TX, 512, 16, false><<<nb, 512, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 512, 16, sizeof(T) == 4 ? kTwice : kHeld>
+        <<<nb, 512, 0, s>>>(a, sums);
   else
-    residual_norm_backward_kernel<T, TY, TX, 1024, 16, false><<<nb, 1024, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 1024, 16, kTwice><<<nb, 1024, 0, s>>>(a, sums);
 }
 hipError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a, float* ws,
                                          hipStream_t s) {
