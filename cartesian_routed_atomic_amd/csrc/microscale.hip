@@ -625,6 +625,8 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(ExpertMatmulAr
 bool microscaled_matmul_fits(const ExpertMatmulArgs& a) {
   // offsets within a tile's weights are 32 bits, and so is an expert's number rounded up to 64
   if (a.n > 1 << 22 || a.k > 1 << 22 || a.E > 1 << 30) return false;
+  // an up row is n rows behind its gate row
+  if (a.swiglu && (a.n + 256ll) * (a.k / 2) >= 1ll << 32) return false;
   return a.M == 0 || mx_tiles(a, pick_mx_form(a)) < (1ll << 32) / 512;
 }
 template <typename TO, bool SW>

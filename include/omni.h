@@ -633,8 +633,9 @@ omni_status omni_microscale_rows(omni_dtype dt, int R, int k, const void* x, uin
  * OMNI_ACT_SWIGLU: wq [2n, k / 2], ws [2n, G], gate half first, out = silu(gate) *
  * up.  Sums are float32, rounded once to out_dt; scales as small as 2^-127 on both
  * sides may lose products below float32's normal numbers.
- * Requires k a multiple of 32, n and k at most 2^22, else UNSUPPORTED; xq, wq, out
- * 16-byte aligned, xs, ws 4-byte aligned.
+ * Requires k a multiple of 32, n and k at most 2^22, and for SWIGLU (n + 256) k / 2
+ * below 2^32 (an expert's gate half), else UNSUPPORTED; xq, wq, out 16-byte aligned,
+ * xs, ws 4-byte aligned.
  *
  * omni_microscaled_expert_matmul — the same over tasks sorted by expert, wq
  * [E, n, k / 2] and ws [E, n, G] (SWIGLU: 2n), xs [R, G] beside xq [R, k / 2];

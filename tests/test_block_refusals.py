@@ -119,6 +119,7 @@ def test_microscale_argument_checks():
             assert call(**bad) == INV, bad
         assert call(k=48) == UNS and call(n=(1 << 22) + 1) == UNS and call(k=(1 << 22) + 32) == UNS
         assert call(M=1 << 30, R=1 << 30, Ro=1 << 30, n=1 << 20) == UNS
+        assert call(act=1, n=1 << 17, k=1 << 16) == UNS and call(act=1, n=1 << 22, k=2048) == UNS
         assert call(M=0, R=0, Ro=0, x=None, xs=None, out=None) == OK
 
 
