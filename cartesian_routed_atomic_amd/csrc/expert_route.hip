@@ -4,7 +4,7 @@
 // experts can lie within float32's rounding of each other, so their order is that
 // of float64.  Nearly always float32 tells it; where any two that had to be told
 // apart are closer than twice its error, those are decided in float64 (16384 tokens,
-// 256 experts, 8 of them, sigmoid, groups: 15.9 us, with float64 throughout 43.9).
+// 256 experts, 8 of them, sigmoid, groups: 17.6 us, with float64 throughout 43.9).
 // Without a bias the score grows with the logit, which is compared as it stands.
 //
 // The error of c, in units of 2^-24.  e^x: the exponent's product with log2 e is off
@@ -19,6 +19,8 @@
 #include "device.hpp"
 #include "launch.hpp"
 
+#include <type_traits>
+
 namespace omni {
 
 // T lanes (a DPP row, or the wave) share a token; lane l of them holds experts
@@ -28,6 +30,20 @@ template <int ctrl>
 __device__ __forceinline__ uint32_t dpp_row(uint32_t v) {
   return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), ctrl, 0xf, 0xf, true));
 }
+// lane `from` of the token's (T == kWave: the same one for all) as all of them see it
+template <int T, typename V>
+__device__ __forceinline__ V of_lane(V v, int from) {
+  if constexpr (T != kWave) {
+    return __shfl(v, from, T);
+  } else if constexpr (sizeof(V) == 4) {
+    return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), from));
+  } else {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), from);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), from);
+    return __builtin_bit_cast(V, static_cast<uint64_t>(hi) << 32 | lo);
+  }
+}
 // op over the token's lanes, the result in all of them; halves are added to halves,
 // so every lane forms the same sum
 template <int T, class Op>
@@ -36,10 +52,8 @@ __device__ __forceinline__ uint32_t over_lanes(uint32_t v, Op op) {
   v = op(v, dpp_row<0x124>(v));
   v = op(v, dpp_row<0x122>(v));
   v = op(v, dpp_row<0x121>(v));
-  if constexpr (T == kWave) {
-    v = op(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 16)));
-    v = op(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 32)));
-  }
+  if constexpr (T == kWave)
+    v = op(op(of_lane<T>(v, 0), of_lane<T>(v, 16)), op(of_lane<T>(v, 32), of_lane<T>(v, 48)));
   return v;
 }
 template <int T>
@@ -64,11 +78,20 @@ __device__ __forceinline__ uint64_t lanes_max(uint64_t v) {
   const uint32_t lo = lanes_max<T>(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
   return static_cast<uint64_t>(hi) << 32 | lo;
 }
-template <int T>
-__device__ __forceinline__ int lanes_min(int v) {  // of numbers not negative
-  return static_cast<int>(over_lanes<T>(static_cast<uint32_t>(v), [](uint32_t a, uint32_t b) {
-    return min(a, b);
-  }));
+// over the wave
+__device__ __forceinline__ double lanes_sum(double v) {
+  auto turned = [&](auto by) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = dpp_row<by()>(static_cast<uint32_t>(u));
+    const uint32_t hi = dpp_row<by()>(static_cast<uint32_t>(u >> 32));
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+  };
+  v += turned(std::integral_constant<int, 0x128>{});
+  v += turned(std::integral_constant<int, 0x124>{});
+  v += turned(std::integral_constant<int, 0x122>{});
+  v += turned(std::integral_constant<int, 0x121>{});
+  return (of_lane<kWave>(v, 0) + of_lane<kWave>(v, 16)) +
+         (of_lane<kWave>(v, 32) + of_lane<kWave>(v, 48));
 }
 // true in all of the token's lanes if in any
 template <int T>
@@ -192,10 +215,12 @@ __device__ __forceinline__ int take_best(uint64_t (&key)[V], int K) {
 #pragma unroll
     for (int v = 1; v < V; ++v) best = max(best, key[v]);
     best = lanes_max<kWave>(best);
-    int at = 1 << 20;
+    int at = 0;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v) at = key[v] == best ? v * 64 + l : at;
-    at = lanes_min<kWave>(at);
+    for (int v = V - 1; v >= 0; --v) {
+      const uint64_t m = __ballot(key[v] == best);
+      if (m != 0) at = v * 64 + __ffsll(static_cast<long long>(m)) - 1;
+    }
     if (l == k) mine = at;
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = key[v] == best && at == v * 64 + l ? 0 : key[v];
@@ -241,7 +266,7 @@ __device__ __forceinline__ uint64_t best_groups(const F* c, const ExpertRouteArg
   const Key key = order_key(value);
   int ahead = 0;
   for (int j = 0; j < a.groups; ++j) {
-    const Key other = __shfl(key, j << shift, T);
+    const Key other = of_lane<T>(key, j << shift);
     ahead += other > key || (other == key && j < g) ? 1 : 0;
   }
   const int low = T == kWave ? 0 : lane() & ~(T - 1);  // the token's first lane
@@ -250,8 +275,8 @@ __device__ __forceinline__ uint64_t best_groups(const F* c, const ExpertRouteArg
   };
   const int last = lane_of(a.top_groups - 1), first = lane_of(a.top_groups);
   const F terms = a.group_best == 2 && size > 1 ? fabs(b1) + fabs(b2) : fabs(b1);
-  apart(__shfl(value, last, T), __shfl(value, first, T),
-        __shfl(terms, last, T) + __shfl(terms, first, T));
+  apart(of_lane<T>(value, last), of_lane<T>(value, first),
+        of_lane<T>(terms, last) + of_lane<T>(terms, first));
   const uint64_t stay = __ballot(mine && ahead < a.top_groups);
   return T == kWave ? stay : stay >> low & ((1ull << (T & 63)) - 1);
 }
@@ -284,7 +309,7 @@ __device__ __forceinline__ int decide_exactly(const ExpertRouteArgs& a, size_t t
     }
     if (!a.sigmoid) {
       bad = __any(bad);
-      for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
+      total = lanes_sum(total);
 #pragma unroll
       for (int v = 0; v < V; ++v)
         d[v] = bad ? __builtin_nan("") : total > 0.0 ? d[v] / total : 0.0;
@@ -341,7 +366,7 @@ __device__ __forceinline__ bool rank_near(const ExpertRouteArgs& a, const L* row
     upto += dpp_u<0x142, 0xa>(0u, upto);
     upto += dpp_u<0x143, 0xc>(0u, upto);
   }
-  const int n = __shfl(static_cast<int>(upto), T - 1, T);
+  const int n = of_lane<T>(static_cast<int>(upto), T - 1);
   const bool fits = n >= a.K && n <= T;
   int at = static_cast<int>(upto) - count;
   wave_lds_fence();
@@ -370,9 +395,10 @@ __device__ __forceinline__ bool rank_near(const ExpertRouteArgs& a, const L* row
       ahead += other > mine || (other == mine && static_cast<int>(id) < e) ? 1 : 0;
     }
   } else {
-    for (int j = 0; j < T; ++j) {
-      const uint64_t other = __shfl(mine, j);
-      const int id = __shfl(e, j);
+    const int some = min(n, T);
+    for (int j = 0; j < some; ++j) {
+      const uint64_t other = of_lane<T>(mine, j);
+      const int id = of_lane<T>(e, j);
       ahead += other > mine || (other == mine && id < e) ? 1 : 0;
     }
   }
@@ -409,15 +435,15 @@ __global__ __launch_bounds__(256) void expert_route_kernel(ExpertRouteArgs a) {
   const bool sums = GROUPS && (biased || a.group_best == 2);  // groups compared by scores
   float largest = 1.f;  // score, or above it
   if (!a.sigmoid) {
-    float sum = 0.f;
+    float parts[2] = {0.f, 0.f};  // of 16 each
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       bad |= z[v] != z[v] || z[v] == INFINITY;
       s[v] = __expf(z[v] - from);
-      sum += s[v];
+      parts[v / 16] += s[v];
     }
     bad = lanes_any<T>(bad);
-    sum = lanes_sum<T>(sum);
+    const float sum = lanes_sum<T>(parts[0] + parts[1]);
     largest = bad ? __builtin_nanf("") : sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] *= largest;
@@ -580,8 +606,8 @@ __global__ __launch_bounds__(256) void expert_route_backward_kernel(ExpertRouteB
   // the same expert more than once: each of its lanes forms the sum, in order
   float sum = 0.f;
   for (int k = 0; k < a.K; ++k) {
-    const int other = __shfl(id, k, T);
-    const float x = __shfl(up, k, T);
+    const int other = of_lane<T>(id, k);
+    const float x = of_lane<T>(up, k);
     if (other == id) sum += x;
   }
   wave_lds_fence();
@@ -636,14 +662,25 @@ __global__ __launch_bounds__(256) void expert_route_backward_kernel(ExpertRouteB
   }
 }
 
-// Sixteen lanes per token where they hold its experts, groups and selection.
+// Sixteen lanes per token, four tokens a wave, take fewer instructions, a wave per token
+// is sooner done with it: sixteen where they hold the token's experts, groups and
+// selection and the tokens are many; either way a token of up to 64 experts has four
+// slots a lane.  us, sixteen lanes and 64, 8 selected, softmax scores:
+//   tokens           1          1024       2048       4096       8192       16384
+//   128 experts      3.8 3.5    4.1 3.9    4.1 4.2    4.2 5.2    4.5 7.7    5.9 12.6
+//   256 experts      4.9 3.3    5.3 3.8    5.4 4.2    5.5 5.2    6.0 7.8    8.3 12.5
+//   512 experts      7.5 4.0    7.9 4.5    7.9 4.9    8.0 6.5    9.1 10.0   13.2 17.0
+static bool sixteen_lanes(int L, int E, int K, int groups) {
+  return E <= 512 && K <= 16 && groups <= 16 && (E <= 64 || L > 16 * E);
+}
 template <typename L, bool GROUPS>
 static void run_route(const ExpertRouteArgs& a, hipStream_t s) {
   const unsigned n = static_cast<unsigned>(a.L), few = (n + 15) / 16, many = (n + 3) / 4;
-  if (a.E <= 256 && a.K <= 16 && a.groups <= 16) {
+  if (sixteen_lanes(a.L, a.E, a.K, a.groups)) {
     if (a.E <= 64) expert_route_kernel<L, 16, 4, GROUPS><<<few, 256, 0, s>>>(a);
     else if (a.E <= 128) expert_route_kernel<L, 16, 8, GROUPS><<<few, 256, 0, s>>>(a);
-    else expert_route_kernel<L, 16, 16, GROUPS><<<few, 256, 0, s>>>(a);
+    else if (a.E <= 256) expert_route_kernel<L, 16, 16, GROUPS><<<few, 256, 0, s>>>(a);
+    else expert_route_kernel<L, 16, 32, GROUPS><<<few, 256, 0, s>>>(a);
   } else if (a.E <= 256) expert_route_kernel<L, 64, 4, GROUPS><<<many, 256, 0, s>>>(a);
   else if (a.E <= 512) expert_route_kernel<L, 64, 8, GROUPS><<<many, 256, 0, s>>>(a);
   else expert_route_kernel<L, 64, 16, GROUPS><<<many, 256, 0, s>>>(a);
@@ -654,10 +691,12 @@ hipError_t launch_expert_route(const ExpertRouteArgs& a, hipStream_t s) {
   else groups ? run_route<float, true>(a, s) : run_route<float, false>(a, s);
   return hipGetLastError();
 }
+// As above; 2.4 us for 2.7 of one token of 256 experts, 7.7 for 5.8 of 16384.  Rows of
+// more than 256 experts are a wave's: 17.6 us for 20.0 of 16384 of 512.
 template <typename L>
 static void run_route_backward(const ExpertRouteBackwardArgs& a, hipStream_t s) {
   const unsigned n = static_cast<unsigned>(a.L), few = (n + 15) / 16, many = (n + 3) / 4;
-  if (a.E <= 256 && a.K <= 16) {
+  if (a.E <= 256 && a.K <= 16 && (a.E <= 64 || a.L > 8 * a.E)) {
     if (a.E <= 64) expert_route_backward_kernel<L, 16, 4><<<few, 256, 0, s>>>(a);
     else if (a.E <= 128) expert_route_backward_kernel<L, 16, 8><<<few, 256, 0, s>>>(a);
     else expert_route_backward_kernel<L, 16, 16><<<few, 256, 0, s>>>(a);
