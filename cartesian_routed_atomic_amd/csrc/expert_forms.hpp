@@ -171,16 +171,18 @@ inline long long mx_blocks(const ExpertMatmulArgs& a, MxForm f) {
   const bool rows = f == kMxRows16 || f == kMxRows32;
   return rows || !mx_tiles_in_turn(a.k) || t < mx_slots(f) ? t : mx_slots(f);
 }
-// Which one: the tile of least expected time, in us: its rounds of the chip times
-// the stages of 256 elements of a tile, and its start.  Fitted to (us; 2048 inputs,
-// the last two lines 704 and 8192):
-//   tiles of 256 x 256    256 x 256   128 x 256   128 x 128   64 x 128
-//   16                    19.4        13.5        11.0        9.1
-//   64                    20.7        14.9        12.7        12.9
-//   256                   37.4        30.4        30.5        38.9
-//   704                   67.8        77.0        79.8        107
-//   192 (32 experts)      28.8        21.2        19.3        23.3
-//   1024                  311         367         387         498
+// Which one: the tile of least expected time, in us: its rounds of the chip times a
+// start and the stages of 256 elements of a tile.  Workgroups of two a CU share it:
+// where the last round has few of them, those are faster, and so are 256 or fewer.
+// Fitted over 170 shapes, where the tile chosen takes 0.5 % more than the best one in
+// the geometric mean; some of them (us; tasks of all experts x outputs x inputs):
+//   tiles of                          256 x 256   128 x 256   128 x 128   64 x 128
+//   2048 x 2048 x 2048                20.3        14.4        11.6        11.9
+//   8192 x 5632 x 2048                67.8        77.0        79.8        107
+//   8192 x 2048 x 2048                27.0        28.4        29.6        35.4
+//   12234 x 1408 x 704, 32 experts    28.8        21.2        19.3        23.3
+//   4096 x 1408 x 2048, 64 experts    40.1        27.9        23.6        23.5
+//   4096 x 4096 x 4096, 8 experts     69.4        65.6        59.7        70.5
 // The rows kernels where a few of the smallest tiles have few rows (us; rows of 16
 // and of 32 against 64 x 128 tiles; 2048 inputs):
 //   1 expert, 2048 outputs, 1 / 64 / 128 / 256     6.8 6.9 10 17 / 6.5 6.7 7.7 10 / 8.7 8.8 8.8 8.8
@@ -191,18 +193,23 @@ inline MxForm pick_mx_form(const ExpertMatmulArgs& a) {
   const double nk = (a.k + 255) / 256;
   const double small = expected_tiles(a, 64, 128 / h);
   if (small <= 96 && small * r <= 2048) return r <= 8 ? kMxRows16 : kMxRows32;
-  auto rounds = [](double tiles, int slots) {
-    const double t = tiles / slots;
-    return t <= 1 ? 1. : t <= 4 ? static_cast<double>(static_cast<int>(t + 0.999)) : t;
+  struct Rounds {
+    double part, whole;
   };
-  // half the chip's slots: alone on a CU, a workgroup is faster
-  auto half = [](double tiles) { return tiles <= 256 ? 0.55 : 1.; };
+  auto rounds = [](double tiles, int slots) {
+    const double t = tiles / slots < 1 ? 1. : tiles / slots;
+    const double up = t <= 64 ? static_cast<double>(static_cast<int>(t + 0.999)) : t;
+    return Rounds{t, up < t ? t : up};
+  };
+  auto half = [](double tiles) { return tiles <= 256 ? 0.6 : 1.; };
   const double mid = expected_tiles(a, 128, 128 / h), wide = expected_tiles(a, 128, 256 / h),
                big = expected_tiles(a, 256, 256 / h);
-  const double t_small = 4 + rounds(small, 512) * (0.97 * nk + 1.2) * half(small);
-  const double t_mid = 5 + rounds(mid, 512) * (1.5 * nk + 0.8) * half(mid);
-  const double t_wide = 6 + rounds(wide, 256) * (1.43 * nk + 0.7);
-  const double t_big = 14 + (big > 256 ? big / 256 : 1.) * (2.4 * nk + 1);
+  const Rounds r_small = rounds(small, 512), r_mid = rounds(mid, 512);
+  const double t_small =
+      3.3 + (0.5 * r_small.part + 0.5 * r_small.whole) * (0.825 * nk + 2.5) * half(small);
+  const double t_mid = 3.1 + (0.75 * r_mid.part + 0.25 * r_mid.whole) * (1.12 * nk + 4.1) * half(mid);
+  const double t_wide = 0.7 + rounds(wide, 256).whole * (0.94 * nk + 5.7);
+  const double t_big = rounds(big, 256).whole * (1.47 * nk + 8.5);
   if (t_big <= t_wide && t_big <= t_mid && t_big <= t_small) return kMxBig;
   if (t_wide <= t_mid && t_wide <= t_small) return kMxWide;
   return t_mid <= t_small ? kMxMid : kMxSmall;

@@ -21,12 +21,12 @@ CASES = [
     ("small", True, [9 + e % 5 for e in range(60)], 650, 416, True),
     ("mid", False, [900, 600, 80], 2040, 864, False),
     ("mid", False, [1200, 700], 1016, 2080, True),
-    ("mid", True, [1900, 40, 0, 1800], 2424, 448, False),
-    ("mid", True, [2000, 0, 1700], 1210, 992, True),
+    ("mid", True, [4000, 40, 0, 3900], 2424, 448, False),
+    ("mid", True, [4001, 0, 3899], 1210, 992, True),
     ("wide", False, [1020, 5], 4088, 5152, False),
     ("wide", False, [1020, 5], 2044, 5152, True),
-    ("wide", True, [5000], 2568, 3232, False),
-    ("wide", True, [4600], 1284, 3232, True),
+    ("wide", True, [90 + e for e in range(34)], 2568, 2336, False),
+    ("wide", True, [90 + e for e in range(34)], 1284, 2336, True),
     ("big", True, [5001, 0, 4900], 2312, 3360, False),
     ("big", True, [5001, 0, 4900], 1156, 3360, True),
 ]
