@@ -183,16 +183,18 @@ inline long long mx_blocks(const ExpertMatmulArgs& a, MxForm f) {
 //   12234 x 1408 x 704, 32 experts    28.8        21.2        19.3        23.3
 //   4096 x 1408 x 2048, 64 experts    40.1        27.9        23.6        23.5
 //   4096 x 4096 x 4096, 8 experts     69.4        65.6        59.7        70.5
-// The rows kernels where a few of the smallest tiles have few rows (us; rows of 16
-// and of 32 against 64 x 128 tiles; 2048 inputs):
-//   1 expert, 2048 outputs, 1 / 64 / 128 / 256     6.8 6.9 10 17 / 6.5 6.7 7.7 10 / 8.7 8.8 8.8 8.8
-//   1 expert, 5632 outputs, SWIGLU, 1 / 8 / 32     7.1 7.7 11 / 7.3 8.2 11 / 10 9.8 9.2
-//   64 experts, 1408 outputs, 1 / 8                30 44 / 31 39 / 20 20
+// The rows kernels where their workgroups are about one for a CU, two for those of
+// 16 with few rows (us; rows of 16 and of 32 against 64 x 128 tiles, 2048 inputs):
+//   1 expert, 2048 outputs, 1 / 64 / 128 / 256     4.3 6.3 9.8 17 / 5.0 6.5 6.6 10 / 7.7 8.2 8.2 8.2
+//   1 expert, 5632 outputs, 1 / 16 / 64            4.6 6.1 13 / 4.9 5.7 10 / 7.6 7.8 8.2
+//   1 expert, 5632 outputs, SWIGLU, 1 / 8 / 32     6.7 7.6 11 / 7.1 8.1 10 / 8.2 8.4 8.5
+//   64 experts, 1408 outputs, 1 / 8                29 43 / 30 39 / 19 20
 inline MxForm pick_mx_form(const ExpertMatmulArgs& a) {
   const int h = a.swiglu ? 2 : 1, r = a.M / used_experts(a);
   const double nk = (a.k + 255) / 256;
-  const double small = expected_tiles(a, 64, 128 / h);
-  if (small <= 96 && small * r <= 2048) return r <= 8 ? kMxRows16 : kMxRows32;
+  const double rows = expected_tiles(a, 16, 16);
+  if (rows <= 300 || (r <= 8 && rows <= 512)) return kMxRows16;
+  if (expected_tiles(a, 32, 32 / h) <= 300) return kMxRows32;
   struct Rounds {
     double part, whole;
   };
@@ -202,8 +204,8 @@ inline MxForm pick_mx_form(const ExpertMatmulArgs& a) {
     return Rounds{t, up < t ? t : up};
   };
   auto half = [](double tiles) { return tiles <= 256 ? 0.6 : 1.; };
-  const double mid = expected_tiles(a, 128, 128 / h), wide = expected_tiles(a, 128, 256 / h),
-               big = expected_tiles(a, 256, 256 / h);
+  const double small = expected_tiles(a, 64, 128 / h), mid = expected_tiles(a, 128, 128 / h),
+               wide = expected_tiles(a, 128, 256 / h), big = expected_tiles(a, 256, 256 / h);
   const Rounds r_small = rounds(small, 512), r_mid = rounds(mid, 512);
   const double t_small =
       3.3 + (0.5 * r_small.part + 0.5 * r_small.whole) * (0.825 * nk + 2.5) * half(small);

@@ -10,11 +10,11 @@ FORMS = ("rows16", "rows32", "small", "mid", "wide", "big")
 CASES = [
     ("rows16", False, [5, 0, 9, 7], 264, 4896, False),
     ("rows16", False, [5, 0, 9, 7], 264, 4896, True),
-    ("rows32", False, [64, 65], 520, 4896, False),
-    ("rows32", False, [33, 40], 200, 4896, True),
+    ("rows32", False, [64, 65], 776, 4896, False),
+    ("rows32", False, [33, 40], 904, 4896, True),
     # rows of less than 16 scales: a tile each
     ("small", False, [300, 3, 0, 70], 1032, 96, False),
-    ("small", False, [200, 33], 520, 384, True),
+    ("small", False, [200, 33], 648, 384, True),
     ("small", False, [510, 3], 2056, 1120, False),
     ("small", False, [300, 0, 129], 1032, 736, True),
     ("small", True, [16 + e % 7 for e in range(60)], 1288, 800, False),
