@@ -1,4 +1,5 @@
-"""Build libomni.so (the C-ABI library) for gfx950 with hipcc, in-tree.
+"""Build libomni.so (the C-ABI library) for gfx950 with hipcc, and _host_call.so (the
+binding's host part, C++ on Python's and torch's headers), in-tree.
 
     python -m cartesian_routed_atomic_amd.build
 
@@ -11,12 +12,16 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libomni.so")
+HOST_CALL = os.path.join(HERE, "_host_call.so")
 SOURCES = ["api.hip", "router.hip", "topk.hip", "schedule.hip", "execute.hip", "backward.hip",
            "flat_router.hip", "grouped.hip", "chunked.hip", "expert_matmul.hip",
            "expert_combine.hip", "quantize.hip", "microscale.hip", "expert_route.hip",
@@ -29,6 +34,10 @@ def hipcc() -> str:
         if c and (os.path.isabs(c) and os.path.exists(c) or not os.path.isabs(c)):
             return c
     return "hipcc"
+
+
+def rocm() -> str:
+    return os.environ.get("ROCM_PATH", "/opt/rocm")
 
 
 def common_flags():
@@ -51,10 +60,29 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_host_call() -> None:
+    from torch.utils import cpp_extension
+    lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"],
+                *cpp_extension.include_paths(), os.path.join(rocm(), "include")]
+    tmp = HOST_CALL + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D__HIP_PLATFORM_AMD__",  # whose types the runtime's header declares
+           *(f for d in includes for f in ("-isystem", d)),
+           os.path.join(CSRC, "host_call.cpp"), "-o", tmp, "-L" + lib_dir, "-ltorch_python",
+           "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"host_call.cpp failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST_CALL)
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     with cf.ThreadPoolExecutor(min(len(SOURCES), os.cpu_count() or 1)) as ex:
+        host = ex.submit(_build_host_call)
         objs = list(ex.map(_compile, SOURCES))
+        host.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
