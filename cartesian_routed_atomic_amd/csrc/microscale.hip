@@ -152,7 +152,9 @@ __device__ __forceinline__ void mx_mma(f32x4& c, const MxFrag& q, const MxFrag& 
 }
 
 // 16 RT tasks x 16 CT rows of W per workgroup, the contraction split over its KS
-// waves, whose sums are added through LDS in wave order.
+// waves, whose sums are added through LDS in wave order.  Bound by one memory latency:
+// all of a wave's loads are out before its first MFMA.  One row by 11264 x 2048, 12.3
+// MB of weights: 7.5 us, of which reading them at a copy's rate takes 2.4.
 // SWIGLU: the first CT / 2 column tiles are gate rows, the others their up rows.
 template <typename TO, bool SWIGLU, int RT, int CT, int KS, int U>
 __global__ __launch_bounds__(KS * 64) void mx_rows_kernel(ExpertMatmulArgs a) {
@@ -283,9 +285,14 @@ __device__ __forceinline__ TilePlace same_in_wave(TilePlace p) {
 }
 
 // Tile BM tasks x BN columns, WM x WN waves, ring of S stages of 128 bytes (256
-// elements, a cache line) a row.  A workgroup runs its tiles one after the other as one stream
-// of stages: the next tile's first stages are under way while this one's last run
-// and its results are stored.
+// elements, a cache line: with 64 every line was fetched twice, 76 us for 70) a row.  A
+// workgroup runs its tiles one after the other as one stream of stages: the next
+// tile's first stages are under way while this one's last run and its results are
+// stored (8192 x 5632 x 2048 in a launch's workgroup per tile: 83 us for 72).
+// 8192 x 5632 x 2048: 67 us, 2.8 POP/s, 39 % of the MFMAs' cycles at the 1.7 GHz that
+// power leaves (64 without its loads, 56 without its stores, 49 without either); 8192
+// x 8192 x 8192: 313 us, 3.5 POP/s; 2048 tasks of 64 experts of 1408 x 2048, 98 MB of
+// weights and scales: 27 us, 3.6 TB/s.
 template <typename TO, bool SWIGLU, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * 64, 2) void mx_tile_kernel(ExpertMatmulArgs a) {
   constexpr int NW = WM * WN, S = 2;

@@ -672,7 +672,8 @@ omni_status omni_microscaled_expert_matmul(omni_dtype out_dt, int M, int E, int 
  * s = 0 and gates 0.  A bias of -infinity ranks an expert behind all others that
  * can be selected.  A NaN logit, or with softmax a +infinity, makes its row's s
  * NaN (sigmoid: that expert's), and gates of NaN s are NaN; a NaN in what is
- * compared ranks as -infinity.  K scores of 0 give K gates of 0.  The K ids are distinct and in [0, E) whatever the logits hold.
+ * compared ranks as -infinity.  K scores of 0 give K gates of 0.  The K ids are
+ * distinct and in [0, E) whatever the logits hold.
  * Renormalised gates are formed from ratios that cannot lose all K (logits of
  * -200 under sigmoid share out as exp does).
  * Requires 1 <= K <= top_groups * (E / groups), 1 <= top_groups <= groups, E a
