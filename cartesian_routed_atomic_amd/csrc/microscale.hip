@@ -154,11 +154,12 @@ __device__ __forceinline__ void mx_mma(f32x4& c, const MxFrag& q, const MxFrag& 
 // 16 RT tasks x 16 CT rows of W per workgroup, the contraction split over its KS
 // waves, whose sums are added through LDS in wave order.  Bound by one memory latency:
 // all of a wave's loads are out before its first MFMA.  One row by 11264 x 2048, 12.3
-// MB of weights: 7.5 us, of which reading them at a copy's rate takes 2.4.
+// MB of weights: 6.3 us, of which reading them at a copy's rate takes 2.4.
 // SWIGLU: the first CT / 2 column tiles are gate rows, the others their up rows.
 template <typename TO, bool SWIGLU, int RT, int CT, int KS, int U>
 __global__ __launch_bounds__(KS * 64) void mx_rows_kernel(ExpertMatmulArgs a) {
   constexpr int BM = 16 * RT, H = SWIGLU ? 2 : 1, CO = CT / H, BNO = 16 * CO;
+  static_assert(U == 2 || U == 4, "align_scales");
   static_assert(CT % H == 0, "gate and up tiles in pairs");
   __shared__ __attribute__((aligned(16))) f32x4 part[KS][RT * CT][64];
   const int wv = threadIdx.x >> 6, l = threadIdx.x & 63, fr = l & 15, g = l >> 4;
@@ -176,41 +177,77 @@ __global__ __launch_bounds__(KS * 64) void mx_rows_kernel(ExpertMatmulArgs a) {
     const int m = min(t.m0 + i * 16 + fr, t.m1 - 1);
     const size_t row = min(max(a.x_row ? a.x_row[m] : m, 0), a.R - 1);
     psrc[i] = static_cast<const uint8_t*>(a.x) + row * row_bytes + g * 16;
-    pscale[i] = a.x_mx + row * row_scales + g;
+    pscale[i] = a.x_mx + row * row_scales;
   }
 #pragma unroll
   for (int j = 0; j < CT; ++j) {
     const size_t row = first + min(n0 + j % CO * 16 + fr, N - 1) + static_cast<size_t>(j / CO) * N;
     qsrc[j] = static_cast<const uint8_t*>(a.w) + row * row_bytes + g * 16;
-    qscale[j] = a.w_mx + row * row_scales + g;
+    qscale[j] = a.w_mx + row * row_scales;
   }
   const int blocks = a.k / kMxBlock, nk = (blocks + 3) / 4;
   const int per = (nk + KS - 1) / KS, kb = min(nk, wv * per), ke = min(nk, kb + per);
   f32x4 acc[RT][CT] = {};
-  // past the end of a row zeros with a scale of one
-  auto fetch = [&](const uint8_t* src, const uint8_t* scale, int kt) {
-    MxFrag f = {{0, 0, 0, 0}, 127};
-    if (kt < ke && kt * 4 + g < blocks) {
-      f.q = *reinterpret_cast<const i32x4*>(src + static_cast<size_t>(kt) * 64);
-      f.scale = scale[kt * 4];
+  // The scales of U steps from k0 on, a word each, in one load: a byte at a time they
+  // took a quarter of the kernel (1 x 11264 x 2048: 7.3 us for 6.3).  A row's last
+  // 4 U bytes are those of its last U steps.
+  auto load_scales = [&](uint32_t (&w)[U], const uint8_t* scale, int k0) {
+    if (nk < U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        w[u] = k0 + u < nk ? *reinterpret_cast<const uint32_t*>(scale + (k0 + u) * 4) : 0u;
+      return;
     }
-    return f;
+    __builtin_memcpy(w, __builtin_assume_aligned(scale + min(k0, nk - U) * 4, 4), 4 * U);
+  };
+  // to step k0's first where the load began before it
+  auto align_scales = [&](uint32_t (&w)[U], int k0) {
+    const int early = nk < U ? 0 : k0 - min(k0, nk - U);
+    if constexpr (U == 4) {
+      if (early & 2) {
+        w[0] = w[2];
+        w[1] = w[3];
+      }
+    }
+    if (early & 1) {
+#pragma unroll
+      for (int u = 0; u + 1 < U; ++u) w[u] = w[u + 1];
+    }
+  };
+  // past the end of a row zeros with a scale of one
+  auto inside = [&](int kt) { return kt < ke && kt * 4 + g < blocks; };
+  auto fetch = [&](const uint8_t* src, int kt) {
+    return inside(kt) ? *reinterpret_cast<const i32x4*>(src + static_cast<size_t>(kt) * 64)
+                      : i32x4{0, 0, 0, 0};
   };
   for (int k0 = kb; k0 < ke; k0 += U) {
-    MxFrag p[U][RT], q[U][CT];
+    i32x4 p[U][RT], q[U][CT];
+    uint32_t ps[RT][U], qs[CT][U];
+#pragma unroll
+    for (int j = 0; j < CT; ++j) load_scales(qs[j], qscale[j], k0);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) load_scales(ps[i], pscale[i], k0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int j = 0; j < CT; ++j) q[u][j] = fetch(qsrc[j], qscale[j], k0 + u);
+      for (int j = 0; j < CT; ++j) q[u][j] = fetch(qsrc[j], k0 + u);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) p[u][i] = fetch(psrc[i], pscale[i], k0 + u);
+      for (int i = 0; i < RT; ++i) p[u][i] = fetch(psrc[i], k0 + u);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int j = 0; j < CT; ++j) align_scales(qs[j], k0);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) align_scales(ps[i], k0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = inside(k0 + u);
+      auto own = [&](uint32_t w) { return static_cast<int>(in ? w >> (8 * g) : 127u); };
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int j = 0; j < CT; ++j) mx_mma(acc[i][j], q[u][j], p[u][i]);
+        for (int j = 0; j < CT; ++j)
+          mx_mma(acc[i][j], {q[u][j], own(qs[j][u])}, {p[u][i], own(ps[i][u])});
+    }
   }
 #pragma unroll
   for (int i = 0; i < RT; ++i)
@@ -640,8 +677,16 @@ template <typename TO, bool SW>
 static hipError_t run_mx(const ExpertMatmulArgs& a, hipStream_t s) {
   const MxForm f = pick_mx_form(a);
   const unsigned nb = static_cast<unsigned>(mx_blocks(a, f));
-  if (f == kMxRows16) mx_rows_kernel<TO, SW, 1, SW ? 2 : 1, 8, 2><<<nb, 512, 0, s>>>(a);
-  else if (f == kMxRows32) mx_rows_kernel<TO, SW, 2, 2, 8, 2><<<nb, 512, 0, s>>>(a);
+  // steps of a wave at a time: two where a wave has no more (1 x 4096 x 4096: 4.7 us
+  // with four, 4.9 with two; 1 x 11264 x 2048: 6.4 and 6.3)
+  const bool more = a.k > 2048;
+  if (f == kMxRows16) {
+    if (more) mx_rows_kernel<TO, SW, 1, SW ? 2 : 1, 8, 4><<<nb, 512, 0, s>>>(a);
+    else mx_rows_kernel<TO, SW, 1, SW ? 2 : 1, 8, 2><<<nb, 512, 0, s>>>(a);
+  } else if (f == kMxRows32) {
+    if (more) mx_rows_kernel<TO, SW, 2, 2, 8, 4><<<nb, 512, 0, s>>>(a);
+    else mx_rows_kernel<TO, SW, 2, 2, 8, 2><<<nb, 512, 0, s>>>(a);
+  }
   else if (f == kMxSmall) mx_tile_kernel<TO, SW, 64, 128, 2, 2><<<nb, 256, 0, s>>>(a);
   else if (f == kMxMid) mx_tile_kernel<TO, SW, 128, 128, 2, 2><<<nb, 256, 0, s>>>(a);
   else if (f == kMxWide) mx_tile_kernel<TO, SW, 128, 256, 2, 4><<<nb, 512, 0, s>>>(a);
