@@ -183,18 +183,19 @@ inline long long mx_blocks(const ExpertMatmulArgs& a, MxForm f) {
 //   12234 x 1408 x 704, 32 experts    28.8        21.2        19.3        23.3
 //   4096 x 1408 x 2048, 64 experts    40.1        27.9        23.6        23.5
 //   4096 x 4096 x 4096, 8 experts     69.4        65.6        59.7        70.5
-// The rows kernels where their workgroups are about one for a CU, two for those of
-// 16 with few rows (us; rows of 16 and of 32 against 64 x 128 tiles, 2048 inputs):
-//   1 expert, 2048 outputs, 1 / 64 / 128 / 256     4.3 6.3 9.8 17 / 5.0 6.5 6.6 10 / 7.7 8.2 8.2 8.2
-//   1 expert, 5632 outputs, 1 / 16 / 64            4.6 6.1 13 / 4.9 5.7 10 / 7.6 7.8 8.2
-//   1 expert, 5632 outputs, SWIGLU, 1 / 8 / 32     6.7 7.6 11 / 7.1 8.1 10 / 8.2 8.4 8.5
+// The rows kernels where their workgroups are few a CU (us; rows of 16 and of 32
+// against 64 x 128 tiles, 2048 inputs; where the choice lies within 0.5 % of the best
+// in the geometric mean of 170 shapes):
+//   1 expert, 2048 outputs, 1 / 64 / 128 / 256     3.6 5.1 7.4 12 / 4.5 5.4 5.5 7.8 / 7.7 8.3 8.3 8.3
+//   1 expert, 8192 outputs, 1 / 16 / 32 / 64       4.4 5.1 7.4 12 / 4.5 5.0 5.4 7.9 / 7.6 7.8 8.0 8.3
+//   the same, SWIGLU                               5.7 6.5 9.9 17 / 6.3 7.0 7.9 13 / 8.4 8.5 8.6 8.7
 //   64 experts, 1408 outputs, 1 / 8                29 43 / 30 39 / 19 20
 inline MxForm pick_mx_form(const ExpertMatmulArgs& a) {
   const int h = a.swiglu ? 2 : 1, r = a.M / used_experts(a);
   const double nk = (a.k + 255) / 256;
   const double rows = expected_tiles(a, 16, 16);
-  if (rows <= 300 || (r <= 8 && rows <= 512)) return kMxRows16;
-  if (expected_tiles(a, 32, 32 / h) <= 300) return kMxRows32;
+  if (rows <= 300 || (r <= 16 && rows <= 1024)) return kMxRows16;
+  if (expected_tiles(a, 32, 32 / h) <= 640) return kMxRows32;
   struct Rounds {
     double part, whole;
   };

@@ -13,8 +13,8 @@ CASES = [
     ("rows32", False, [64, 65], 776, 4896, False),
     ("rows32", False, [33, 40], 904, 4896, True),
     # rows of less than 16 scales: a tile each
-    ("small", False, [300, 3, 0, 70], 1032, 96, False),
-    ("small", False, [200, 33], 648, 384, True),
+    ("small", False, [300, 3, 0, 70], 2056, 96, False),
+    ("small", False, [200, 33], 1288, 384, True),
     ("small", False, [510, 3], 2056, 1120, False),
     ("small", False, [300, 0, 129], 1032, 736, True),
     ("small", True, [16 + e % 7 for e in range(60)], 1288, 800, False),
