@@ -1036,7 +1036,6 @@ def residual_norm_backward(r_out, dx=None, dr_out=None, y=None, weight=None, pos
         y_code = _type_code(y.dtype)
     elif post or gate is not None:
         raise ValueError("post norm and gate need y")
-    fits = (_host or _load_host()).fits
     # name: type and shape of each result
     res = {"dr": (dt, shape)}
     sums = False
@@ -1054,21 +1053,26 @@ def residual_norm_backward(r_out, dx=None, dr_out=None, y=None, weight=None, pos
         for name, t in out.items():
             if t is not None and name not in res:
                 raise ValueError(f"out has {name!r}, which this call does not give")
+    specs = [r_out, dt, shape, dx, None if dx is None else dx.dtype, shape, dr_out, dt, shape,
+             y, None if y is None else y.dtype, shape, weight, dt, (d,), post_weight, dt, (d,),
+             gate, dt, None if gate is None else gate.shape]
+    names = []  # of the given results, which follow in specs
     for name, (dtype, size) in res.items():
         t = out.get(name) if out else None
         if t is None:
             t = _empty(size, dtype, r_out, stream)
-        elif not fits(dev, t, dtype, size):
-            _tensors(dev, (t, name, dtype, size))
+        else:
+            specs += (t, dtype, size)
+            names.append(name)
         res[name] = t
-    if not fits(dev, r_out, dt, shape, dx, None if dx is None else dx.dtype, shape,
-                dr_out, dt, shape, y, None if y is None else y.dtype, shape, weight, dt, (d,),
-                post_weight, dt, (d,), gate, dt, None if gate is None else gate.shape):
+    if not (_host or _load_host()).fits(dev, *specs):
         _given(dev, (r_out, "r_out", dt, shape),
                (y, "y", None if y is None else y.dtype, shape), (weight, "weight", dt, (d,)),
                (post_weight, "post_weight", dt, (d,)), (dr_out, "dr_out", dt, shape),
                (dx, "dx", None if dx is None else dx.dtype, shape),
-               (gate, "gate", dt, None if gate is None else gate.shape))
+               (gate, "gate", dt, None if gate is None else gate.shape),
+               *((t, name, dtype, size) for t, name, dtype, size in
+                 zip(specs[21::3], names, specs[22::3], specs[23::3])))
     nws = _norm_workspace(code, L, d) if sums else 0
     ws = _workspace(workspace, nws, r_out, stream) if nws else None
     get = res.get

@@ -221,11 +221,13 @@ struct Unit {
 //   dx and y 211 us for 363, 2048 x 8192 float32 102 for 114, but from bfloat16, which
 //   does not spill, 89 for 81).
 enum RowIn { kAhead, kHeld, kTwice };
-template <typename T, typename TY, typename TX, int NT, int EPT, RowIn IN>
+// Y: there is a y, and with it what belongs to it.  A norm alone takes half the registers:
+// 11984 x 632 from bfloat16 17 us where the kernel for both took 27.
+template <typename T, typename TY, typename TX, int NT, int EPT, RowIn IN, bool Y>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_kernel(
     ResidualNormBackwardArgs a, float* sums) {
   constexpr int U = 16 / sizeof(T), NV = EPT / U, ROWS = NT < 256 ? 256 / NT : 1;
-  constexpr int NS = 6;
+  constexpr int NS = Y ? 6 : 2, SUMS = Y ? 3 : 1;
   __shared__ float part[2][NS][16];
   __shared__ __attribute__((aligned(16))) float joined[ROWS > 1 ? ROWS * NT * EPT : 4];
   int t = threadIdx.x % NT;
@@ -242,8 +244,10 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
     v.w.v[0] = v.pw.v[0] = v.g.v[0] = make_uint4(kOne, kOne, kOne, kOne);
     if (column(u) >= d) return;
     if (a.w) v.w.load(static_cast<const T*>(a.w) + column(u));
-    if (a.post_w) v.pw.load(static_cast<const T*>(a.post_w) + column(u));
-    if (a.gate_kind == kGateColumn) v.g.load(gate + column(u));
+    if constexpr (Y) {
+      if (a.post_w) v.pw.load(static_cast<const T*>(a.post_w) + column(u));
+      if (a.gate_kind == kGateColumn) v.g.load(gate + column(u));
+    }
   };
   if constexpr (IN == kAhead) {
 #pragma unroll
@@ -271,20 +275,23 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
       v.r.load(static_cast<const T*>(a.r_out) + base + column(u));
       v.dx.load(static_cast<const TX*>(a.dx) + base + column(u));
     }
-    if (a.y) v.y.load(static_cast<const TY*>(a.y) + base + column(u));
-    if (a.gate_kind == kGateFull) v.g.load(gate + base + column(u));
+    if constexpr (Y) {
+      v.y.load(static_cast<const TY*>(a.y) + base + column(u));
+      if (a.gate_kind == kGateFull) v.g.load(gate + base + column(u));
+    }
   };
   auto fetch_gate = [&](size_t row) {
-    return row < static_cast<size_t>(a.L) && a.gate_kind == kGateToken ? load_one(gate + row) : 1.f;
+    return Y && row < static_cast<size_t>(a.L) && a.gate_kind == kGateToken ? load_one(gate + row)
+                                                                           : 1.f;
   };
   auto fetch = [&](Row& v, size_t row) {
     v.gate = fetch_gate(row);
 #pragma unroll
     for (int u = 0; u < NV; ++u) fetch_unit(v.u[u], row, u);
   };
-  float total[3][NV][U] = {};
+  float total[SUMS][NV][U] = {};
   const size_t step = static_cast<size_t>(gridDim.x) * ROWS;
-  const bool full = a.gate_kind == kGateFull;
+  const bool full = Y && a.gate_kind == kGateFull;
   int turn = 0;
   // the rows of a workgroup's turn: all its threads take part in the same turns
   size_t row = static_cast<size_t>(blockIdx.x) * ROWS + sub;
@@ -325,24 +332,30 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
       (full ? x.g : k.g).floats(g);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const float p = dx[i] * wf[i], q = g[i] * pf[i] * y[i];
+        const float p = dx[i] * wf[i];
         v[0] = fmaf(r[i], r[i], v[0]);
         v[1] = fmaf(p, r[i], v[1]);
-        v[2] = fmaf(y[i], y[i], v[2]);
-        v[3] = fmaf(q, dr[i], v[3]);
-        v[4] = fmaf(q, p, v[4]);
-        v[5] = fmaf(q, r[i], v[5]);
+        if constexpr (Y) {
+          const float q = g[i] * pf[i] * y[i];
+          v[2] = fmaf(y[i], y[i], v[2]);
+          v[3] = fmaf(q, dr[i], v[3]);
+          v[4] = fmaf(q, p, v[4]);
+          v[5] = fmaf(q, r[i], v[5]);
+        }
       }
     }
     row_sums<NT>(v, part[turn]);
     const float s = a.dx ? rsqrtf(fmaf(v[0], over, a.eps)) : 0.f;
     const float c = a.dx ? s * s * s * (v[1] * over) : 0.f;
-    const float b = a.post ? rsqrtf(fmaf(v[2], over, a.eps)) : 1.f;
-    const float qy = v[3] + s * v[4] - c * v[5];  // sum of t dr
-    const float row_gate = a.alpha * now.gate;
-    const float back = a.post ? b * b * b * (row_gate * qy * over) : 0.f;
-    if (live && a.gate_kind == kGateToken && a.dgate && t == 0)
-      static_cast<float*>(a.dgate)[row] = a.alpha * b * qy;
+    float b = 1.f, row_gate = 0.f, back = 0.f;
+    if constexpr (Y) {
+      if (a.post) b = rsqrtf(fmaf(v[2], over, a.eps));
+      const float qy = v[3] + s * v[4] - c * v[5];  // sum of t dr
+      row_gate = a.alpha * now.gate;
+      if (a.post) back = b * b * b * (row_gate * qy * over);
+      if (live && a.gate_kind == kGateToken && a.dgate && t == 0)
+        static_cast<float*>(a.dgate)[row] = a.alpha * b * qy;
+    }
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       float r[U], dx[U], y[U], dr[U], wf[U], pf[U], g[U], dg[U];
@@ -360,28 +373,32 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
       for (int i = 0; i < U; ++i) {
         dr[i] += s * (dx[i] * wf[i]) - c * r[i];
         total[kSumW][u][i] = fmaf(dx[i], r[i] * s, total[kSumW][u][i]);
-        const float dn = row_gate * g[i] * dr[i], yb = y[i] * b;
-        dg[i] = a.alpha * dr[i] * (yb * pf[i]);
-        total[kSumPost][u][i] = fmaf(dn, yb, total[kSumPost][u][i]);
-        total[kSumGate][u][i] += dg[i];
-        y[i] = b * (dn * pf[i]) - back * y[i];
+        if constexpr (Y) {
+          const float dn = row_gate * g[i] * dr[i], yb = y[i] * b;
+          dg[i] = a.alpha * dr[i] * (yb * pf[i]);
+          total[kSumPost][u][i] = fmaf(dn, yb, total[kSumPost][u][i]);
+          total[kSumGate][u][i] += dg[i];
+          y[i] = b * (dn * pf[i]) - back * y[i];
+        }
       }
       if (!live || column(u) >= d) continue;
       store_unit(static_cast<T*>(a.dr) + base + column(u), dr);
-      if (full && a.dgate) store_unit(static_cast<T*>(a.dgate) + base + column(u), dg);
-      if (a.dy) store_unit(static_cast<TY*>(a.dy) + base + column(u), y);
+      if constexpr (Y) {
+        if (full && a.dgate) store_unit(static_cast<T*>(a.dgate) + base + column(u), dg);
+        if (a.dy) store_unit(static_cast<TY*>(a.dy) + base + column(u), y);
+      }
     }
     if constexpr (IN == kAhead) now = then;
     if constexpr (IN == kHeld) fetch(now, row + step);
   }
-  if (!sums) return;
-  const float* wanted[3] = {a.dw, a.dpost_w,
-                            a.gate_kind == kGateColumn ? static_cast<const float*>(a.dgate)
-                                                       : nullptr};
+  float* wanted[3] = {a.dw, a.dpost_w,
+                      a.gate_kind == kGateColumn ? static_cast<float*>(a.dgate) : nullptr};
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
+  for (int k = 0; k < SUMS; ++k) {
     if (!wanted[k]) continue;
-    float* out = sums + (static_cast<size_t>(blockIdx.x) * 3 + k) * d;
+    // one part is the sum
+    float* out = gridDim.x == 1 ? wanted[k]
+                                : sums + (static_cast<size_t>(blockIdx.x) * SUMS + k) * d;
     if constexpr (ROWS > 1) {  // the rows at a time of a workgroup, in order
       __syncthreads();
 #pragma unroll
@@ -402,8 +419,10 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
 }
 
 // The partial sums in part order: 16 columns by 64 runs of the parts a workgroup.
-__global__ __launch_bounds__(256) void norm_sums_kernel(const float* sums, int parts, int d,
-                                                        float* dw, float* dpost, float* dgate) {
+// kinds: sums of a part.
+__global__ __launch_bounds__(256) void norm_sums_kernel(const float* sums, int parts, int kinds,
+                                                        int d, float* dw, float* dpost,
+                                                        float* dgate) {
   __shared__ float4 run[64][4];
   float* out = blockIdx.y == kSumW ? dw : blockIdx.y == kSumPost ? dpost : dgate;
   if (!out) return;
@@ -419,8 +438,8 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(const float* sums, int p
     const int per = (parts + 63) / 64, end = min(parts, (z + 1) * per);
 #pragma unroll 8
     for (int p = z * per; p < end; ++p)
-      add(s, *reinterpret_cast<const float4*>(sums + (static_cast<size_t>(p) * 3 + blockIdx.y) * d +
-                                              c));
+      add(s, *reinterpret_cast<const float4*>(
+                 sums + (static_cast<size_t>(p) * kinds + blockIdx.y) * d + c));
   }
   run[z][l] = s;
   __syncthreads();
@@ -463,49 +482,61 @@ constexpr int kNormParts = 512;
 static int norm_threads(int d) {  // of a row
   return d <= 256 ? 32 : d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 8192 ? 512 : 1024;
 }
-static int norm_parts(int L, int d) {
+// Rows that four turns of one workgroup hold are one part, without a second launch (4
+// rows of 2048: 5.8 us, 10.5 with it).  A norm alone has room for twice the workgroups
+// (8192 x 2048 from bfloat16 29 us, with three times as many 31).
+static int norm_parts(int L, int d, bool y) {
   const int nt = norm_threads(d), rows = nt < 256 ? 256 / nt : 1, n = (L + rows - 1) / rows;
-  const int most = nt <= 256 ? kNormParts : kNormParts * 256 / nt;
-  return n < most ? n : most;
+  const int most = (nt <= 256 ? kNormParts : kNormParts * 256 / nt) * (y ? 1 : 2);
+  return n <= 4 ? (n < 1 ? n : 1) : n < most ? n : most;
 }
+// three sums of a part with a y, one without: those of both
 size_t residual_norm_backward_ws_bytes(int bf16, int L, int d) {
-  return static_cast<size_t>(norm_parts(L, d)) * 3 * d * 4;
+  const int with = norm_parts(L, d, true), without = norm_parts(L, d, false);
+  if (with <= 1) return 0;
+  return static_cast<size_t>(with * 3 > without ? with * 3 : without) * d * 4;
 }
-template <typename T, typename TY, typename TX>
+template <typename T, typename TY, typename TX, bool Y>
 static void run_norm_backward(const ResidualNormBackwardArgs& a, float* sums, hipStream_t s) {
-  const unsigned nb = norm_parts(a.L, a.d);
+  const unsigned nb = norm_parts(a.L, a.d, Y);
   if (a.d <= 256)
-    residual_norm_backward_kernel<T, TY, TX, 32, 8, kAhead><<<nb, 256, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 32, 8, kAhead, Y><<<nb, 256, 0, s>>>(a, sums);
   else if (a.d <= 512)
-    residual_norm_backward_kernel<T, TY, TX, 64, 8, kAhead><<<nb, 256, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 64, 8, kAhead, Y><<<nb, 256, 0, s>>>(a, sums);
   else if (a.d <= 1024)
-    residual_norm_backward_kernel<T, TY, TX, 128, 8, kAhead><<<nb, 256, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 128, 8, kAhead, Y><<<nb, 256, 0, s>>>(a, sums);
   else if (a.d <= 2048)
-    residual_norm_backward_kernel<T, TY, TX, 256, 8, kAhead><<<nb, 256, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 256, 8, kAhead, Y><<<nb, 256, 0, s>>>(a, sums);
   else if (a.d <= 4096)
-    residual_norm_backward_kernel<T, TY, TX, 512, 8, kAhead><<<nb, 512, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 512, 8, kAhead, Y><<<nb, 512, 0, s>>>(a, sums);
   else if (a.d <= 8192)
-    residual_norm_backward_kernel<T, TY, TX, 512, 16, sizeof(T) == 4 ? kTwice : kHeld>
+    residual_norm_backward_kernel<T, TY, TX, 512, 16, sizeof(T) == 4 && Y ? kTwice : kHeld, Y>
         <<<nb, 512, 0, s>>>(a, sums);
   else
-    residual_norm_backward_kernel<T, TY, TX, 1024, 16, kTwice><<<nb, 1024, 0, s>>>(a, sums);
+    residual_norm_backward_kernel<T, TY, TX, 1024, 16, sizeof(T) == 4 || Y ? kTwice : kHeld, Y>
+        <<<nb, 1024, 0, s>>>(a, sums);
 }
 hipError_t launch_residual_norm_backward(const ResidualNormBackwardArgs& a, float* ws,
                                          hipStream_t s) {
   float* dgate = a.gate_kind == kGateColumn ? static_cast<float*>(a.dgate) : nullptr;
   float* sums = a.dw || a.dpost_w || dgate ? ws : nullptr;
   if (a.L > 0) {
-    if (!a.bf16) run_norm_backward<float, float, float>(a, sums, s);
-    else if (a.y_bf16 && a.dx_bf16) run_norm_backward<uint16_t, uint16_t, uint16_t>(a, sums, s);
-    else if (a.y_bf16) run_norm_backward<uint16_t, uint16_t, float>(a, sums, s);
-    else if (a.dx_bf16) run_norm_backward<uint16_t, float, uint16_t>(a, sums, s);
-    else run_norm_backward<uint16_t, float, float>(a, sums, s);
+    if (!a.y) {
+      if (!a.bf16) run_norm_backward<float, float, float, false>(a, sums, s);
+      else if (a.dx_bf16) run_norm_backward<uint16_t, uint16_t, uint16_t, false>(a, sums, s);
+      else run_norm_backward<uint16_t, uint16_t, float, false>(a, sums, s);
+    } else if (!a.bf16) run_norm_backward<float, float, float, true>(a, sums, s);
+    else if (a.y_bf16 && a.dx_bf16) run_norm_backward<uint16_t, uint16_t, uint16_t, true>(a, sums, s);
+    else if (a.y_bf16) run_norm_backward<uint16_t, uint16_t, float, true>(a, sums, s);
+    else if (a.dx_bf16) run_norm_backward<uint16_t, float, uint16_t, true>(a, sums, s);
+    else run_norm_backward<uint16_t, float, float, true>(a, sums, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.dw || a.dpost_w || dgate)
-    norm_sums_kernel<<<dim3((a.d + 15) / 16, 3), 256, 0, s>>>(sums, norm_parts(a.L, a.d), a.d, a.dw,
-                                                              a.dpost_w, dgate);
+  const int parts = norm_parts(a.L, a.d, a.y), kinds = a.y || a.L == 0 ? 3 : 1;
+  if ((a.dw || a.dpost_w || dgate) && parts != 1)
+    norm_sums_kernel<<<dim3((a.d + 15) / 16, kinds), 256, 0, s>>>(sums, parts, kinds, a.d, a.dw,
+                                                                  a.dpost_w, dgate);
   return hipGetLastError();
 }
 

@@ -759,8 +759,8 @@ omni_status omni_residual_norm(omni_dtype dt, omni_dtype y_dt, int L, int d, con
  * and y must be NULL where the forward had none.  dr may be dr_out, dy may be y, and
  * either may be dx if of its type; no other overlap.
  * ws / ws_bytes: at least omni_residual_norm_backward_workspace(...) bytes, 256-byte
- * aligned, or NULL with 0 where none of dw, dpost_w and a column gate's dgate is
- * wanted (their sums over parts of the rows; one workspace serves one call at a
+ * aligned, or NULL with 0 where that is 0 or none of dw, dpost_w and a column gate's
+ * dgate is wanted (their sums over parts of the rows; one workspace serves one call at a
  * time).  Sizes as in the forward.  Deterministic: every sum runs in a fixed order.
  */
 size_t omni_residual_norm_backward_workspace(omni_dtype dt, int L, int d);

@@ -69,8 +69,8 @@ def test_norm_argument_checks():
 def test_norm_backward_argument_checks():
     f, need = B.lib().omni_residual_norm_backward, B.lib().omni_residual_norm_backward_workspace
 
-    def call(dt=1, yt=0, xt=0, L=4, d=64, r=FAKE, y=FAKE, post=0, pw=None, g=None, gk=0, al=1.0,
-             eps=1e-6, w=FAKE, dro=FAKE, dx=FAKE, dr=FAKE, dy=FAKE, dg=None, dw=None, dpw=None,
+    def call(dt=1, yt=0, xt=0, L=200, d=64, r=FAKE, y=FAKE, post=0, pw=None, g=None, gk=0,
+             al=1.0, eps=1e-6, w=FAKE, dro=FAKE, dx=FAKE, dr=FAKE, dy=FAKE, dg=None, dw=None, dpw=None,
              ws=None, n=0):
         return f(dt, yt, xt, L, d, r, y, post, pw, g, gk, al, eps, w, dro, dx, dr, dy, dg, dw,
                  dpw, ws, n, None)
@@ -83,8 +83,9 @@ def test_norm_backward_argument_checks():
                 dict(eps=-1.0), dict(al=INF)):
         assert call(**bad) == INV, bad
     assert call(d=60) == UNS and call(d=16392) == UNS and call(L=1 << 22) == UNS
-    n = need(1, 4, 64)
-    assert n > 0 and need(2, 4, 64) == 0 and need(1, -1, 64) == 0 and need(1, 4, 1 << 20) == 0
+    n = need(1, 200, 64)
+    assert n > 0 and need(2, 200, 64) == 0 and need(1, -1, 64) == 0 and need(1, 200, 1 << 20) == 0
+    assert need(1, 32, 64) == 0 < need(1, 33, 64) and need(0, 4, 16384) == 0 < need(0, 5, 16384)
     for bad in (dict(), dict(ws=FAKE, n=n - 1), dict(ws=MIS, n=n)):
         assert call(dw=FAKE, **bad) == B.OMNI_ERR_WORKSPACE
         assert call(post=1, dpw=FAKE, **bad) == B.OMNI_ERR_WORKSPACE
