@@ -11,6 +11,7 @@
 
 #include <climits>
 #include <cstring>
+#include <exception>
 #include <tuple>
 #include <utility>
 
@@ -54,7 +55,11 @@ struct Argument<T*> {
     if (o == Py_None) {
       v = nullptr;
     } else if (THPVariable_Check(o)) {
-      v = static_cast<T*>(const_cast<void*>(THPVariable_Unpack(o).const_data_ptr()));
+      try {  // a tensor may have no memory
+        v = static_cast<T*>(const_cast<void*>(THPVariable_Unpack(o).const_data_ptr()));
+      } catch (const std::exception& e) {
+        return argument_error(e.what());
+      }
     } else {
       v = static_cast<T*>(PyLong_AsVoidPtr(o));
       if (!v && PyErr_Occurred()) return argument_error("a pointer is a tensor, an int or None");
@@ -104,6 +109,25 @@ PyObject* entry(PyObject*, PyObject* args) {
   return PyErr_Format(PyExc_KeyError, "%s", name);
 }
 
+// 1 or 0, or -1 with a Python error
+int one_fits(const at::Tensor& t, PyObject* dtype, PyObject* shape, long dev) {
+  try {  // tensors that are not strided have no sizes or memory to ask for
+    if (t.layout() != at::kStrided || t.is_nested()) return 0;
+    const auto sizes = t.sizes();
+    if (t.scalar_type() != reinterpret_cast<THPDtype*>(dtype)->scalar_type || !t.is_cuda() ||
+        t.get_device() != dev || static_cast<Py_ssize_t>(sizes.size()) != PyTuple_GET_SIZE(shape) ||
+        !t.is_contiguous())
+      return 0;
+    for (size_t j = 0; j < sizes.size(); ++j) {
+      const long long want = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, j));
+      if (want == -1 && PyErr_Occurred()) return -1;
+      if (sizes[j] != want) return 0;
+    }
+    return 1;
+  } catch (const std::exception&) {
+    return 0;
+  }
+}
 PyObject* fits(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n % 3 != 1) return PyErr_Format(PyExc_TypeError, "a device, then tensor, dtype, shape each");
   const long dev = PyLong_AsLong(args[0]);
@@ -112,17 +136,9 @@ PyObject* fits(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyObject *o = args[i], *dtype = args[i + 1], *shape = args[i + 2];
     if (o == Py_None) continue;
     if (!THPVariable_Check(o) || !THPDtype_Check(dtype) || !PyTuple_Check(shape)) Py_RETURN_FALSE;
-    const at::Tensor& t = THPVariable_Unpack(o);
-    const auto sizes = t.sizes();
-    if (t.scalar_type() != reinterpret_cast<THPDtype*>(dtype)->scalar_type || !t.is_cuda() ||
-        t.get_device() != dev || static_cast<Py_ssize_t>(sizes.size()) != PyTuple_GET_SIZE(shape) ||
-        !t.is_contiguous())
-      Py_RETURN_FALSE;
-    for (size_t j = 0; j < sizes.size(); ++j) {
-      const long long want = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, j));
-      if (want == -1 && PyErr_Occurred()) return nullptr;
-      if (sizes[j] != want) Py_RETURN_FALSE;
-    }
+    const int fit = one_fits(THPVariable_Unpack(o), dtype, shape, dev);
+    if (fit < 0) return nullptr;
+    if (fit == 0) Py_RETURN_FALSE;
   }
   Py_RETURN_TRUE;
 }

@@ -58,3 +58,18 @@ def test_entries_are_the_librarys():
     address = ctypes.cast(B.lib().omni_expert_route, ctypes.c_void_p).value
     again = H.entry("omni_expert_route", address)
     assert again.__self__ == address == B._entries["omni_expert_route"].__self__
+
+
+def test_tensors_without_memory_of_their_own():
+    """Refused or told apart, without a C++ exception out of the module."""
+    odd = [torch.eye(4).to_sparse(), torch.eye(4).to_sparse_csr(),
+           torch.nested.nested_tensor([torch.zeros(2), torch.zeros(3)]),
+           torch.zeros(4, 4, device="meta")]
+    for t in odd:
+        assert not H.fits(0, t, F32, (4, 4))
+    for t in odd[:2]:
+        with pytest.raises(TypeError):
+            B._entries["omni_microscale_rows"](1, 0, 64, t, None, None, None)
+    for t in odd[:2]:
+        with pytest.raises((ValueError, TypeError, RuntimeError)):
+            B.microscale_rows(t)
