@@ -1,6 +1,6 @@
 """The residual norms and their gradients against the float64 oracle.
 
-Tolerances.  A sum of squares of d <= 16384 columns over at least 64 lanes runs at
+Tolerances.  A sum of squares of d <= 16384 columns over 64 lanes or more (32 up to 256) runs at
 most 32 + 6 + 16 additions deep for its partial sums (each 2^-24 of a positive
 sum), its root halves that, the root itself adds 2^-22, and each product 2^-24:
 c = 40 x 2^-23 of every term of r_out.  x also carries r_out's error, directly and
