@@ -356,36 +356,40 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
       if (live && a.gate_kind == kGateToken && a.dgate && t == 0)
         static_cast<float*>(a.dgate)[row] = a.alpha * b * qy;
     }
+    // a place beyond the last row has no part in the sums either: the root of its mean of
+    // zeros may be infinite
+    if (ROWS == 1 || live) {
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      float r[U], dx[U], y[U], dr[U], wf[U], pf[U], g[U], dg[U];
-      RowUnit x;
-      Column k;
-      unit(u, x, k);
-      x.r.floats(r);
-      x.dx.floats(dx);
-      x.y.floats(y);
-      x.dr.floats(dr);
-      k.w.floats(wf);
-      k.pw.floats(pf);
-      (full ? x.g : k.g).floats(g);
+      for (int u = 0; u < NV; ++u) {
+        float r[U], dx[U], y[U], dr[U], wf[U], pf[U], g[U], dg[U];
+        RowUnit x;
+        Column k;
+        unit(u, x, k);
+        x.r.floats(r);
+        x.dx.floats(dx);
+        x.y.floats(y);
+        x.dr.floats(dr);
+        k.w.floats(wf);
+        k.pw.floats(pf);
+        (full ? x.g : k.g).floats(g);
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        dr[i] += s * (dx[i] * wf[i]) - c * r[i];
-        total[kSumW][u][i] = fmaf(dx[i], r[i] * s, total[kSumW][u][i]);
-        if constexpr (Y) {
-          const float dn = row_gate * g[i] * dr[i], yb = y[i] * b;
-          dg[i] = a.alpha * dr[i] * (yb * pf[i]);
-          total[kSumPost][u][i] = fmaf(dn, yb, total[kSumPost][u][i]);
-          total[kSumGate][u][i] += dg[i];
-          y[i] = b * (dn * pf[i]) - back * y[i];
+        for (int i = 0; i < U; ++i) {
+          dr[i] += s * (dx[i] * wf[i]) - c * r[i];
+          total[kSumW][u][i] = fmaf(dx[i], r[i] * s, total[kSumW][u][i]);
+          if constexpr (Y) {
+            const float dn = row_gate * g[i] * dr[i], yb = y[i] * b;
+            dg[i] = a.alpha * dr[i] * (yb * pf[i]);
+            total[kSumPost][u][i] = fmaf(dn, yb, total[kSumPost][u][i]);
+            total[kSumGate][u][i] += dg[i];
+            y[i] = b * (dn * pf[i]) - back * y[i];
+          }
         }
-      }
-      if (!live || column(u) >= d) continue;
-      store_unit(static_cast<T*>(a.dr) + base + column(u), dr);
-      if constexpr (Y) {
-        if (full && a.dgate) store_unit(static_cast<T*>(a.dgate) + base + column(u), dg);
-        if (a.dy) store_unit(static_cast<TY*>(a.dy) + base + column(u), y);
+        if (column(u) >= d) continue;
+        store_unit(static_cast<T*>(a.dr) + base + column(u), dr);
+        if constexpr (Y) {
+          if (full && a.dgate) store_unit(static_cast<T*>(a.dgate) + base + column(u), dg);
+          if (a.dy) store_unit(static_cast<TY*>(a.dy) + base + column(u), y);
+        }
       }
     }
     if constexpr (IN == kAhead) now = then;

@@ -300,3 +300,23 @@ def test_norm_captured_and_workspaces():
     assert torch.equal(r2, r1) and torch.equal(x2, x)
     for n in out:
         assert torch.equal(out[n], o2[n])
+
+
+# a width of each kernel that holds a row its own way
+CLASSES = {"bf16": [64, 256, 512, 1000, 2048, 4096, 8192, 16384],
+           "f32": [64, 256, 508, 1024, 2048, 4096, 8192, 16384]}
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-30])
+@pytest.mark.parametrize("L", [1, 5, 33])
+@pytest.mark.parametrize("dt,d", [(t, d) for t in CLASSES for d in CLASSES[t]])
+def test_norm_backward_sums_with_little_eps(dt, d, L, eps):
+    """Places that a workgroup has beyond the last row add nothing to the sums over the
+    rows: there the mean of the squares is eps alone, its root 0 or next to it."""
+    rng = np.random.default_rng(d + L)
+    for yt, post, gate in ((None, "none", None), ("f32", "weight", "column")):
+        a = make(rng, L, d, dt, yt, post, gate)
+        dx, dr = arr(rng, (L, d), "f32"), arr(rng, (L, d), dt)
+        t = {k: dev(v) for k, v in a.items()}
+        got = B.residual_norm_backward(t.pop("r"), dx=dev(dx), dr_out=dev(dr), **t, eps=eps)
+        backward_close(a, dt, "f32", post != "none", 1.0, eps, dx, dr, got)
