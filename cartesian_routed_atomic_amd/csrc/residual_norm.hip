@@ -346,13 +346,15 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
     }
     row_sums<NT>(v, part[turn]);
     const float s = a.dx ? rsqrtf(fmaf(v[0], over, a.eps)) : 0.f;
-    const float c = a.dx ? s * s * s * (v[1] * over) : 0.f;
+    // a mean of squares is taken out factor by factor: its root's cube leaves float32's
+    // range long before the gradients do
+    const float c = a.dx ? v[1] * over * s : 0.f;  // mean(p r1 a)
     float b = 1.f, row_gate = 0.f, back = 0.f;
     if constexpr (Y) {
       if (a.post) b = rsqrtf(fmaf(v[2], over, a.eps));
-      const float qy = v[3] + s * v[4] - c * v[5];  // sum of t dr
+      const float qy = v[3] + s * (v[4] - c * (s * v[5]));  // sum of t dr
       row_gate = a.alpha * now.gate;
-      if (a.post) back = b * b * b * (row_gate * qy * over);
+      if (a.post) back = row_gate * qy * over * b;  // mean(q y b)
       if (live && a.gate_kind == kGateToken && a.dgate && t == 0)
         static_cast<float*>(a.dgate)[row] = a.alpha * b * qy;
     }
@@ -374,14 +376,15 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
         (full ? x.g : k.g).floats(g);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          dr[i] += s * (dx[i] * wf[i]) - c * r[i];
-          total[kSumW][u][i] = fmaf(dx[i], r[i] * s, total[kSumW][u][i]);
+          const float ra = r[i] * s;
+          dr[i] += s * (dx[i] * wf[i] - c * ra);
+          total[kSumW][u][i] = fmaf(dx[i], ra, total[kSumW][u][i]);
           if constexpr (Y) {
             const float dn = row_gate * g[i] * dr[i], yb = y[i] * b;
             dg[i] = a.alpha * dr[i] * (yb * pf[i]);
             total[kSumPost][u][i] = fmaf(dn, yb, total[kSumPost][u][i]);
             total[kSumGate][u][i] += dg[i];
-            y[i] = b * (dn * pf[i]) - back * y[i];
+            y[i] = b * (dn * pf[i] - back * yb);
           }
         }
         if (column(u) >= d) continue;

@@ -320,3 +320,35 @@ def test_norm_backward_sums_with_little_eps(dt, d, L, eps):
         t = {k: dev(v) for k, v in a.items()}
         got = B.residual_norm_backward(t.pop("r"), dx=dev(dx), dr_out=dev(dr), **t, eps=eps)
         backward_close(a, dt, "f32", post != "none", 1.0, eps, dx, dr, got)
+
+
+@pytest.mark.parametrize("power", [50, -50])
+@pytest.mark.parametrize("dt,d", [(t, d) for t in CLASSES for d in CLASSES[t]])
+def test_norm_backward_of_large_and_small_rows(dt, d, power):
+    """Rows of 2^50 and 2^-50, whose inverse root's cube is no float32, without eps; dr_out
+    of the size of dx over them, so that every term counts."""
+    rng = np.random.default_rng(d)
+    L = 5
+    for yt, post, gate in ((None, "none", None), ("f32", "weight", "column"), (dt, "ones", "token")):
+        a = make(rng, L, d, dt, yt, post, gate)
+        a["r"] = arr(rng, (L, d), dt, 2.0 ** power)
+        if yt:
+            a["y"] = arr(rng, (L, d), yt, 2.0 ** power)
+        dx, dr = arr(rng, (L, d), "f32"), arr(rng, (L, d), dt, 2.0 ** -power)
+        t = {k: dev(v) for k, v in a.items()}
+        got = B.residual_norm_backward(t.pop("r"), dx=dev(dx), dr_out=dev(dr), **t,
+                                       post=post != "none", eps=0.0)
+        backward_close(a, dt, "f32", post != "none", 1.0, 0.0, dx, dr, got)
+
+
+@pytest.mark.parametrize("dt,d", [(t, d) for t in CLASSES for d in CLASSES[t]])
+def test_norm_backward_of_zero_rows_with_little_eps(dt, d):
+    """A row of zeros among others: its gradient is dx w / sqrt(eps), and so on to dy."""
+    rng = np.random.default_rng(d)
+    L, eps = 5, 1e-30
+    a = make(rng, L, d, dt, "f32", "weight", "column")
+    a["r"][2], a["y"][2], a["y"][4] = 0, 0, 0
+    dx, dr = arr(rng, (L, d), "f32"), arr(rng, (L, d), dt)
+    t = {k: dev(v) for k, v in a.items()}
+    got = B.residual_norm_backward(t.pop("r"), dx=dev(dx), dr_out=dev(dr), **t, eps=eps)
+    backward_close(a, dt, "f32", True, 1.0, eps, dx, dr, got)
