@@ -352,7 +352,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
     float b = 1.f, row_gate = 0.f, back = 0.f;
     if constexpr (Y) {
       if (a.post) b = rsqrtf(fmaf(v[2], over, a.eps));
-      const float qy = v[3] + s * (v[4] - c * (s * v[5]));  // sum of t dr
+      // sum of t dr; without dx its other terms would be 0 times a y that may be infinite
+      const float qy = a.dx ? v[3] + s * (v[4] - c * (s * v[5])) : v[3];
       row_gate = a.alpha * now.gate;
       if (a.post) back = row_gate * qy * over * b;  // mean(q y b)
       if (live && a.gate_kind == kGateToken && a.dgate && t == 0)
@@ -384,7 +385,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
             dg[i] = a.alpha * dr[i] * (yb * pf[i]);
             total[kSumPost][u][i] = fmaf(dn, yb, total[kSumPost][u][i]);
             total[kSumGate][u][i] += dg[i];
-            y[i] = b * (dn * pf[i] - back * yb);
+            // without a post norm y has no part in dy, infinite or not
+            y[i] = a.post ? b * (dn * pf[i] - back * yb) : dn;
           }
         }
         if (column(u) >= d) continue;

@@ -751,6 +751,9 @@ omni_status omni_residual_norm(omni_dtype dt, omni_dtype y_dt, int L, int d, con
  *   post: dpost_w = sum over rows of dn y b;  q = dn post_w,
  *         dy = b q - y b^3 mean(q y);  else dy = dn
  *
+ * Without post dy does not depend on y, which may then hold NaN and infinities; where
+ * there is a dx, dgate [L] of such a row may be NaN where the formula is infinite.
+ *
  * r_out, dr_out, dr [L, d] of dt; dx [L, d] of dx_dt (dt or OMNI_F32); y, dy of y_dt;
  * post_w, w, gate as in the forward; dw, dpost_w [d] float32; dgate float32 [d] or
  * [L], for OMNI_GATE_FULL [L, d] of dt.  Everything overwritten.  dx NULL: x was not

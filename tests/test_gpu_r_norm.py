@@ -352,3 +352,39 @@ def test_norm_backward_of_zero_rows_with_little_eps(dt, d):
     t = {k: dev(v) for k, v in a.items()}
     got = B.residual_norm_backward(t.pop("r"), dx=dev(dx), dr_out=dev(dr), **t, eps=eps)
     backward_close(a, dt, "f32", True, 1.0, eps, dx, dr, got)
+
+
+@pytest.mark.parametrize("gate", [None, "column", "token", "full"])
+@pytest.mark.parametrize("dt,d", [(t, d) for t in CLASSES for d in CLASSES[t]])
+def test_norm_backward_of_y_not_finite_without_post_norm(dt, d, gate):
+    """Without a post norm dy is alpha g dr, whatever y holds; from dr_out alone the
+    gate's gradient is that of the formula too."""
+    rng = np.random.default_rng(d)
+    L = 6
+    a = make(rng, L, d, dt, "f32", "none", gate)
+    a["y"][1, 3], a["y"][2, 0], a["y"][4, d - 1], a["y"][4, 1] = np.inf, np.nan, -np.inf, -np.inf
+    dx, dr = arr(rng, (L, d), "f32"), arr(rng, (L, d), dt)
+    t = {k: dev(v) for k, v in a.items()}
+    r, w = t.pop("r"), t.pop("weight")
+    for given, weight in (((None, dr), None), ((dx, dr), w)):
+        got = B.residual_norm_backward(r, dx=dev(given[0]), dr_out=dev(given[1]), **t,
+                                       weight=weight, alpha=0.5)
+        wide = got.pop("dgate", None)
+        with np.errstate(invalid="ignore"):
+            backward_close(a, dt, "f32", False, 0.5, 1e-6, *given, got)
+        if gate is None:
+            continue
+        with np.errstate(invalid="ignore"):
+            want, mass = OB.residual_norm_backward(
+                a["r"], *given, a["y"], a["weight"] if weight is not None else None, None, False,
+                a["gate"], 0.5, 1e-6)["dgate"]
+        wide = host(wide)
+        half = 2.0 ** -8 if wide.dtype == np.uint16 else 2.0 ** -24
+        wide = bf16_bits_to_f32(wide) if wide.dtype == np.uint16 else wide
+        finite = np.isfinite(want)
+        assert not finite.all() and finite.any() and (np.isfinite(wide) == finite).all()
+        if given[0] is None or gate != "token":
+            np.testing.assert_array_equal(wide[~finite], want[~finite])
+        # as backward_close
+        tol = (132 + L) * 2.0 ** -23 * mass[finite] + half * 1.001 * np.abs(want[finite]) + 1e-36
+        assert (np.abs(wide[finite] - want[finite]) <= tol).all()
