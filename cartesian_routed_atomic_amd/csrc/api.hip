@@ -618,8 +618,9 @@ static omni_status route_args(omni_dtype dt, int L, int E, int K, omni_score_fn 
   if (fn != OMNI_SCORE_SOFTMAX && fn != OMNI_SCORE_SIGMOID) return OMNI_ERR_INVALID_ARG;
   if (L < 0 || E < 1 || K < 1 || !fits_i32(static_cast<long long>(L) * K) || !isfinite(scale))
     return OMNI_ERR_INVALID_ARG;
-  // a wave holds a token's logits and one selected expert per lane
-  return K > 64 || E > 1024 || L >= 1 << 26 ? OMNI_ERR_UNSUPPORTED : OMNI_OK;
+  // a wave holds a token's logits and one selected expert per lane; with a wave for each
+  // token, four to a workgroup, a launch stays below 2^32 work-items
+  return K > 64 || E > 1024 || L > (1 << 26) - 4 ? OMNI_ERR_UNSUPPORTED : OMNI_OK;
 }
 
 omni_status omni_expert_route(omni_dtype dt, int L, int E, int K, const void* logits,

@@ -679,7 +679,7 @@ omni_status omni_microscaled_expert_matmul(omni_dtype out_dt, int M, int E, int 
  * Requires 1 <= K <= top_groups * (E / groups), 1 <= top_groups <= groups, E a
  * multiple of groups, group_best 1 or 2, scale finite; top_groups == groups
  * leaves every expert.  K > 64, E > 1024 or groups > 64 is UNSUPPORTED, as is
- * L >= 2^26; L * K < 2^31.  Deterministic.
+ * L > 2^26 - 4; L * K < 2^31.  Deterministic.
  */
 typedef enum omni_score_fn {
   OMNI_SCORE_SOFTMAX = 0,

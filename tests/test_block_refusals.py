@@ -186,3 +186,16 @@ def test_python_calls_refuse_mismatched_arguments():
         B.microscaled_matmul(q, s, q.to(torch.int8), s)
     with pytest.raises(ValueError, match="even"):
         B.microscaled_matmul(q, s, q[:3].contiguous(), s[:3].contiguous(), swiglu=True)
+
+
+@pytest.mark.parametrize("more", [1, 2, 3])
+def test_route_of_more_tokens_than_a_launch_holds(more):
+    """Four tokens a workgroup of 256: from 2^26 - 3 on they are 2^24 workgroups, 2^32
+    work-items, one more than a launch takes."""
+    L = (1 << 26) - 4 + more
+    assert (L + 3) // 4 * 256 == 1 << 32 and (L - more + 3) // 4 * 256 < 1 << 32
+    for E, K in ((16, 2), (128, 17), (520, 1), (1024, 1)):
+        assert B.lib().omni_expert_route(1, L, E, K, FAKE, None, 0, 1, 1, 1, 1, 1.0, FAKE, FAKE,
+                                         None, None) == UNS
+        assert B.lib().omni_expert_route_backward(1, L, E, K, FAKE, FAKE, FAKE, 0, 1, 1.0, None, 0,
+                                                  FAKE, None) == UNS

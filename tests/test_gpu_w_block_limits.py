@@ -152,3 +152,20 @@ def test_calls_on_two_streams_at_once():
         for a, b in zip(want, got):
             for p, q in zip(a, b):
                 assert torch.equal(p, q)
+
+
+def test_route_of_the_most_tokens():
+    """2^26 - 4 of them, four to a workgroup: 2^32 - 256 work-items."""
+    rng = np.random.default_rng(6)
+    L, E, K, n = (1 << 26) - 4, 17, 17, 6
+    ends = rand(rng, (n, E), BF, 2.0)
+    z = far(L, E, BF, ends)
+    idx, gate, _ = B.expert_route(z, K, scores="sigmoid")
+    alone = B.expert_route(ends, K, scores="sigmoid")
+    assert torch.equal(idx[-n:], alone[0]) and torch.equal(gate[-n:], alone[1])
+    # equal logits: the experts in order, an equal share each
+    assert (idx[:-n] == torch.arange(K, device="cuda", dtype=torch.int32)).all()
+    assert (gate[:-n] == gate[0, 0]).all() and abs(float(gate[0, 0]) - 1 / K) < 1e-6
+    dz = B.expert_route_backward(z, idx, gate, scores="sigmoid", renormalize=False)
+    want = B.expert_route_backward(ends, alone[0], alone[1], scores="sigmoid", renormalize=False)
+    assert torch.equal(dz[-n:], want) and (dz[:-n] == dz[0, 0]).all() and (want != 0).all()
