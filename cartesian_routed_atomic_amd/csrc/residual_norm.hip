@@ -218,8 +218,8 @@ struct Unit {
 // kHeld: the row (longer ones);
 // kTwice: nothing, it is read again for the results, from the L2 or the chip's last
 //   cache (longer still, where holding spills: 1024 x 16384 from bfloat16 with float32
-//   dx and y 211 us for 363, 2048 x 8192 float32 102 for 114, but from bfloat16, which
-//   does not spill, 89 for 81).
+//   dx and y 217 us for 403, 2048 x 8192 float32 118 for 121, but from bfloat16, which
+//   does not spill, 85 for 80; without a y 1024 x 16384 float32 71 for 57).
 enum RowIn { kAhead, kHeld, kTwice };
 // Y: there is a y, and with it what belongs to it.  A norm alone takes half the registers:
 // 11984 x 632 from bfloat16 17 us where the kernel for both took 27.
@@ -352,8 +352,11 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void residual_norm_backward_ke
     float b = 1.f, row_gate = 0.f, back = 0.f;
     if constexpr (Y) {
       if (a.post) b = rsqrtf(fmaf(v[2], over, a.eps));
-      // sum of t dr; without dx its other terms would be 0 times a y that may be infinite
-      const float qy = a.dx ? v[3] + s * (v[4] - c * (s * v[5])) : v[3];
+      // sum of t dr.  Without dx its other terms would be 0 times a y that may be infinite;
+      // of finite numbers whose squares pass float32's range, so that a or b is 0, the
+      // products may as well, and the row passes nothing
+      float qy = a.dx && (s != 0.f || c != 0.f) ? v[3] + s * (v[4] - c * (s * v[5])) : v[3];
+      if (b == 0.f && fabsf(v[3]) < INFINITY) qy = 0.f;
       row_gate = a.alpha * now.gate;
       if (a.post) back = row_gate * qy * over * b;  // mean(q y b)
       if (live && a.gate_kind == kGateToken && a.dgate && t == 0)

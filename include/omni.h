@@ -721,6 +721,8 @@ omni_status omni_expert_route_backward(omni_dtype dt, int L, int E, int K, const
  *   x = r_out / sqrt(mean r_out^2 + eps) * w      (before r_out is rounded)
  *
  * row by row, means over the d columns, all in float32; each output rounded once.
+ * Numbers whose squares sum past float32's range have an infinite mean: a norm of 0,
+ * which passes no gradient (as long as sums of products with them stay in that range).
  * Without y (NULL; then post = 0, no gate, r_out NULL) it is the norm alone: x =
  * r / sqrt(mean r^2 + eps) * w.  x may be NULL (then w too) where only the
  * residual is wanted.

@@ -388,3 +388,57 @@ def test_norm_backward_of_y_not_finite_without_post_norm(dt, d, gate):
         # as backward_close
         tol = (132 + L) * 2.0 ** -23 * mass[finite] + half * 1.001 * np.abs(want[finite]) + 1e-36
         assert (np.abs(wide[finite] - want[finite]) <= tol).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 2048, 16384])
+def test_norm_of_rows_whose_squares_pass_float32(dt, d):
+    """An infinite mean of squares: the norm is 0, with its gradients; the others' stay."""
+    rng = np.random.default_rng(d)
+    a = make(rng, 3, d, dt, "f32", "weight", None)
+    a["r"][1], a["y"][1] = (f32_to_bf16_bits(np.float32(1e25)) if dt == "bf16" else 1e25), -1e25
+    t = {k: dev(v) for k, v in a.items()}
+    r1, x = B.residual_norm(**t)
+    assert torch.equal(r1[1], t["r"][1]) and (x[1] == 0).all() and (x[[0, 2]] != 0).any(dim=1).all()
+    dx = dev(arr(rng, (3, d), "f32"))
+    g = B.residual_norm_backward(r1, dx=dx, **{k: v for k, v in t.items() if k != "r"})
+    rest = B.residual_norm_backward(r1[[0, 2]], dx=dx[[0, 2]], y=t["y"][[0, 2]],
+                                    weight=t["weight"], post_weight=t["post_weight"])
+    for name in ("dr", "dy"):
+        assert (g[name][1] == 0).all() and torch.equal(g[name][[0, 2]], rest[name])
+    for name in ("dweight", "dpost_weight"):
+        assert torch.isfinite(g[name]).all()
+
+
+@pytest.mark.parametrize("gate", [None, "token"])
+@pytest.mark.parametrize("r,y", [(1e25, 1.0), (1.0, 1e25), (1e14, 1e25), (1e25, 1e14)])
+def test_norm_gradients_of_one_norm_past_float32(r, y, gate):
+    """Against the oracle with the lost norm's root as 0: the product of y and r passes
+    float32's range in the last two."""
+    rng = np.random.default_rng(3)
+    L, d = 5, 136
+    a = make(rng, L, d, "f32", "f32", "weight", gate)
+    a["r"][2] *= np.float32(r)
+    a["y"][2] *= np.float32(y)
+    dx, dr = arr(rng, (L, d), "f32"), arr(rng, (L, d), "f32")
+    t = {k: dev(v) for k, v in a.items()}
+    got = {k: host(v) for k, v in
+           B.residual_norm_backward(t.pop("r"), dx=dev(dx), dr_out=dev(dr), **t).items()}
+    b = dict(a)
+    if r == 1e25:  # x of that row is 0: dr is dr_out, and so dx may be taken as 0
+        dx[2] = 0
+    kw = {k: b.get(k) for k in ("y", "post_weight", "gate")}
+    want = OB.residual_norm_backward(b["r"], dx, dr, kw["y"], b["weight"], kw["post_weight"], True,
+                                     kw["gate"], 1.0, 1e-6)
+    for name, g in got.items():
+        w, mass = (v.copy() for v in want[name])
+        if y == 1e25 and name in ("dy", "dgate"):
+            w[2], mass[2] = 0, 0
+        if y == 1e25 and name == "dpost_weight":  # without that row's term
+            rows = [0, 1, 3, 4]
+            part = {k: v[rows] if v is not None and v.shape[0] == L else v for k, v in kw.items()}
+            w, mass = OB.residual_norm_backward(b["r"][rows], dx[rows], dr[rows], part["y"],
+                                                b["weight"], part["post_weight"], True,
+                                                part["gate"], 1.0, 1e-6)[name]
+        steps = 100 + (L + 32 if name in ("dweight", "dpost_weight") else 0)
+        close(g, w, steps * 2.0 ** -23 * mass + 2.0 ** -24 * 1.001 * np.abs(w) + 1e-36, name)
